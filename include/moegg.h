@@ -69,9 +69,17 @@ typedef enum {
 #define MOEGG_DERR_EXPERT_ID 1 /* a top-k expert id outside [0, E): slot dropped  */
 #define MOEGG_DERR_M_SIZES 2   /* m_sizes negative or summing past S: clipped     */
 #define MOEGG_DERR_GATHER 4    /* a gather index outside [0, S): row skipped      */
+#define MOEGG_DERR_LOGIT 8     /* a gate logit or bias NaN or +inf: expert masked */
 
 #define MOEGG_MAX_EXPERTS 1024
 #define MOEGG_MAX_GROUPS 16
+#define MOEGG_MAX_TOPK 64       /* moegg_gate: picks a token                       */
+#define MOEGG_MAX_GATE_GROUPS 64
+
+/* Element types of the entry points that take a dtype. */
+#define MOEGG_BF16 0
+#define MOEGG_FP16 1
+#define MOEGG_FP32 2
 
 /* Human-readable name of a status code (static string). */
 const char *moegg_status_string(moegg_status status);
@@ -389,6 +397,145 @@ moegg_status moegg_combine_bwd(const void *dOut, const void *Y, const int32_t *s
                                const float *topk_weights, int64_t num_tokens, int32_t topk,
                                int32_t N, int64_t y_rows, void *dY, float *dw,
                                int32_t *error_flags, void *stream);
+
+/* Gate flags. */
+#define MOEGG_GATE_SIGMOID 1u /* scores are sigmoids of the logits, not their softmax   */
+#define MOEGG_GATE_RENORM 2u  /* weights are divided by the sum of the picked scores    */
+
+/*
+ * moegg_gate -- from router logits to each token's top-k expert ids and
+ * weights: the step in front of moegg_route, whose topk_ids these ids are
+ * (and the topk_weights of the GEMMs and combines, slot order).
+ *
+ *   score_i = softmax(logits[t])_i, or 1 / (1 + e^-l_i) with GATE_SIGMOID
+ *   key_i   = score_i + bias_i (bias 0 when NULL); the topk largest keys are
+ *             picked, in falling order, equal keys by rising expert index
+ *   w_j     = scale * score_{id_j}; with GATE_RENORM divided by the sum of
+ *             the picked scores
+ *   n_groups > 1: experts form n_groups groups of E / n_groups neighbours; a
+ *             group's value is the sum of its two largest keys (its only key
+ *             when one expert is left), and experts are picked inside the
+ *             topk_groups groups of largest value (equal values by rising
+ *             group index).
+ *
+ * A logit of -inf masks its expert: score 0, never picked.  So does a bias
+ * that is not finite, for the pick alone.  A logit that is NaN or +inf is
+ * taken as -inf and raises MOEGG_DERR_LOGIT, as does a bias that is NaN or
+ * +inf.  A token with fewer than topk experts left (none, for a padding row
+ * of -inf) gets id -1 and weight 0 in the places left over; moegg_route
+ * drops those slots (and raises MOEGG_DERR_EXPERT_ID for them).  Scores,
+ * weights and sums are fp32; keys with a bias or groups are compared in 64
+ * bits, the others by the logits themselves, which give the same order.
+ *
+ *   logits       [T, E] of `dtype`, rows ld_logits >= E elements apart.
+ *   bias         [E] fp32 device, or NULL.
+ *   topk_ids     out [T, topk] int32.    topk_weights  out [T, topk] fp32.
+ *   scores       out [T, E] fp32, or NULL (a load-balancing loss reads them).
+ * T = 0 is a no-op.  Errors: ESHAPE for sizes outside 1 <= E <=
+ * MOEGG_MAX_EXPERTS, 1 <= topk <= min(E, MOEGG_MAX_TOPK), 1 <= topk_groups <=
+ * n_groups <= MOEGG_MAX_GATE_GROUPS, n_groups dividing E, topk <=
+ * topk_groups * E / n_groups, ld_logits >= E; EINVAL for an unknown dtype or
+ * flag, a scale that is not finite, NULL or misaligned pointers.
+ */
+moegg_status moegg_gate(const void *logits, int32_t dtype, int64_t ld_logits, const float *bias,
+                        int64_t num_tokens, int32_t num_experts, int32_t topk, int32_t n_groups,
+                        int32_t topk_groups, float scale, uint32_t flags, int32_t *topk_ids,
+                        float *topk_weights, float *scores, int32_t *error_flags, void *stream);
+
+/*
+ * moegg_gate_bwd -- gradient of moegg_gate's weights and scores with respect
+ * to the logits, for the ids it picked (the pick itself has no gradient):
+ *
+ *   dlogits = (d weights / d logits)^T dweights + (d scores / d logits)^T dscores
+ *
+ *   topk_ids     [T, topk] int32 as moegg_gate wrote them; a negative id has
+ *                no gradient, an id >= E none either (MOEGG_DERR_EXPERT_ID).
+ *   dweights     [T, topk] fp32.   dscores  [T, E] fp32, or NULL for zero.
+ *   dlogits      out [T, E] of `dtype`, contiguous; masked experts get 0.
+ * scale and flags as in the forward; the scores are computed again from the
+ * logits.  Sums in fp32, one rounding to `dtype`.  Errors as moegg_gate.
+ */
+moegg_status moegg_gate_bwd(const void *logits, int32_t dtype, int64_t ld_logits,
+                            const int32_t *topk_ids, const float *dweights, const float *dscores,
+                            int64_t num_tokens, int32_t num_experts, int32_t topk, float scale,
+                            uint32_t flags, void *dlogits, int32_t *error_flags, void *stream);
+
+/*
+ * moegg_permute -- token rows into expert order, each of a token's topk
+ * copies times its weight: Xs[row(s)] = w[s] * X[t] for slot s = t * topk + j.
+ *
+ *   X              [T, K] of `dtype`, row-major.
+ *   scatter_idx    [T*topk] int32, moegg_route's scatter_idx (its entries are
+ *                  distinct); negative entries are dropped slots.
+ *   topk_weights   [T*topk] fp32 slot order, or NULL for weight 1.
+ *   offsets, padded_offsets   moegg_route's, [E+1] int32 each.  Both NULL:
+ *                  row(s) = scatter_idx[s].  Both given: the block-padded
+ *                  layout, row(s) = scatter_idx[s] - offsets[e] +
+ *                  padded_offsets[e] for the slot's expert e, and the pad
+ *                  rows between an expert's last row and the next expert's
+ *                  first are set to zero.
+ *   rows           rows of Xs.  T * topk always suffices without padding,
+ *                  T * topk + E * (block_m - 1) with it.
+ *   Xs             out [rows, K] of `dtype`.  Rows that no slot maps to and
+ *                  that are no pad rows are left as they were.
+ *   row_map        out [T*topk] int32: row(s), -1 for a dropped slot.  What
+ *                  the other three entry points (and moegg_combine, as its
+ *                  scatter_idx) take.  Required in the padded layout,
+ *                  optional without (it then repeats scatter_idx).
+ * A row at or past `rows` raises MOEGG_DERR_GATHER and is skipped.  Products
+ * in fp32, rounded once.  T = 0 writes the pad rows alone.
+ * Errors: ESHAPE for T < 0, topk < 1, K < 1, rows < 0, sizes past 2^40 bytes,
+ * E outside [1, MOEGG_MAX_EXPERTS] in the padded layout; EINVAL for an unknown
+ * dtype, one of offsets / padded_offsets without the other, NULL or
+ * misaligned pointers (rows need the alignment of one element only).
+ */
+moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_idx,
+                           const float *topk_weights, const int32_t *offsets,
+                           const int32_t *padded_offsets, int64_t num_tokens, int32_t topk,
+                           int32_t num_experts, int32_t K, int64_t rows, void *Xs,
+                           int32_t *row_map, int32_t *error_flags, void *stream);
+
+/*
+ * moegg_permute_bwd -- gradient of moegg_permute:
+ *   dX[t] = sum_{j<topk} w[s] * dXs[row_map[s]]   (fp32, j ascending, rounded once)
+ *   dw[s] = sum_n X[t, n] * dXs[row_map[s], n]    (fp32), when dw is not NULL
+ * X is read only for dw (and may be NULL without it).  A dropped slot adds
+ * nothing and gets dw = 0.  Arguments and errors as moegg_permute.
+ */
+moegg_status moegg_permute_bwd(const void *dXs, int32_t dtype, const void *X,
+                               const int32_t *row_map, const float *topk_weights,
+                               int64_t num_tokens, int32_t topk, int32_t K, int64_t rows, void *dX,
+                               float *dw, int32_t *error_flags, void *stream);
+
+/*
+ * moegg_unpermute -- expert-ordered rows back to token order, weighted and
+ * summed onto a base (a residual, a shared expert's output):
+ *   out[t] = base[t] + sum_{j<topk} w[s] * Y[row_map[s]]
+ * in fp32, base first, j ascending, rounded once.  The counterpart of
+ * moegg_permute in its three types and its padded layout; moegg_combine is
+ * the bf16 form that can write fp32.
+ *   Y     [rows, K] of `dtype`.   base  [T, K] of `dtype` or NULL; may be out.
+ * Arguments and errors otherwise as moegg_permute.
+ */
+moegg_status moegg_unpermute(const void *Y, int32_t dtype, const int32_t *row_map,
+                             const float *topk_weights, const void *base, int64_t num_tokens,
+                             int32_t topk, int32_t K, int64_t rows, void *out,
+                             int32_t *error_flags, void *stream);
+
+/*
+ * moegg_unpermute_bwd -- gradient of moegg_unpermute (base's is dOut itself):
+ *   dY[row_map[s]] = w[s] * dOut[t]                (rounded once)
+ *   dw[s] = sum_n dOut[t, n] * Y[row_map[s], n]    (fp32), when dw is not NULL
+ * With offsets and padded_offsets the pad rows of dY are set to zero, so that
+ * products over the padded rows read no stale values; other rows no slot maps
+ * to are left as they were.  Y is read only for dw.
+ */
+moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
+                                 const int32_t *row_map, const float *topk_weights,
+                                 const int32_t *offsets, const int32_t *padded_offsets,
+                                 int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t K,
+                                 int64_t rows, void *dY, float *dw, int32_t *error_flags,
+                                 void *stream);
 
 #ifdef __cplusplus
 }

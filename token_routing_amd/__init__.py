@@ -26,9 +26,16 @@ GATED_SILU = 32
 DERR_EXPERT_ID = 1
 DERR_M_SIZES = 2
 DERR_GATHER = 4
+DERR_LOGIT = 8
 
 MAX_EXPERTS = 1024
 MAX_GROUPS = 16
+MAX_TOPK = 64
+
+GATE_SIGMOID = 1
+GATE_RENORM = 2
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoegg.so")
@@ -92,6 +99,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moegg_combine.restype = ctypes.c_int
     lib.moegg_combine_bwd.argtypes = [vp, vp, vp, vp, i64, i32, i32, i64, vp, vp, vp, vp]
     lib.moegg_combine_bwd.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.moegg_gate.argtypes = [vp, i32, i64, vp, i64, i32, i32, i32, i32, f32, u32, vp, vp, vp, vp,
+                               vp]
+    lib.moegg_gate.restype = ctypes.c_int
+    lib.moegg_gate_bwd.argtypes = [vp, i32, i64, vp, vp, vp, i64, i32, i32, f32, u32, vp, vp, vp]
+    lib.moegg_gate_bwd.restype = ctypes.c_int
+    lib.moegg_permute.argtypes = [vp, i32, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp, vp, vp, vp]
+    lib.moegg_permute.restype = ctypes.c_int
+    lib.moegg_permute_bwd.argtypes = [vp, i32, vp, vp, vp, i64, i32, i32, i64, vp, vp, vp, vp]
+    lib.moegg_permute_bwd.restype = ctypes.c_int
+    lib.moegg_unpermute.argtypes = [vp, i32, vp, vp, vp, i64, i32, i32, i64, vp, vp, vp]
+    lib.moegg_unpermute.restype = ctypes.c_int
+    lib.moegg_unpermute_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp,
+                                        vp, vp, vp]
+    lib.moegg_unpermute_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -373,3 +395,270 @@ def combine_bwd(dOut, Y, topk: int, scatter_idx=None, topk_weights=None, *, want
                                  topk, N, rows, _ptr(dY), _ptr(dw if want_dw else None),
                                  _ptr(error_flags), _stream(stream)), "moegg_combine_bwd")
     return dY, (dw if want_dw else None)
+
+
+# The entry points below check shapes and devices as well, run on the device
+# that holds their tensors, and allocate outputs (and workspaces) on the stream
+# that they launch on.
+
+def _run(device, stream, call):
+    """call(stream handle) with `device` current and, when given, `stream` current."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {device}")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _dtype_code(t, name):
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return code
+
+
+def _arg(t, name, dtype, shape, device):
+    """Address of a contiguous CUDA tensor of this type, shape (None: any size) and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
+    if len(shape) != t.dim() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_arg(t, name, dtype, shape, device):
+    """Address and row stride of a CUDA matrix whose rows are contiguous."""
+    if t.dtype != dtype or t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
+    if t.dim() != 2 or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if (cols > 1 and rows and t.stride(1) != 1) or (rows and ld < cols):
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), max(ld, cols)
+
+
+def _flag_arg(t, device):
+    return None if t is None else _arg(t, "error_flags", torch.int32, (1,), device)
+
+
+def _flat(t):
+    if t is not None and not t.is_contiguous():
+        raise ValueError("per-slot arrays must be contiguous")
+    return None if t is None else t.view(-1)
+
+
+def moe_gate(logits, topk: int, *, bias=None, n_groups: int = 1, topk_groups: int = 1,
+             scale: float = 1.0, sigmoid: bool = False, renorm: bool = False,
+             want_scores: bool = False, ids=None, weights=None, scores=None, error_flags=None,
+             stream=None):
+    """Top-k expert ids and weights from router logits (moegg_gate).
+
+    logits: [T, E] bf16, fp16 or fp32, rows contiguous (any row stride); bias:
+    fp32 [E] added for the pick alone.  sigmoid / renorm / scale and the groups
+    as in the header.  Returns (ids int32 [T, topk], weights fp32 [T, topk],
+    scores fp32 [T, E] or None).  ids feeds moe_route, weights (flattened) the
+    GEMMs and combines; places without an expert hold id -1 and weight 0.
+    """
+    lib = load_library()
+    dev = logits.device
+    T, E = logits.shape
+    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), dev)
+    code = _dtype_code(logits, "logits")
+    topk = int(topk)
+
+    def call(stream_ptr):
+        i = torch.empty(T, topk, dtype=torch.int32, device=dev) if ids is None else ids
+        w = torch.empty(T, topk, dtype=torch.float32, device=dev) if weights is None else weights
+        s = scores
+        if s is None and want_scores:
+            s = torch.empty(T, E, dtype=torch.float32, device=dev)
+        _check(lib.moegg_gate(
+            ptr, code, ld, _arg(bias, "bias", torch.float32, (E,), dev), T, E, topk, int(n_groups),
+            int(topk_groups), float(scale),
+            (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
+            _arg(i, "ids", torch.int32, (T, topk), dev),
+            _arg(w, "weights", torch.float32, (T, topk), dev),
+            _arg(s, "scores", torch.float32, (T, E), dev), _flag_arg(error_flags, dev),
+            stream_ptr), "moegg_gate")
+        return i, w, s
+
+    if topk < 1 or topk > E:
+        raise ValueError(f"topk must be between 1 and {E}")
+    return _run(dev, stream, call)
+
+
+def moe_gate_bwd(logits, ids, dweights, *, dscores=None, scale: float = 1.0,
+                 sigmoid: bool = False, renorm: bool = False, dlogits=None, error_flags=None,
+                 stream=None):
+    """Gradient of moe_gate's weights (and scores, with dscores) in the logits
+    (moegg_gate_bwd), for the ids it picked.  Returns dlogits [T, E] of the
+    logits' type."""
+    lib = load_library()
+    dev = logits.device
+    T, E = logits.shape
+    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), dev)
+    code = _dtype_code(logits, "logits")
+    topk = ids.shape[-1]
+
+    def call(stream_ptr):
+        d = torch.empty(T, E, dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+        _check(lib.moegg_gate_bwd(
+            ptr, code, ld, _arg(ids, "ids", torch.int32, (T, topk), dev),
+            _arg(dweights, "dweights", torch.float32, (T, topk), dev),
+            _arg(dscores, "dscores", torch.float32, (T, E), dev), T, E, topk, float(scale),
+            (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
+            _arg(d, "dlogits", logits.dtype, (T, E), dev), _flag_arg(error_flags, dev),
+            stream_ptr), "moegg_gate_bwd")
+        return d
+
+    return _run(dev, stream, call)
+
+
+def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padded_offsets=None,
+            block_m=None, rows=None, Xs=None, row_map=None, error_flags=None, stream=None):
+    """Token rows into expert order (moegg_permute): Xs[row(s)] = w[s] * X[t].
+
+    X: [T, K] bf16, fp16 or fp32; scatter_idx int32 [T*topk] (moe_route);
+    topk_weights fp32 [T*topk] or None.  With offsets and padded_offsets
+    (moe_route) the block-padded layout, pad rows cleared; a new Xs then needs
+    `rows` or the block_m that was routed with.  Returns (Xs [rows, K],
+    row_map int32 [T*topk]); rows past the last expert's are left as they were
+    (a new Xs leaves them uninitialised).
+    """
+    lib = load_library()
+    dev = X.device
+    T, K = X.shape
+    S = T * topk
+    code = _dtype_code(X, "X")
+    E = 0 if offsets is None else offsets.numel() - 1
+    if Xs is not None:
+        rows = Xs.shape[0]
+    elif rows is None:
+        if padded_offsets is not None and block_m is None:
+            raise ValueError("the padded layout needs rows, block_m or Xs")
+        rows = S + (E * (int(block_m) - 1) if padded_offsets is not None else 0)
+
+    def call(stream_ptr):
+        out = torch.empty(rows, K, dtype=X.dtype, device=dev) if Xs is None else Xs
+        m = torch.empty(S, dtype=torch.int32, device=dev) if row_map is None else row_map
+        _check(lib.moegg_permute(
+            _arg(X, "X", X.dtype, (T, K), dev), code,
+            _arg(_flat(scatter_idx), "scatter_idx", torch.int32, (S,), dev),
+            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), dev), T, topk, E, K,
+            rows, _arg(out, "Xs", X.dtype, (rows, K), dev),
+            _arg(m, "row_map", torch.int32, (S,), dev), _flag_arg(error_flags, dev), stream_ptr),
+            "moegg_permute")
+        return out, m
+
+    return _run(dev, stream, call)
+
+
+def permute_bwd(dXs, X, topk: int, row_map, topk_weights=None, *, want_dw: bool = True, dX=None,
+                dw=None, error_flags=None, stream=None):
+    """Gradient of permute (moegg_permute_bwd): (dX [T, K], dw fp32 [T*topk] or None).
+    X (the forward's input) is read only for dw."""
+    lib = load_library()
+    dev = dXs.device
+    rows, K = dXs.shape
+    S = row_map.numel()
+    T = S // topk
+    code = _dtype_code(dXs, "dXs")
+
+    def call(stream_ptr):
+        out = torch.empty(T, K, dtype=dXs.dtype, device=dev) if dX is None else dX
+        g = dw
+        if want_dw and g is None:
+            g = torch.empty(S, dtype=torch.float32, device=dev)
+        _check(lib.moegg_permute_bwd(
+            _arg(dXs, "dXs", dXs.dtype, (rows, K), dev), code,
+            _arg(X, "X", dXs.dtype, (T, K), dev),
+            _arg(_flat(row_map), "row_map", torch.int32, (T * topk,), dev),
+            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev), T, topk, K, rows,
+            _arg(out, "dX", dXs.dtype, (T, K), dev),
+            _arg(_flat(g) if want_dw else None, "dw", torch.float32, (S,), dev),
+            _flag_arg(error_flags, dev), stream_ptr), "moegg_permute_bwd")
+        return out, (g if want_dw else None)
+
+    return _run(dev, stream, call)
+
+
+def unpermute(Y, topk: int, row_map, topk_weights=None, *, base=None, out=None, error_flags=None,
+              stream=None):
+    """Expert-ordered rows back to token order (moegg_unpermute):
+    out[t] = base[t] + sum_j w[s] * Y[row_map[s]].  base may be out."""
+    lib = load_library()
+    dev = Y.device
+    rows, K = Y.shape
+    S = row_map.numel()
+    T = S // topk
+    code = _dtype_code(Y, "Y")
+
+    def call(stream_ptr):
+        o = torch.empty(T, K, dtype=Y.dtype, device=dev) if out is None else out
+        _check(lib.moegg_unpermute(
+            _arg(Y, "Y", Y.dtype, (rows, K), dev), code,
+            _arg(_flat(row_map), "row_map", torch.int32, (T * topk,), dev),
+            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
+            _arg(base, "base", Y.dtype, (T, K), dev), T, topk, K, rows,
+            _arg(o, "out", Y.dtype, (T, K), dev), _flag_arg(error_flags, dev), stream_ptr),
+            "moegg_unpermute")
+        return o
+
+    return _run(dev, stream, call)
+
+
+def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=None,
+                  padded_offsets=None, rows=None, want_dw: bool = True, dY=None, dw=None,
+                  error_flags=None, stream=None):
+    """Gradient of unpermute (moegg_unpermute_bwd): (dY [rows, K], dw fp32 [T*topk] or None).
+
+    Y (the forward's input) is read only for dw and may be None without it
+    (`rows` or dY then say how many rows dY has).  With offsets and
+    padded_offsets the pad rows of dY are cleared; rows no slot maps to are
+    left as they were.
+    """
+    lib = load_library()
+    dev = dOut.device
+    T, K = dOut.shape
+    S = T * topk
+    code = _dtype_code(dOut, "dOut")
+    E = 0 if offsets is None else offsets.numel() - 1
+    if dY is not None:
+        rows = dY.shape[0]
+    elif Y is not None:
+        rows = Y.shape[0]
+    elif rows is None:
+        raise ValueError("without Y and dY, rows is needed")
+
+    def call(stream_ptr):
+        out = torch.empty(rows, K, dtype=dOut.dtype, device=dev) if dY is None else dY
+        g = dw
+        if want_dw and g is None:
+            g = torch.empty(S, dtype=torch.float32, device=dev)
+        _check(lib.moegg_unpermute_bwd(
+            _arg(dOut, "dOut", dOut.dtype, (T, K), dev), code,
+            _arg(Y, "Y", dOut.dtype, (rows, K), dev),
+            _arg(_flat(row_map), "row_map", torch.int32, (S,), dev),
+            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
+            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), dev), T, topk, E, K,
+            rows, _arg(out, "dY", dOut.dtype, (rows, K), dev),
+            _arg(_flat(g) if want_dw else None, "dw", torch.float32, (S,), dev),
+            _flag_arg(error_flags, dev), stream_ptr), "moegg_unpermute_bwd")
+        return out, (g if want_dw else None)
+
+    return _run(dev, stream, call)

@@ -32,7 +32,8 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"),
 ]
 
-SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "api.hip"]
+SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "gate.hip", "sort.hip",
+           "api.hip"]
 
 
 def _compile(src: str, report: bool, defines=(), build_dir=BUILD) -> str:

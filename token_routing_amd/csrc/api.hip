@@ -11,6 +11,7 @@
 #include "../../include/moegg.h"
 
 #include "gemm_params.h"
+#include "layer_params.h"
 
 namespace {
 
@@ -47,6 +48,15 @@ bool aligned2(const void *p)
 bool aligned4(const void *p)
 {
     return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+bool known_dtype(int32_t dtype)
+{
+    return dtype == MOEGG_BF16 || dtype == MOEGG_FP16 || dtype == MOEGG_FP32;
+}
+bool aligned_elem(const void *p, int32_t dtype)
+{
+    return dtype == MOEGG_FP32 ? aligned4(p) : aligned2(p);
 }
 
 // The tiled kernels move rows as 16-byte chunks: row lengths that are
@@ -488,6 +498,244 @@ moegg_status moegg_combine_bwd(const void *dOut, const void *Y, const int32_t *s
     p.N = N;
     return from_hip(tiled ? moegg::combine_bwd_launch(p, static_cast<hipStream_t>(stream))
                           : moegg::combine_bwd_any_launch(p, static_cast<hipStream_t>(stream)));
+}
+
+// Shared checks of the gate entry points.
+static moegg_status check_gate(const void *logits, int32_t dtype, int64_t ld, int64_t num_tokens,
+                               int32_t E, int32_t topk, float scale, uint32_t flags)
+{
+    if (num_tokens < 0 || E < 1 || E > MOEGG_MAX_EXPERTS || topk < 1 || topk > E ||
+        topk > MOEGG_MAX_TOPK || ld < E)
+        return MOEGG_ESHAPE;
+    if (num_tokens > INT32_MAX / topk || ld > ((int64_t)1 << 40) / (num_tokens + 1) / 4)
+        return MOEGG_ESHAPE;
+    if (!known_dtype(dtype) || (flags & ~(uint32_t)(MOEGG_GATE_SIGMOID | MOEGG_GATE_RENORM)) ||
+        !(scale - scale == 0.0f))
+        return MOEGG_EINVAL;
+    if (num_tokens > 0 && (!logits || !aligned_elem(logits, dtype)))
+        return MOEGG_EINVAL;
+    return MOEGG_OK;
+}
+
+moegg_status moegg_gate(const void *logits, int32_t dtype, int64_t ld_logits, const float *bias,
+                        int64_t num_tokens, int32_t num_experts, int32_t topk, int32_t n_groups,
+                        int32_t topk_groups, float scale, uint32_t flags, int32_t *topk_ids,
+                        float *topk_weights, float *scores, int32_t *error_flags, void *stream)
+{
+    moegg_status st =
+        check_gate(logits, dtype, ld_logits, num_tokens, num_experts, topk, scale, flags);
+    if (st != MOEGG_OK)
+        return st;
+    if (n_groups < 1 || n_groups > MOEGG_MAX_GATE_GROUPS || num_experts % n_groups != 0 ||
+        topk_groups < 1 || topk_groups > n_groups || topk > topk_groups * (num_experts / n_groups))
+        return MOEGG_ESHAPE;
+    if (num_tokens == 0)
+        return MOEGG_OK;
+    if (!topk_ids || !topk_weights || !aligned4(topk_ids) || !aligned4(topk_weights) ||
+        !aligned4(scores) || !aligned4(bias))
+        return MOEGG_EINVAL;
+    moegg::GateParams p;
+    p.logits = logits;
+    p.bias = bias;
+    p.ids = topk_ids;
+    p.weights = topk_weights;
+    p.scores = scores;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.ld = ld_logits;
+    p.E = num_experts;
+    p.topk = topk;
+    p.n_groups = n_groups;
+    p.topk_groups = topk_groups;
+    p.dtype = dtype;
+    p.scale = scale;
+    p.sigmoid = flags & MOEGG_GATE_SIGMOID;
+    p.renorm = flags & MOEGG_GATE_RENORM;
+    return from_hip(moegg::gate_launch(p, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_gate_bwd(const void *logits, int32_t dtype, int64_t ld_logits,
+                            const int32_t *topk_ids, const float *dweights, const float *dscores,
+                            int64_t num_tokens, int32_t num_experts, int32_t topk, float scale,
+                            uint32_t flags, void *dlogits, int32_t *error_flags, void *stream)
+{
+    moegg_status st =
+        check_gate(logits, dtype, ld_logits, num_tokens, num_experts, topk, scale, flags);
+    if (st != MOEGG_OK)
+        return st;
+    if (num_tokens == 0)
+        return MOEGG_OK;
+    if (!topk_ids || !dweights || !dlogits || !aligned4(topk_ids) || !aligned4(dweights) ||
+        !aligned4(dscores) || !aligned_elem(dlogits, dtype))
+        return MOEGG_EINVAL;
+    moegg::GateBwdParams p;
+    p.logits = logits;
+    p.ids = topk_ids;
+    p.dweights = dweights;
+    p.dscores = dscores;
+    p.dlogits = dlogits;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.ld = ld_logits;
+    p.E = num_experts;
+    p.topk = topk;
+    p.dtype = dtype;
+    p.scale = scale;
+    p.sigmoid = flags & MOEGG_GATE_SIGMOID;
+    p.renorm = flags & MOEGG_GATE_RENORM;
+    return from_hip(moegg::gate_bwd_launch(p, static_cast<hipStream_t>(stream)));
+}
+
+// Shared checks of the permute and unpermute entry points: tok holds [T, K]
+// rows, sorted the [rows, K] ones.
+static moegg_status check_sort(const void *tok, const void *sorted, int32_t dtype,
+                               const int32_t *map, const float *weights, int64_t num_tokens,
+                               int32_t topk, int32_t K, int64_t rows)
+{
+    constexpr int64_t kMax = (int64_t)1 << 38;  // elements: 2^40 bytes of fp32
+    if (num_tokens < 0 || topk < 1 || K < 1 || K > (1 << 30) || rows < 0 || rows > INT32_MAX)
+        return MOEGG_ESHAPE;
+    if (num_tokens > INT32_MAX / topk || num_tokens > kMax / K || rows > kMax / K)
+        return MOEGG_ESHAPE;
+    if (!known_dtype(dtype))
+        return MOEGG_EINVAL;
+    if (num_tokens > 0 && (!tok || !map || !aligned_elem(tok, dtype) || !aligned4(map) ||
+                           !aligned4(weights)))
+        return MOEGG_EINVAL;
+    if (rows > 0 && num_tokens > 0 && (!sorted || !aligned_elem(sorted, dtype)))
+        return MOEGG_EINVAL;
+    return MOEGG_OK;
+}
+
+// The padded layout's metadata: both offset arrays or neither.
+static moegg_status check_padded(const int32_t *offsets, const int32_t *padded, int32_t E,
+                                 const void *sorted, int32_t dtype, int64_t rows)
+{
+    if (!offsets != !padded)
+        return MOEGG_EINVAL;
+    if (!padded)
+        return MOEGG_OK;
+    if (E < 1 || E > MOEGG_MAX_EXPERTS)
+        return MOEGG_ESHAPE;
+    if (!aligned4(offsets) || !aligned4(padded))
+        return MOEGG_EINVAL;
+    if (rows > 0 && (!sorted || !aligned_elem(sorted, dtype)))
+        return MOEGG_EINVAL;
+    return MOEGG_OK;
+}
+
+moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_idx,
+                           const float *topk_weights, const int32_t *offsets,
+                           const int32_t *padded_offsets, int64_t num_tokens, int32_t topk,
+                           int32_t num_experts, int32_t K, int64_t rows, void *Xs,
+                           int32_t *row_map, int32_t *error_flags, void *stream)
+{
+    moegg_status st =
+        check_sort(X, Xs, dtype, scatter_idx, topk_weights, num_tokens, topk, K, rows);
+    if (st == MOEGG_OK)
+        st = check_padded(offsets, padded_offsets, num_experts, Xs, dtype, rows);
+    if (st != MOEGG_OK)
+        return st;
+    if (num_tokens > 0 && ((padded_offsets && !row_map) || !aligned4(row_map)))
+        return MOEGG_EINVAL;
+    moegg::SpreadParams p = {};
+    p.src = X;
+    p.map = scatter_idx;
+    p.weights = topk_weights;
+    p.offsets = offsets;
+    p.padded = padded_offsets;
+    p.dst = Xs;
+    p.row_map = row_map;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.rows = rows;
+    p.topk = topk;
+    p.E = num_experts;
+    p.K = K;
+    return from_hip(moegg::spread_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_permute_bwd(const void *dXs, int32_t dtype, const void *X,
+                               const int32_t *row_map, const float *topk_weights,
+                               int64_t num_tokens, int32_t topk, int32_t K, int64_t rows, void *dX,
+                               float *dw, int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_sort(dX, dXs, dtype, row_map, topk_weights, num_tokens, topk, K, rows);
+    if (st != MOEGG_OK || num_tokens == 0)
+        return st;
+    if (dw && (!X || !aligned_elem(X, dtype) || !aligned4(dw)))
+        return MOEGG_EINVAL;
+    moegg::CollectParams p = {};
+    p.rows_in = dXs;
+    p.other = dw ? X : nullptr;
+    p.map = row_map;
+    p.weights = topk_weights;
+    p.out = dX;
+    p.dw = dw;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.rows = rows;
+    p.topk = topk;
+    p.K = K;
+    return from_hip(moegg::collect_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_unpermute(const void *Y, int32_t dtype, const int32_t *row_map,
+                             const float *topk_weights, const void *base, int64_t num_tokens,
+                             int32_t topk, int32_t K, int64_t rows, void *out,
+                             int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_sort(out, Y, dtype, row_map, topk_weights, num_tokens, topk, K, rows);
+    if (st != MOEGG_OK || num_tokens == 0)
+        return st;
+    if (base && !aligned_elem(base, dtype))
+        return MOEGG_EINVAL;
+    moegg::CollectParams p = {};
+    p.rows_in = Y;
+    p.base = base;
+    p.map = row_map;
+    p.weights = topk_weights;
+    p.out = out;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.rows = rows;
+    p.topk = topk;
+    p.K = K;
+    return from_hip(moegg::collect_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
+                                 const int32_t *row_map, const float *topk_weights,
+                                 const int32_t *offsets, const int32_t *padded_offsets,
+                                 int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t K,
+                                 int64_t rows, void *dY, float *dw, int32_t *error_flags,
+                                 void *stream)
+{
+    moegg_status st =
+        check_sort(dOut, dY, dtype, row_map, topk_weights, num_tokens, topk, K, rows);
+    if (st == MOEGG_OK)
+        st = check_padded(offsets, padded_offsets, num_experts, dY, dtype, rows);
+    if (st != MOEGG_OK)
+        return st;
+    if (num_tokens > 0 && dw && ((rows > 0 && !Y) || !aligned_elem(Y, dtype) || !aligned4(dw)))
+        return MOEGG_EINVAL;
+    moegg::SpreadParams p = {};
+    p.src = dOut;
+    p.other = dw ? Y : nullptr;
+    p.map = row_map;
+    p.weights = topk_weights;
+    p.offsets = offsets;
+    p.padded = padded_offsets;
+    p.map_is_padded = true;
+    p.dst = dY;
+    p.dw = dw;
+    p.err = error_flags;
+    p.T = num_tokens;
+    p.rows = rows;
+    p.topk = topk;
+    p.E = num_experts;
+    p.K = K;
+    return from_hip(moegg::spread_launch(p, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
