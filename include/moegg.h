@@ -70,11 +70,13 @@ typedef enum {
 #define MOEGG_DERR_M_SIZES 2   /* m_sizes negative or summing past S: clipped     */
 #define MOEGG_DERR_GATHER 4    /* a gather index outside [0, S): row skipped      */
 #define MOEGG_DERR_LOGIT 8     /* a gate logit or bias NaN or +inf: expert masked */
+#define MOEGG_DERR_RANK 16     /* an adapter's rank outside [0, R]: clipped       */
 
 #define MOEGG_MAX_EXPERTS 1024
 #define MOEGG_MAX_GROUPS 16
 #define MOEGG_MAX_TOPK 64       /* moegg_gate: picks a token                       */
 #define MOEGG_MAX_GATE_GROUPS 64
+#define MOEGG_MAX_LORA_RANK 256
 
 /* Element types of the entry points that take a dtype. */
 #define MOEGG_BF16 0
@@ -536,6 +538,90 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
                                  int64_t num_tokens, int32_t topk, int32_t num_experts, int32_t K,
                                  int64_t rows, void *dY, float *dw, int32_t *error_flags,
                                  void *stream);
+
+/* Adapter flag: write dA and dB in fp32 instead of `dtype`. */
+#define MOEGG_LORA_FP32_GRAD 1u
+
+/*
+ * moegg_lora_fwd -- low-rank adapters of many requests at once, added to a
+ * shared projection's output: for sorted position p of adapter a and row
+ * i = gather_idx[p],
+ *   h[p, r] = sum_k X[i, k] * A[a, r, k]                      r < ranks[a]
+ *   Y[i, n] = base[i, n] + scales[a] * sum_r h[p, r] * B[a, n, r]
+ * The rows are grouped by moegg_route over one adapter id a row (topk 1), once
+ * for all projections of a batch.  With m_sizes and rows in expert order
+ * (gather_idx NULL) the same call adapts the experts' products, L = E.
+ *
+ *   X          rows of K elements of `dtype` (MOEGG_BF16 or MOEGG_FP16), ldx
+ *              elements apart.
+ *   A, B       [L, R, K] and [L, N, R] of `dtype`, contiguous.
+ *   m_sizes    [L] int32 rows of each adapter (0 allowed).
+ *   gather_idx [T] int32: row at sorted position p; entries are distinct.
+ *              NULL: i = p.  An entry outside [0, T) raises
+ *              MOEGG_DERR_GATHER and is skipped.
+ *   ranks      [L] int32 in [0, R], or NULL for R everywhere.  Rows of A and
+ *              columns of B at or past an adapter's rank are not read into the
+ *              result; rank 0 is no adapter (Y = base).
+ *   scales     [L] fp32, or NULL for 1.
+ *   base, Y    rows of N elements, ld_base and ldy apart.  base NULL: Y holds
+ *              the projection's output and is added to in place (base = Y
+ *              says the same).  They overlap in no other way.
+ *   H          out [T, R] fp32: h by sorted position, columns at or past the
+ *              rank zero, for the backward; or NULL.
+ *   workspace  device, 16-byte aligned, moegg_lora_workspace_bytes(...) bytes,
+ *              no initialisation.
+ * Rows at no sorted position below the sum of m_sizes (moegg_route's dropped
+ * ids) keep what Y holds: with a separate base give rows without an adapter
+ * one of rank 0.  h is kept in fp32 and enters the second product with 16
+ * (bf16) or 22 (fp16) bits of mantissa; sums in fp32; Y is rounded once.
+ * Bit-for-bit deterministic.  Any K, N and strides; rows need the alignment of
+ * one element.  T = 0 is a no-op.
+ * Errors: ESHAPE for T < 0, L outside [1, MOEGG_MAX_EXPERTS], R outside
+ * [1, MOEGG_MAX_LORA_RANK], K or N < 1, a row stride below its row, sizes past
+ * 2^40 bytes; EUNSUPPORTED for MOEGG_FP32; EINVAL for an unknown dtype, NULL
+ * or misaligned pointers, base = Y with different strides; EWORKSPACE.
+ */
+moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const void *B,
+                            const int32_t *m_sizes, const int32_t *gather_idx,
+                            const int32_t *ranks, const float *scales, int32_t dtype,
+                            int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
+                            int32_t N, const void *base, int64_t ld_base, void *Y, int64_t ldy,
+                            float *H, void *workspace, size_t workspace_bytes,
+                            int32_t *error_flags, void *stream);
+
+/* Workspace of moegg_lora_fwd; 0 for sizes it refuses. */
+size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
+                                  int32_t N);
+
+/*
+ * moegg_lora_bwd -- gradients of moegg_lora_fwd:
+ *   dh[p, r]    = scales[a] * sum_n dY[i, n] * B[a, n, r]     r < ranks[a]
+ *   dX[i, k]    = base[i, k] + sum_r dh[p, r] * A[a, r, k]
+ *   dA[a, r, k] = sum_{p of a} dh[p, r] * X[i, k]
+ *   dB[a, n, r] = scales[a] * sum_{p of a} dY[i, n] * H[p, r]
+ *   H          the forward's H.
+ *   base, dX   as base and Y in the forward (base: the shared projection's
+ *              input gradient); dX NULL skips it.
+ *   dA, dB     out [L, R, K] and [L, N, R] of `dtype`, fp32 with
+ *              MOEGG_LORA_FP32_GRAD; every element is written, zeros for
+ *              adapters without rows and past an adapter's rank.  Both NULL
+ *              skips them (X and H are then not read and may be NULL).
+ *   workspace  moegg_lora_bwd_workspace_bytes(...) bytes.
+ * Arguments, precision, determinism and errors otherwise as in the forward;
+ * EINVAL for one of dA and dB without the other.  T = 0 writes zeros to dA
+ * and dB.
+ */
+moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t lddy,
+                            const void *A, const void *B, const float *H, const int32_t *m_sizes,
+                            const int32_t *gather_idx, const int32_t *ranks, const float *scales,
+                            int32_t dtype, int64_t num_rows, int32_t num_adapters, int32_t R,
+                            int32_t K, int32_t N, const void *base, int64_t ld_base, void *dX,
+                            int64_t lddx, void *dA, void *dB, uint32_t flags, void *workspace,
+                            size_t workspace_bytes, int32_t *error_flags, void *stream);
+
+/* Workspace of moegg_lora_bwd; 0 for sizes it refuses. */
+size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R,
+                                      int32_t K, int32_t N);
 
 #ifdef __cplusplus
 }

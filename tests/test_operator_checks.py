@@ -1,4 +1,4 @@
-"""Refusals of the gate, permute and unpermute entry points: every call here
+"""Refusals of the gate, permute, unpermute and adapter entry points: every call here
 fails on the host, before anything is enqueued."""
 
 import ctypes
@@ -119,3 +119,72 @@ def test_python_argument_checks():
         mg._dtype_code(torch.zeros(2, dtype=torch.float64), "x")
     with pytest.raises(ValueError):
         mg._flat(torch.zeros(4, 4).t())
+
+
+def lora(lib, X=P, ldx=64, A=P, B=P, m=P, gather=P, ranks=None, scales=None, dtype=BF16, T=10, L=4,
+         R=16, K=64, N=96, base=P, ldb=96, Y=P, ldy=96, H=None, ws=P, size=1 << 20):
+    return lib.moegg_lora_fwd(X, ldx, A, B, m, gather, ranks, scales, dtype, T, L, R, K, N, base,
+                              ldb, Y, ldy, H, ws, size, None, None)
+
+
+EUNSUP, EWS = 3, 4
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), ESHAPE), (dict(T=1 << 31), ESHAPE), (dict(L=0), ESHAPE), (dict(L=1025), ESHAPE),
+    (dict(R=0), ESHAPE), (dict(R=257), ESHAPE), (dict(K=0), ESHAPE), (dict(N=0), ESHAPE),
+    (dict(ldx=63), ESHAPE), (dict(ldy=95), ESHAPE), (dict(ldb=95, Y=ODD), ESHAPE),
+    (dict(ldx=1 << 40), ESHAPE), (dict(L=1024, R=256, K=1 << 30, ldx=1 << 30), ESHAPE),
+    (dict(T=(1 << 31) - 1, N=1 << 20, ldy=1 << 20, ldb=1 << 20), ESHAPE),
+    (dict(dtype=FP32), EUNSUP), (dict(dtype=5), EINVAL),
+    (dict(X=None), EINVAL), (dict(A=None), EINVAL), (dict(B=None), EINVAL), (dict(m=None), EINVAL),
+    (dict(Y=None), EINVAL), (dict(X=ODD), EINVAL), (dict(A=ODD), EINVAL), (dict(B=ODD), EINVAL),
+    (dict(Y=ODD), EINVAL), (dict(base=ODD), EINVAL), (dict(m=TWO), EINVAL),
+    (dict(gather=TWO), EINVAL), (dict(ranks=TWO), EINVAL), (dict(scales=TWO), EINVAL),
+    (dict(H=TWO), EINVAL), (dict(ldb=100), EINVAL),             # base is Y, other strides
+    (dict(ws=None), EWS), (dict(size=10), EWS), (dict(ws=TWO), EWS),
+])
+def test_lora_refusals(lib, kw, want):
+    assert lora(lib, **kw) == want
+
+
+def test_lora_no_rows(lib):
+    assert lora(lib, T=0, X=None, Y=None, base=None, ws=None, size=0) == 0
+
+
+def lora_bwd(lib, X=P, ldx=64, dY=P, lddy=96, A=P, B=P, H=P, m=P, gather=P, ranks=None, scales=None,
+             dtype=BF16, T=10, L=4, R=16, K=64, N=96, base=P, ldb=64, dX=P, lddx=64, dA=P, dB=P,
+             flags=0, ws=P, size=1 << 20):
+    return lib.moegg_lora_bwd(X, ldx, dY, lddy, A, B, H, m, gather, ranks, scales, dtype, T, L, R,
+                              K, N, base, ldb, dX, lddx, dA, dB, flags, ws, size, None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(T=-1), ESHAPE), (dict(L=0), ESHAPE), (dict(R=300), ESHAPE), (dict(lddy=95), ESHAPE),
+    (dict(ldx=63), ESHAPE), (dict(lddx=63), ESHAPE), (dict(ldb=63, dX=TWO), ESHAPE),
+    (dict(dtype=FP32), EUNSUP), (dict(dtype=-1), EINVAL), (dict(flags=2), EINVAL),
+    (dict(dA=None), EINVAL), (dict(dB=None), EINVAL), (dict(X=None), EINVAL), (dict(H=None), EINVAL),
+    (dict(dY=None), EINVAL), (dict(A=None), EINVAL), (dict(B=None), EINVAL), (dict(m=None), EINVAL),
+    (dict(dX=ODD, base=None), EINVAL), (dict(base=ODD), EINVAL), (dict(dA=ODD), EINVAL),
+    (dict(dB=TWO, flags=1), EINVAL), (dict(H=TWO), EINVAL), (dict(ldb=80), EINVAL),
+    (dict(ws=None), EWS), (dict(size=100), EWS),
+])
+def test_lora_bwd_refusals(lib, kw, want):
+    assert lora_bwd(lib, **kw) == want
+
+
+def test_lora_workspace_sizes(lib):
+    f, b = lib.moegg_lora_workspace_bytes, lib.moegg_lora_bwd_workspace_bytes
+    # 64 rows over 32 adapters: 36 tiles, 8 workgroups a tile over 4096 columns
+    assert f(64, 32, 16, 4096, 4096) == 8 * 64 * 16 * 4
+    # many tiles: one sum each
+    assert f(8192, 8, 64, 4096, 4096) == 8192 * 64 * 4
+    assert f(0, 4, 16, 64, 64) == 0 and b(0, 4, 16, 64, 64) == 0
+    assert f(-1, 4, 16, 64, 64) == 0 and b(10, 4, 300, 64, 64) == 0
+    # dh alone up to one chunk of rows, then at most 2 T / chunk partial sums
+    assert b(512, 1, 16, 64, 96) == 512 * 16 * 4
+    assert b(4096, 4, 32, 4096, 4096) == 4096 * 32 * 4 + 16 * 32 * 8192 * 4
+    # a size just below what is needed
+    need = f(64, 32, 16, 4096, 4096)
+    assert lora(lib, T=64, L=32, K=4096, N=4096, ldx=4096, ldy=4096, ldb=4096,
+                size=need - 1) == EWS

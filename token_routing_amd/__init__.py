@@ -27,13 +27,17 @@ DERR_EXPERT_ID = 1
 DERR_M_SIZES = 2
 DERR_GATHER = 4
 DERR_LOGIT = 8
+DERR_RANK = 16
 
 MAX_EXPERTS = 1024
 MAX_GROUPS = 16
 MAX_TOPK = 64
+MAX_LORA_RANK = 256
 
 GATE_SIGMOID = 1
 GATE_RENORM = 2
+
+LORA_FP32_GRAD = 1
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -114,6 +118,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moegg_unpermute_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, i32, i32, i32, i64, vp,
                                         vp, vp, vp]
     lib.moegg_unpermute_bwd.restype = ctypes.c_int
+    lib.moegg_lora_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+    lib.moegg_lora_workspace_bytes.restype = sz
+    lib.moegg_lora_bwd_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+    lib.moegg_lora_bwd_workspace_bytes.restype = sz
+    lib.moegg_lora_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32,
+                                   vp, i64, vp, i64, vp, vp, sz, vp, vp]
+    lib.moegg_lora_fwd.restype = ctypes.c_int
+    lib.moegg_lora_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i64, i32,
+                                   i32, i32, i32, vp, i64, vp, i64, vp, vp, u32, vp, sz, vp, vp]
+    lib.moegg_lora_bwd.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -660,5 +674,115 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
             _arg(_flat(g) if want_dw else None, "dw", torch.float32, (S,), dev),
             _flag_arg(error_flags, dev), stream_ptr), "moegg_unpermute_bwd")
         return out, (g if want_dw else None)
+
+    return _run(dev, stream, call)
+
+
+def lora_workspace_bytes(num_rows: int, num_adapters: int, R: int, K: int, N: int) -> int:
+    """Workspace bytes of lora_fwd."""
+    return int(load_library().moegg_lora_workspace_bytes(num_rows, num_adapters, R, K, N))
+
+
+def lora_bwd_workspace_bytes(num_rows: int, num_adapters: int, R: int, K: int, N: int) -> int:
+    """Workspace bytes of lora_bwd."""
+    return int(load_library().moegg_lora_bwd_workspace_bytes(num_rows, num_adapters, R, K, N))
+
+
+def _workspace_arg(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, _arg(workspace, "workspace", torch.uint8, (None,), device)
+
+
+def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base=None, Y=None,
+             H=None, want_h: bool = False, workspace=None, error_flags=None, stream=None):
+    """Low-rank adapters of many requests on a shared projection's output
+    (moegg_lora_fwd): Y[i] = base[i] + scales[a] * (X[i] A_a^T) B_a^T.
+
+    X: [T, K] bf16 or fp16, A: [L, R, K], B: [L, N, R]; m_sizes int32 [L] and
+    gather_idx int32 [T] from moe_route over the rows' adapter ids (None: rows
+    are in adapter order already); ranks int32 [L] or None (R); scales fp32 [L]
+    or None (1).  base [T, N]: the projection's output; None adds to Y in
+    place.  X, base and Y may have any row stride.  Returns (Y, H): H is fp32
+    [T, R] in adapter order for lora_bwd, None unless given or want_h.
+    """
+    lib = load_library()
+    dev = X.device
+    L, R, K = A.shape
+    T, N = X.shape[0], B.shape[1]
+    dt = X.dtype
+    code = _dtype_code(X, "X")
+    if base is None and Y is None:
+        raise ValueError("base or Y is needed")
+
+    def call(stream_ptr):
+        y = torch.empty(T, N, dtype=dt, device=dev) if Y is None else Y
+        h = H
+        if h is None and want_h:
+            h = torch.empty(T, R, dtype=torch.float32, device=dev)
+        need = lib.moegg_lora_workspace_bytes(T, L, R, K, N)
+        ws, ws_ptr = _workspace_arg(workspace, need, dev)
+        x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), dev)
+        y_ptr, ldy = _rows_arg(y, "Y", dt, (T, N), dev)
+        b_ptr, ldb = (None, ldy) if base is None else _rows_arg(base, "base", dt, (T, N), dev)
+        _check(lib.moegg_lora_fwd(
+            x_ptr, ldx, _arg(A, "A", dt, (L, R, K), dev), _arg(B, "B", dt, (L, N, R), dev),
+            _arg(m_sizes, "m_sizes", torch.int32, (L,), dev),
+            _arg(gather_idx, "gather_idx", torch.int32, (T,), dev),
+            _arg(ranks, "ranks", torch.int32, (L,), dev),
+            _arg(scales, "scales", torch.float32, (L,), dev), code, T, L, R, K, N, b_ptr, ldb,
+            y_ptr, ldy, _arg(h, "H", torch.float32, (T, R), dev), ws_ptr, ws.numel(),
+            _flag_arg(error_flags, dev), stream_ptr), "moegg_lora_fwd")
+        return y, h
+
+    return _run(dev, stream, call)
+
+
+def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=None, base=None,
+             dX=None, dA=None, dB=None, want_dx: bool = True, want_weights: bool = True,
+             fp32_grads: bool = False, workspace=None, error_flags=None, stream=None):
+    """Gradients of lora_fwd (moegg_lora_bwd): (dX [T, K], dA [L, R, K], dB [L, N, R]).
+
+    base [T, K]: the shared projection's input gradient, which dX adds to; None
+    adds to the dX given.  want_dx=False or want_weights=False leave dX or dA
+    and dB out (None in their place).  fp32_grads writes dA and dB in fp32.
+    """
+    lib = load_library()
+    dev = dY.device
+    L, R, K = A.shape
+    T, N = dY.shape
+    dt = dY.dtype
+    code = _dtype_code(dY, "dY")
+    if want_dx and base is None and dX is None:
+        raise ValueError("base or dX is needed (or want_dx=False)")
+    wt = torch.float32 if fp32_grads else dt
+
+    def call(stream_ptr):
+        dx, x_ptr, ldx, dx_ptr, lddx, b_ptr, ldb = None, None, K, None, K, None, K
+        da = db = None
+        if want_dx:
+            dx = torch.empty(T, K, dtype=dt, device=dev) if dX is None else dX
+            dx_ptr, lddx = _rows_arg(dx, "dX", dt, (T, K), dev)
+            if base is not None:
+                b_ptr, ldb = _rows_arg(base, "base", dt, (T, K), dev)
+        if want_weights:
+            da = torch.empty(L, R, K, dtype=wt, device=dev) if dA is None else dA
+            db = torch.empty(L, N, R, dtype=wt, device=dev) if dB is None else dB
+            x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), dev)
+        dy_ptr, lddy = _rows_arg(dY, "dY", dt, (T, N), dev)
+        need = lib.moegg_lora_bwd_workspace_bytes(T, L, R, K, N)
+        ws, ws_ptr = _workspace_arg(workspace, need, dev)
+        _check(lib.moegg_lora_bwd(
+            x_ptr, ldx, dy_ptr, lddy, _arg(A, "A", dt, (L, R, K), dev),
+            _arg(B, "B", dt, (L, N, R), dev),
+            _arg(H, "H", torch.float32, (T, R), dev) if want_weights else None,
+            _arg(m_sizes, "m_sizes", torch.int32, (L,), dev),
+            _arg(gather_idx, "gather_idx", torch.int32, (T,), dev),
+            _arg(ranks, "ranks", torch.int32, (L,), dev),
+            _arg(scales, "scales", torch.float32, (L,), dev), code, T, L, R, K, N, b_ptr, ldb,
+            dx_ptr, lddx, _arg(da, "dA", wt, (L, R, K), dev), _arg(db, "dB", wt, (L, N, R), dev),
+            LORA_FP32_GRAD if fp32_grads else 0, ws_ptr, ws.numel(), _flag_arg(error_flags, dev),
+            stream_ptr), "moegg_lora_bwd")
+        return dx, da, db
 
     return _run(dev, stream, call)

@@ -33,7 +33,7 @@ FLAGS = [
 ]
 
 SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "gate.hip", "sort.hip",
-           "api.hip"]
+           "lora.hip", "api.hip"]
 
 
 def _compile(src: str, report: bool, defines=(), build_dir=BUILD) -> str:

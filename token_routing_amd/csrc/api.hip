@@ -12,6 +12,7 @@
 
 #include "gemm_params.h"
 #include "layer_params.h"
+#include "lora_params.h"
 
 namespace {
 
@@ -736,6 +737,217 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
     p.E = num_experts;
     p.K = K;
     return from_hip(moegg::spread_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+// Sizes of the adapter entry points; also bounds every launch's grid.
+static moegg_status check_lora_sizes(int64_t T, int32_t L, int32_t R, int32_t K, int32_t N)
+{
+    constexpr int64_t kMax = (int64_t)1 << 39;  // elements: 2^40 bytes of 16 bits
+    if (T < 0 || T > INT32_MAX || L < 1 || L > MOEGG_MAX_EXPERTS || R < 1 ||
+        R > MOEGG_MAX_LORA_RANK || K < 1 || N < 1 || K > (1 << 30) || N > (1 << 30))
+        return MOEGG_ESHAPE;
+    const int64_t wide = K > N ? K : N;
+    if ((int64_t)L * R > kMax / wide || (T > 0 && wide > kMax / T))
+        return MOEGG_ESHAPE;
+    const int64_t cols = wide / 128 + 1, tiles = (T / 32 + 1 + L) * cols;
+    const int64_t items = (L + T / 512) * (2 * cols) * ((R + 15) / 16);
+    if (tiles > INT32_MAX || items > INT32_MAX)
+        return MOEGG_ESHAPE;
+    return MOEGG_OK;
+}
+
+// Row stride of a matrix of T rows of n elements.
+static bool stride_ok(int64_t ld, int64_t n, int64_t T)
+{
+    return ld >= n && (T == 0 || ld <= ((int64_t)1 << 39) / T);
+}
+
+static size_t lora_h_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
+{
+    const size_t b = (size_t)moegg::lora_splits(T, L, C) * (size_t)T * (size_t)R * sizeof(float);
+    return (b + 255) / 256 * 256;
+}
+
+size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
+                                  int32_t N)
+{
+    if (check_lora_sizes(num_rows, num_adapters, R, K, N) != MOEGG_OK)
+        return 0;
+    return lora_h_bytes(num_rows, num_adapters, R, K);
+}
+
+size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R,
+                                      int32_t K, int32_t N)
+{
+    if (check_lora_sizes(num_rows, num_adapters, R, K, N) != MOEGG_OK)
+        return 0;
+    // dh, then the chunks' partial sums: adapters of more than one chunk hold
+    // fewer than 2 T / chunk of them together
+    const int64_t chunk = moegg::lora_chunk(num_rows);
+    const size_t parts = num_rows > chunk ? (size_t)(2 * num_rows / chunk) : 0;
+    return lora_h_bytes(num_rows, num_adapters, R, N) +
+           parts * (size_t)R * ((size_t)K + (size_t)N) * sizeof(float);
+}
+
+static moegg_status check_lora_dtype(int32_t dtype)
+{
+    return !known_dtype(dtype) ? MOEGG_EINVAL : dtype == MOEGG_FP32 ? MOEGG_EUNSUPPORTED : MOEGG_OK;
+}
+
+moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const void *B,
+                            const int32_t *m_sizes, const int32_t *gather_idx,
+                            const int32_t *ranks, const float *scales, int32_t dtype,
+                            int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
+                            int32_t N, const void *base, int64_t ld_base, void *Y, int64_t ldy,
+                            float *H, void *workspace, size_t workspace_bytes,
+                            int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_lora_sizes(num_rows, num_adapters, R, K, N);
+    if (st == MOEGG_OK)
+        st = check_lora_dtype(dtype);
+    if (st != MOEGG_OK)
+        return st;
+    if (!base) {
+        base = Y;
+        ld_base = ldy;
+    }
+    if (!stride_ok(ldx, K, num_rows) || !stride_ok(ldy, N, num_rows) ||
+        !stride_ok(ld_base, N, num_rows))
+        return MOEGG_ESHAPE;
+    if (num_rows == 0)
+        return MOEGG_OK;
+    if (!X || !A || !B || !m_sizes || !Y || !aligned2(X) || !aligned2(A) || !aligned2(B) ||
+        !aligned4(m_sizes) || !aligned4(gather_idx) || !aligned4(ranks) || !aligned4(scales) ||
+        !aligned2(base) || !aligned2(Y) || !aligned4(H) || (base == Y && ld_base != ldy))
+        return MOEGG_EINVAL;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < moegg_lora_workspace_bytes(num_rows, num_adapters, R, K, N))
+        return MOEGG_EWORKSPACE;
+    moegg::LoraParams p = {};
+    p.m_sizes = m_sizes;
+    p.gather = gather_idx;
+    p.ranks = ranks;
+    p.scales = scales;
+    p.err = error_flags;
+    p.T = num_rows;
+    p.L = num_adapters;
+    p.R = R;
+    p.splits = moegg::lora_splits(num_rows, num_adapters, K);
+    p.split_stride = num_rows * R;
+    p.h = H && p.splits == 1 ? H : static_cast<float *>(workspace);
+    p.in = static_cast<const uint16_t *>(X);
+    p.w = static_cast<const uint16_t *>(A);
+    p.ld_in = ldx;
+    p.C = K;
+    hipError_t e = moegg::lora_shrink_launch(p, dtype, false, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess)
+        return from_hip(e);
+    p.w = static_cast<const uint16_t *>(B);
+    p.C = N;
+    p.base = static_cast<const uint16_t *>(base);
+    p.out = static_cast<uint16_t *>(Y);
+    p.ld_base = ld_base;
+    p.ld_out = ldy;
+    p.h_out = p.splits > 1 ? H : nullptr;
+    return from_hip(
+        moegg::lora_expand_launch(p, dtype, false, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t lddy,
+                            const void *A, const void *B, const float *H, const int32_t *m_sizes,
+                            const int32_t *gather_idx, const int32_t *ranks, const float *scales,
+                            int32_t dtype, int64_t num_rows, int32_t num_adapters, int32_t R,
+                            int32_t K, int32_t N, const void *base, int64_t ld_base, void *dX,
+                            int64_t lddx, void *dA, void *dB, uint32_t flags, void *workspace,
+                            size_t workspace_bytes, int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_lora_sizes(num_rows, num_adapters, R, K, N);
+    if (st == MOEGG_OK)
+        st = check_lora_dtype(dtype);
+    if (st != MOEGG_OK)
+        return st;
+    if (!dA != !dB || (flags & ~(uint32_t)MOEGG_LORA_FP32_GRAD))
+        return MOEGG_EINVAL;
+    if (!dX)
+        lddx = K;
+    if (!base || !dX) {
+        base = dX;
+        ld_base = lddx;
+    }
+    if (!dA)
+        ldx = K;
+    if (!stride_ok(ldx, K, num_rows) || !stride_ok(lddy, N, num_rows) ||
+        !stride_ok(lddx, K, num_rows) || !stride_ok(ld_base, K, num_rows))
+        return MOEGG_ESHAPE;
+    if (num_rows == 0 && !dA)
+        return MOEGG_OK;
+    if (!m_sizes || !aligned4(m_sizes) || !aligned4(gather_idx) || !aligned4(ranks) ||
+        !aligned4(scales) || !aligned2(base) || !aligned2(dX) || (base == dX && ld_base != lddx))
+        return MOEGG_EINVAL;
+    if (num_rows > 0 && (!dY || !A || !B || !aligned2(dY) || !aligned2(A) || !aligned2(B)))
+        return MOEGG_EINVAL;
+    if (dA) {
+        if (num_rows > 0 && (!X || !H || !aligned2(X) || !aligned4(H)))
+            return MOEGG_EINVAL;
+        if ((flags & MOEGG_LORA_FP32_GRAD) ? !aligned4(dA) || !aligned4(dB)
+                                           : !aligned2(dA) || !aligned2(dB))
+            return MOEGG_EINVAL;
+    }
+    if (num_rows > 0 &&
+        (!workspace || !aligned16(workspace) ||
+         workspace_bytes < moegg_lora_bwd_workspace_bytes(num_rows, num_adapters, R, K, N)))
+        return MOEGG_EWORKSPACE;
+    moegg::LoraParams p = {};
+    p.m_sizes = m_sizes;
+    p.gather = gather_idx;
+    p.ranks = ranks;
+    p.scales = scales;
+    p.err = error_flags;
+    p.T = num_rows;
+    p.L = num_adapters;
+    p.R = R;
+    p.splits = moegg::lora_splits(num_rows, num_adapters, N);
+    p.split_stride = num_rows * R;
+    p.h = static_cast<float *>(workspace);
+    p.scale_shrink = true;
+    p.in = static_cast<const uint16_t *>(dY);
+    p.w = static_cast<const uint16_t *>(B);
+    p.ld_in = lddy;
+    p.C = N;
+    hipError_t e = moegg::lora_shrink_launch(p, dtype, true, static_cast<hipStream_t>(stream));
+    if (e == hipSuccess && dX) {
+        p.w = static_cast<const uint16_t *>(A);
+        p.C = K;
+        p.base = static_cast<const uint16_t *>(base);
+        p.out = static_cast<uint16_t *>(dX);
+        p.ld_base = ld_base;
+        p.ld_out = lddx;
+        e = moegg::lora_expand_launch(p, dtype, true, static_cast<hipStream_t>(stream));
+    }
+    if (e != hipSuccess || !dA)
+        return from_hip(e);
+    moegg::GradParams g = {};
+    g.l = p;
+    g.x = static_cast<const uint16_t *>(X);
+    g.dy = static_cast<const uint16_t *>(dY);
+    g.h = H;
+    g.dh = p.h;
+    g.dA = dA;
+    g.dB = dB;
+    g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                           lora_h_bytes(num_rows, num_adapters, R, N));
+    g.ld_x = ldx;
+    g.ld_dy = lddy;
+    g.split_stride = p.split_stride;
+    g.R = R;
+    g.K = K;
+    g.N = N;
+    g.splits = p.splits;
+    g.chunk = moegg::lora_chunk(num_rows);
+    g.col_tiles_a = (K + 127) / 128;
+    g.col_tiles_b = (N + 127) / 128;
+    g.fp32_out = flags & MOEGG_LORA_FP32_GRAD;
+    return from_hip(moegg::lora_grad_launch(g, dtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

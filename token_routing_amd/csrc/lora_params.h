@@ -1,0 +1,71 @@
+// Kernel parameter blocks, launch sizes and host launchers of the low-rank
+// adapters.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moegg {
+
+constexpr int kShrinkRows = 16;   // rows of a shrink tile
+constexpr int kExpandRows = 64;   // rows of an expand tile, forward
+constexpr int kExpandRowsT = 32;  // and with transposed weights (dx)
+
+// Shrink (in, w -> h) and expand (h, w, base -> out) of T rows; C is the wide
+// dimension: columns of `in` or of `out`.
+struct LoraParams {
+    const uint16_t *in;
+    const uint16_t *w;
+    const int32_t *m_sizes;
+    const int32_t *gather;
+    const int32_t *ranks;
+    const float *scales;
+    const uint16_t *base;
+    uint16_t *out;
+    float *h;      // [splits][T][R]
+    float *h_out;  // [T][R] the caller's sum of the splits, or null
+    int32_t *err;
+    int64_t T, ld_in, ld_base, ld_out, split_stride;
+    int L, R, C, splits;
+    bool scale_shrink;  // the adapter's scale belongs to h (backward), not to out
+};
+
+struct GradParams {
+    LoraParams l;  // m_sizes, gather, ranks, scales, err, T, L
+    const uint16_t *x;
+    const uint16_t *dy;
+    const float *h;
+    const float *dh;
+    void *dA;
+    void *dB;
+    float *partials;
+    int64_t ld_x, ld_dy, split_stride;
+    int R, K, N, splits, chunk;
+    int col_tiles_a, col_tiles_b;  // 128-column tiles of dA and dB (0: not wanted)
+    bool fp32_out;
+};
+
+// Shrink splits: how many workgroups share a tile's reduction of C columns.
+// One workgroup a compute unit (256) is aimed at; a wave's share stays at 64
+// columns or more, and at most 16 partial sums are left to add.
+inline int lora_splits(int64_t T, int L, int C)
+{
+    const int64_t tiles = (T + kShrinkRows - 1) / kShrinkRows + (T < L ? T : L);
+    int64_t n = tiles > 0 ? (256 + tiles - 1) / tiles : 1;
+    n = n < C / 512 ? n : C / 512;
+    return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
+}
+
+// Rows of one chunk of the gradients' reduction: 512, more when that would
+// leave over 16 chunks to add.
+inline int lora_chunk(int64_t T)
+{
+    const int64_t c = ((T + 15) / 16 + 127) / 128 * 128;
+    return (int)(c < 512 ? 512 : c);
+}
+
+hipError_t lora_shrink_launch(const LoraParams &p, int dtype, bool transposed, hipStream_t stream);
+hipError_t lora_expand_launch(const LoraParams &p, int dtype, bool transposed, hipStream_t stream);
+hipError_t lora_grad_launch(const GradParams &p, int dtype, hipStream_t stream);
+
+}  // namespace moegg
