@@ -118,7 +118,18 @@ def test_python_argument_checks():
     with pytest.raises(ValueError):
         mg._dtype_code(torch.zeros(2, dtype=torch.float64), "x")
     with pytest.raises(ValueError):
-        mg._flat(torch.zeros(4, 4).t())
+        mg.lora_fwd(cpu, torch.zeros(1, 2, 8), torch.zeros(1, 3, 2),
+                    torch.zeros(1, dtype=torch.int32), base=torch.zeros(4, 3))
+    # checks of layout, on tensors that need no GPU (index -1 is the CPU)
+    assert mg._rows_arg(torch.zeros(4, 9)[:, 2:5], "x", torch.float32, (4, 3), -1)[1] == 9
+    assert mg._rows_arg(torch.zeros(4, 9)[2:3, 2:5], "x", torch.float32, (1, 3), -1)[1] >= 3
+    for t in (torch.zeros(3, 4).t(), torch.zeros(1, 3).expand(4, 3), torch.zeros(4, 6)[:, ::2]):
+        with pytest.raises(ValueError):
+            mg._rows_arg(t, "x", torch.float32, (4, 3), -1)
+    with pytest.raises(ValueError):
+        mg._slots_arg(torch.zeros(4, 4).t(), "w", torch.float32, 16, -1)
+    with pytest.raises(ValueError):
+        mg._arg(torch.zeros(4, 4), "w", torch.float32, (4, 5), -1)
 
 
 def lora(lib, X=P, ldx=64, A=P, B=P, m=P, gather=P, ranks=None, scales=None, dtype=BF16, T=10, L=4,

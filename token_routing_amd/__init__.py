@@ -417,17 +417,18 @@ def combine_bwd(dOut, Y, topk: int, scatter_idx=None, topk_weights=None, *, want
 
 def _run(device, stream, call):
     """call(stream handle) with `device` current and, when given, `stream` current."""
-    if device.type != "cuda":
+    index = device.index
+    if index is None or device.type != "cuda":
         raise ValueError(f"tensors must be on a GPU, not on {device}")
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            return call(torch._C._cuda_getCurrentRawStream(index))
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):        # makes the stream's device current as well
+        return call(stream.cuda_stream)
 
 
 def _dtype_code(t, name):
@@ -437,40 +438,52 @@ def _dtype_code(t, name):
     return code
 
 
-def _arg(t, name, dtype, shape, device):
-    """Address of a contiguous CUDA tensor of this type, shape (None: any size) and device."""
+def _refuse(t, name, dtype, shape, index):
+    if t.dtype != dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor on cuda:{index}, not {t.dtype} on "
+                         f"{t.device}")
+    raise ValueError(f"{name} must be contiguous of shape {tuple(shape)}, not {tuple(t.shape)} "
+                     f"with strides {t.stride()}")
+
+
+def _arg(t, name, dtype, shape, index):
+    """Address of a contiguous tensor of this type and shape on GPU `index`."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
-    if len(shape) != t.dim() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, index)
 
 
-def _rows_arg(t, name, dtype, shape, device):
-    """Address and row stride of a CUDA matrix whose rows are contiguous."""
-    if t.dtype != dtype or t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a {dtype} tensor on {device}, not {t.dtype} on {t.device}")
-    if t.dim() != 2 or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    if (cols > 1 and rows and t.stride(1) != 1) or (rows and ld < cols):
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), max(ld, cols)
+def _slots_arg(t, name, dtype, slots, index):
+    """Address of a contiguous per-slot tensor: [slots] or [T, topk]."""
+    if t is None:
+        return None
+    if (t.dtype is dtype and t.numel() == slots and t.get_device() == index
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, (slots,), index)
 
 
-def _flag_arg(t, device):
-    return None if t is None else _arg(t, "error_flags", torch.int32, (1,), device)
+def _rows_arg(t, name, dtype, shape, index):
+    """Address and row stride of a matrix whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, name, dtype, shape, index)
+    rows, cols = shape
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    ld, step = t.stride()
+    if rows == 1:
+        ld = max(ld, cols)
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, not strides "
+                         f"{t.stride()}")
+    return t.data_ptr(), ld
 
 
-def _flat(t):
-    if t is not None and not t.is_contiguous():
-        raise ValueError("per-slot arrays must be contiguous")
-    return None if t is None else t.view(-1)
+def _flag_arg(t, index):
+    return None if t is None else _slots_arg(t, "error_flags", torch.int32, 1, index)
 
 
 def moe_gate(logits, topk: int, *, bias=None, n_groups: int = 1, topk_groups: int = 1,
@@ -487,8 +500,9 @@ def moe_gate(logits, topk: int, *, bias=None, n_groups: int = 1, topk_groups: in
     """
     lib = load_library()
     dev = logits.device
+    index = dev.index
     T, E = logits.shape
-    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), dev)
+    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), index)
     code = _dtype_code(logits, "logits")
     topk = int(topk)
 
@@ -499,12 +513,12 @@ def moe_gate(logits, topk: int, *, bias=None, n_groups: int = 1, topk_groups: in
         if s is None and want_scores:
             s = torch.empty(T, E, dtype=torch.float32, device=dev)
         _check(lib.moegg_gate(
-            ptr, code, ld, _arg(bias, "bias", torch.float32, (E,), dev), T, E, topk, int(n_groups),
+            ptr, code, ld, _arg(bias, "bias", torch.float32, (E,), index), T, E, topk, int(n_groups),
             int(topk_groups), float(scale),
             (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
-            _arg(i, "ids", torch.int32, (T, topk), dev),
-            _arg(w, "weights", torch.float32, (T, topk), dev),
-            _arg(s, "scores", torch.float32, (T, E), dev), _flag_arg(error_flags, dev),
+            _arg(i, "ids", torch.int32, (T, topk), index),
+            _arg(w, "weights", torch.float32, (T, topk), index),
+            _arg(s, "scores", torch.float32, (T, E), index), _flag_arg(error_flags, index),
             stream_ptr), "moegg_gate")
         return i, w, s
 
@@ -521,19 +535,20 @@ def moe_gate_bwd(logits, ids, dweights, *, dscores=None, scale: float = 1.0,
     logits' type."""
     lib = load_library()
     dev = logits.device
+    index = dev.index
     T, E = logits.shape
-    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), dev)
+    ptr, ld = _rows_arg(logits, "logits", logits.dtype, (T, E), index)
     code = _dtype_code(logits, "logits")
     topk = ids.shape[-1]
 
     def call(stream_ptr):
         d = torch.empty(T, E, dtype=logits.dtype, device=dev) if dlogits is None else dlogits
         _check(lib.moegg_gate_bwd(
-            ptr, code, ld, _arg(ids, "ids", torch.int32, (T, topk), dev),
-            _arg(dweights, "dweights", torch.float32, (T, topk), dev),
-            _arg(dscores, "dscores", torch.float32, (T, E), dev), T, E, topk, float(scale),
+            ptr, code, ld, _arg(ids, "ids", torch.int32, (T, topk), index),
+            _arg(dweights, "dweights", torch.float32, (T, topk), index),
+            _arg(dscores, "dscores", torch.float32, (T, E), index), T, E, topk, float(scale),
             (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
-            _arg(d, "dlogits", logits.dtype, (T, E), dev), _flag_arg(error_flags, dev),
+            _arg(d, "dlogits", logits.dtype, (T, E), index), _flag_arg(error_flags, index),
             stream_ptr), "moegg_gate_bwd")
         return d
 
@@ -553,6 +568,7 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
     """
     lib = load_library()
     dev = X.device
+    index = dev.index
     T, K = X.shape
     S = T * topk
     code = _dtype_code(X, "X")
@@ -568,13 +584,13 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
         out = torch.empty(rows, K, dtype=X.dtype, device=dev) if Xs is None else Xs
         m = torch.empty(S, dtype=torch.int32, device=dev) if row_map is None else row_map
         _check(lib.moegg_permute(
-            _arg(X, "X", X.dtype, (T, K), dev), code,
-            _arg(_flat(scatter_idx), "scatter_idx", torch.int32, (S,), dev),
-            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
-            _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), dev), T, topk, E, K,
-            rows, _arg(out, "Xs", X.dtype, (rows, K), dev),
-            _arg(m, "row_map", torch.int32, (S,), dev), _flag_arg(error_flags, dev), stream_ptr),
+            _arg(X, "X", X.dtype, (T, K), index), code,
+            _slots_arg(scatter_idx, "scatter_idx", torch.int32, S, index),
+            _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), index),
+            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), index), T, topk, E, K,
+            rows, _arg(out, "Xs", X.dtype, (rows, K), index),
+            _arg(m, "row_map", torch.int32, (S,), index), _flag_arg(error_flags, index), stream_ptr),
             "moegg_permute")
         return out, m
 
@@ -587,6 +603,7 @@ def permute_bwd(dXs, X, topk: int, row_map, topk_weights=None, *, want_dw: bool 
     X (the forward's input) is read only for dw."""
     lib = load_library()
     dev = dXs.device
+    index = dev.index
     rows, K = dXs.shape
     S = row_map.numel()
     T = S // topk
@@ -598,13 +615,13 @@ def permute_bwd(dXs, X, topk: int, row_map, topk_weights=None, *, want_dw: bool 
         if want_dw and g is None:
             g = torch.empty(S, dtype=torch.float32, device=dev)
         _check(lib.moegg_permute_bwd(
-            _arg(dXs, "dXs", dXs.dtype, (rows, K), dev), code,
-            _arg(X, "X", dXs.dtype, (T, K), dev),
-            _arg(_flat(row_map), "row_map", torch.int32, (T * topk,), dev),
-            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev), T, topk, K, rows,
-            _arg(out, "dX", dXs.dtype, (T, K), dev),
-            _arg(_flat(g) if want_dw else None, "dw", torch.float32, (S,), dev),
-            _flag_arg(error_flags, dev), stream_ptr), "moegg_permute_bwd")
+            _arg(dXs, "dXs", dXs.dtype, (rows, K), index), code,
+            _arg(X, "X", dXs.dtype, (T, K), index),
+            _slots_arg(row_map, "row_map", torch.int32, T * topk, index),
+            _slots_arg(topk_weights, "topk_weights", torch.float32, S, index), T, topk, K, rows,
+            _arg(out, "dX", dXs.dtype, (T, K), index),
+            _slots_arg(g if want_dw else None, "dw", torch.float32, S, index),
+            _flag_arg(error_flags, index), stream_ptr), "moegg_permute_bwd")
         return out, (g if want_dw else None)
 
     return _run(dev, stream, call)
@@ -616,6 +633,7 @@ def unpermute(Y, topk: int, row_map, topk_weights=None, *, base=None, out=None, 
     out[t] = base[t] + sum_j w[s] * Y[row_map[s]].  base may be out."""
     lib = load_library()
     dev = Y.device
+    index = dev.index
     rows, K = Y.shape
     S = row_map.numel()
     T = S // topk
@@ -624,11 +642,11 @@ def unpermute(Y, topk: int, row_map, topk_weights=None, *, base=None, out=None, 
     def call(stream_ptr):
         o = torch.empty(T, K, dtype=Y.dtype, device=dev) if out is None else out
         _check(lib.moegg_unpermute(
-            _arg(Y, "Y", Y.dtype, (rows, K), dev), code,
-            _arg(_flat(row_map), "row_map", torch.int32, (T * topk,), dev),
-            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
-            _arg(base, "base", Y.dtype, (T, K), dev), T, topk, K, rows,
-            _arg(o, "out", Y.dtype, (T, K), dev), _flag_arg(error_flags, dev), stream_ptr),
+            _arg(Y, "Y", Y.dtype, (rows, K), index), code,
+            _slots_arg(row_map, "row_map", torch.int32, T * topk, index),
+            _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
+            _arg(base, "base", Y.dtype, (T, K), index), T, topk, K, rows,
+            _arg(o, "out", Y.dtype, (T, K), index), _flag_arg(error_flags, index), stream_ptr),
             "moegg_unpermute")
         return o
 
@@ -647,6 +665,7 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
     """
     lib = load_library()
     dev = dOut.device
+    index = dev.index
     T, K = dOut.shape
     S = T * topk
     code = _dtype_code(dOut, "dOut")
@@ -664,15 +683,15 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
         if want_dw and g is None:
             g = torch.empty(S, dtype=torch.float32, device=dev)
         _check(lib.moegg_unpermute_bwd(
-            _arg(dOut, "dOut", dOut.dtype, (T, K), dev), code,
-            _arg(Y, "Y", dOut.dtype, (rows, K), dev),
-            _arg(_flat(row_map), "row_map", torch.int32, (S,), dev),
-            _arg(_flat(topk_weights), "topk_weights", torch.float32, (S,), dev),
-            _arg(offsets, "offsets", torch.int32, (E + 1,), dev),
-            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), dev), T, topk, E, K,
-            rows, _arg(out, "dY", dOut.dtype, (rows, K), dev),
-            _arg(_flat(g) if want_dw else None, "dw", torch.float32, (S,), dev),
-            _flag_arg(error_flags, dev), stream_ptr), "moegg_unpermute_bwd")
+            _arg(dOut, "dOut", dOut.dtype, (T, K), index), code,
+            _arg(Y, "Y", dOut.dtype, (rows, K), index),
+            _slots_arg(row_map, "row_map", torch.int32, S, index),
+            _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
+            _arg(offsets, "offsets", torch.int32, (E + 1,), index),
+            _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), index), T, topk, E, K,
+            rows, _arg(out, "dY", dOut.dtype, (rows, K), index),
+            _slots_arg(g if want_dw else None, "dw", torch.float32, S, index),
+            _flag_arg(error_flags, index), stream_ptr), "moegg_unpermute_bwd")
         return out, (g if want_dw else None)
 
     return _run(dev, stream, call)
@@ -691,7 +710,8 @@ def lora_bwd_workspace_bytes(num_rows: int, num_adapters: int, R: int, K: int, N
 def _workspace_arg(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, _arg(workspace, "workspace", torch.uint8, (None,), device)
+    return workspace, _slots_arg(workspace, "workspace", torch.uint8, workspace.numel(),
+                                 device.index)
 
 
 def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base=None, Y=None,
@@ -708,6 +728,7 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
     """
     lib = load_library()
     dev = X.device
+    index = dev.index
     L, R, K = A.shape
     T, N = X.shape[0], B.shape[1]
     dt = X.dtype
@@ -722,17 +743,17 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
             h = torch.empty(T, R, dtype=torch.float32, device=dev)
         need = lib.moegg_lora_workspace_bytes(T, L, R, K, N)
         ws, ws_ptr = _workspace_arg(workspace, need, dev)
-        x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), dev)
-        y_ptr, ldy = _rows_arg(y, "Y", dt, (T, N), dev)
-        b_ptr, ldb = (None, ldy) if base is None else _rows_arg(base, "base", dt, (T, N), dev)
+        x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), index)
+        y_ptr, ldy = _rows_arg(y, "Y", dt, (T, N), index)
+        b_ptr, ldb = (None, ldy) if base is None else _rows_arg(base, "base", dt, (T, N), index)
         _check(lib.moegg_lora_fwd(
-            x_ptr, ldx, _arg(A, "A", dt, (L, R, K), dev), _arg(B, "B", dt, (L, N, R), dev),
-            _arg(m_sizes, "m_sizes", torch.int32, (L,), dev),
-            _arg(gather_idx, "gather_idx", torch.int32, (T,), dev),
-            _arg(ranks, "ranks", torch.int32, (L,), dev),
-            _arg(scales, "scales", torch.float32, (L,), dev), code, T, L, R, K, N, b_ptr, ldb,
-            y_ptr, ldy, _arg(h, "H", torch.float32, (T, R), dev), ws_ptr, ws.numel(),
-            _flag_arg(error_flags, dev), stream_ptr), "moegg_lora_fwd")
+            x_ptr, ldx, _arg(A, "A", dt, (L, R, K), index), _arg(B, "B", dt, (L, N, R), index),
+            _arg(m_sizes, "m_sizes", torch.int32, (L,), index),
+            _arg(gather_idx, "gather_idx", torch.int32, (T,), index),
+            _arg(ranks, "ranks", torch.int32, (L,), index),
+            _arg(scales, "scales", torch.float32, (L,), index), code, T, L, R, K, N, b_ptr, ldb,
+            y_ptr, ldy, _arg(h, "H", torch.float32, (T, R), index), ws_ptr, ws.numel(),
+            _flag_arg(error_flags, index), stream_ptr), "moegg_lora_fwd")
         return y, h
 
     return _run(dev, stream, call)
@@ -749,6 +770,7 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
     """
     lib = load_library()
     dev = dY.device
+    index = dev.index
     L, R, K = A.shape
     T, N = dY.shape
     dt = dY.dtype
@@ -762,26 +784,26 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
         da = db = None
         if want_dx:
             dx = torch.empty(T, K, dtype=dt, device=dev) if dX is None else dX
-            dx_ptr, lddx = _rows_arg(dx, "dX", dt, (T, K), dev)
+            dx_ptr, lddx = _rows_arg(dx, "dX", dt, (T, K), index)
             if base is not None:
-                b_ptr, ldb = _rows_arg(base, "base", dt, (T, K), dev)
+                b_ptr, ldb = _rows_arg(base, "base", dt, (T, K), index)
         if want_weights:
             da = torch.empty(L, R, K, dtype=wt, device=dev) if dA is None else dA
             db = torch.empty(L, N, R, dtype=wt, device=dev) if dB is None else dB
-            x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), dev)
-        dy_ptr, lddy = _rows_arg(dY, "dY", dt, (T, N), dev)
+            x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), index)
+        dy_ptr, lddy = _rows_arg(dY, "dY", dt, (T, N), index)
         need = lib.moegg_lora_bwd_workspace_bytes(T, L, R, K, N)
         ws, ws_ptr = _workspace_arg(workspace, need, dev)
         _check(lib.moegg_lora_bwd(
-            x_ptr, ldx, dy_ptr, lddy, _arg(A, "A", dt, (L, R, K), dev),
-            _arg(B, "B", dt, (L, N, R), dev),
-            _arg(H, "H", torch.float32, (T, R), dev) if want_weights else None,
-            _arg(m_sizes, "m_sizes", torch.int32, (L,), dev),
-            _arg(gather_idx, "gather_idx", torch.int32, (T,), dev),
-            _arg(ranks, "ranks", torch.int32, (L,), dev),
-            _arg(scales, "scales", torch.float32, (L,), dev), code, T, L, R, K, N, b_ptr, ldb,
-            dx_ptr, lddx, _arg(da, "dA", wt, (L, R, K), dev), _arg(db, "dB", wt, (L, N, R), dev),
-            LORA_FP32_GRAD if fp32_grads else 0, ws_ptr, ws.numel(), _flag_arg(error_flags, dev),
+            x_ptr, ldx, dy_ptr, lddy, _arg(A, "A", dt, (L, R, K), index),
+            _arg(B, "B", dt, (L, N, R), index),
+            _arg(H, "H", torch.float32, (T, R), index) if want_weights else None,
+            _arg(m_sizes, "m_sizes", torch.int32, (L,), index),
+            _arg(gather_idx, "gather_idx", torch.int32, (T,), index),
+            _arg(ranks, "ranks", torch.int32, (L,), index),
+            _arg(scales, "scales", torch.float32, (L,), index), code, T, L, R, K, N, b_ptr, ldb,
+            dx_ptr, lddx, _arg(da, "dA", wt, (L, R, K), index), _arg(db, "dB", wt, (L, N, R), index),
+            LORA_FP32_GRAD if fp32_grads else 0, ws_ptr, ws.numel(), _flag_arg(error_flags, index),
             stream_ptr), "moegg_lora_bwd")
         return dx, da, db
 
