@@ -574,10 +574,10 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
  * ids) keep what Y holds: with a separate base give rows without an adapter
  * one of rank 0.  h is kept in fp32 and enters the second product with 16
  * (bf16) or 22 (fp16) bits of mantissa; sums in fp32; Y is rounded once.
- * Bit-for-bit deterministic.  Any K, N and strides; rows need the alignment of
- * one element.  T = 0 is a no-op.
+ * Bit-for-bit deterministic.  Any K and N from 8 on and any strides; rows need
+ * the alignment of one element.  T = 0 is a no-op.
  * Errors: ESHAPE for T < 0, L outside [1, MOEGG_MAX_EXPERTS], R outside
- * [1, MOEGG_MAX_LORA_RANK], K or N < 1, a row stride below its row, sizes past
+ * [1, MOEGG_MAX_LORA_RANK], K or N < 8, a row stride below its row, sizes past
  * 2^40 bytes; EUNSUPPORTED for MOEGG_FP32; EINVAL for an unknown dtype, NULL
  * or misaligned pointers, base = Y with different strides; EWORKSPACE.
  */

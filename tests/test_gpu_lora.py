@@ -135,7 +135,8 @@ def close(got, ref, err):
 
 # T, L, R, K, N, dtype, ragged
 CASES = [
-    (1, 1, 1, 1, 1, "bf16", False),
+    (1, 1, 1, 8, 8, "bf16", False),
+    (3, 2, 2, 9, 67, "fp16", False),
     (1, 1, 16, 2048, 2048, "bf16", False),
     (1, 3, 8, 100, 70, "fp16", True),
     (7, 5, 4, 515, 264, "bf16", True),

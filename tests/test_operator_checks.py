@@ -143,7 +143,7 @@ EUNSUP, EWS = 3, 4
 
 @pytest.mark.parametrize("kw,want", [
     (dict(T=-1), ESHAPE), (dict(T=1 << 31), ESHAPE), (dict(L=0), ESHAPE), (dict(L=1025), ESHAPE),
-    (dict(R=0), ESHAPE), (dict(R=257), ESHAPE), (dict(K=0), ESHAPE), (dict(N=0), ESHAPE),
+    (dict(R=0), ESHAPE), (dict(R=257), ESHAPE), (dict(K=7), ESHAPE), (dict(N=7), ESHAPE),
     (dict(ldx=63), ESHAPE), (dict(ldy=95), ESHAPE), (dict(ldb=95, Y=ODD), ESHAPE),
     (dict(ldx=1 << 40), ESHAPE), (dict(L=1024, R=256, K=1 << 30, ldx=1 << 30), ESHAPE),
     (dict(T=(1 << 31) - 1, N=1 << 20, ldy=1 << 20, ldb=1 << 20), ESHAPE),
@@ -186,15 +186,21 @@ def test_lora_bwd_refusals(lib, kw, want):
 
 def test_lora_workspace_sizes(lib):
     f, b = lib.moegg_lora_workspace_bytes, lib.moegg_lora_bwd_workspace_bytes
-    # 64 rows over 32 adapters: 36 tiles, 8 workgroups a tile over 4096 columns
-    assert f(64, 32, 16, 4096, 4096) == 8 * 64 * 16 * 4
-    # many tiles: one sum each
-    assert f(8192, 8, 64, 4096, 4096) == 8192 * 64 * 4
+
+    def area(n):                             # n fp32 and a piece of 8 behind them
+        return (n * 4 + 32 + 255) // 256 * 256
+
+    # 64 rows over 32 adapters: 36 tiles of 16 rows, 8 workgroups a tile
+    assert f(64, 32, 16, 4096, 4096) == area(8 * 64 * 16)
+    # 136 tiles of 64 rows: two workgroups a tile
+    assert f(8192, 8, 64, 4096, 4096) == area(2 * 8192 * 64)
     assert f(0, 4, 16, 64, 64) == 0 and b(0, 4, 16, 64, 64) == 0
-    assert f(-1, 4, 16, 64, 64) == 0 and b(10, 4, 300, 64, 64) == 0
+    assert f(-1, 4, 16, 64, 64) == 0 and b(10, 4, 300, 64, 64) == 0 and f(10, 4, 16, 7, 64) == 0
     # dh alone up to one chunk of rows, then at most 2 T / chunk partial sums
-    assert b(512, 1, 16, 64, 96) == 512 * 16 * 4
-    assert b(4096, 4, 32, 4096, 4096) == 4096 * 32 * 4 + 16 * 32 * 8192 * 4
+    assert b(128, 1, 16, 64, 96) == area(128 * 16)
+    chunk = 4096 * 64 // 384 // 32 * 32 + 32
+    assert b(4096, 4, 32, 4096, 4096) == (area(4 * 4096 * 32)
+                                          + 2 * 4096 // chunk * 32 * 8192 * 4)
     # a size just below what is needed
     need = f(64, 32, 16, 4096, 4096)
     assert lora(lib, T=64, L=32, K=4096, N=4096, ldx=4096, ldy=4096, ldb=4096,

@@ -744,14 +744,15 @@ static moegg_status check_lora_sizes(int64_t T, int32_t L, int32_t R, int32_t K,
 {
     constexpr int64_t kMax = (int64_t)1 << 39;  // elements: 2^40 bytes of 16 bits
     if (T < 0 || T > INT32_MAX || L < 1 || L > MOEGG_MAX_EXPERTS || R < 1 ||
-        R > MOEGG_MAX_LORA_RANK || K < 1 || N < 1 || K > (1 << 30) || N > (1 << 30))
+        R > MOEGG_MAX_LORA_RANK || K < 8 || N < 8 || K > (1 << 30) || N > (1 << 30))
         return MOEGG_ESHAPE;
     const int64_t wide = K > N ? K : N;
     if ((int64_t)L * R > kMax / wide || (T > 0 && wide > kMax / T))
         return MOEGG_ESHAPE;
-    const int64_t cols = wide / 128 + 1, tiles = (T / 32 + 1 + L) * cols;
-    const int64_t items = (L + T / 512) * (2 * cols) * ((R + 15) / 16);
-    if (tiles > INT32_MAX || items > INT32_MAX)
+    const int64_t cols = wide / 128 + 1;
+    const int64_t shrink = (T / 16 + 1 + L) * 16, expand = (T / 64 + 1 + L) * cols;
+    const int64_t grad = (L + T / moegg::lora_chunk(T, R, K, N)) * (2 * cols) * ((R + 15) / 16);
+    if (shrink > INT32_MAX || expand > INT32_MAX || grad > INT32_MAX)
         return MOEGG_ESHAPE;
     return MOEGG_OK;
 }
@@ -764,8 +765,9 @@ static bool stride_ok(int64_t ld, int64_t n, int64_t T)
 
 static size_t lora_h_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
 {
-    const size_t b = (size_t)moegg::lora_splits(T, L, C) * (size_t)T * (size_t)R * sizeof(float);
-    return (b + 255) / 256 * 256;
+    // 32 bytes behind the last row: it is read in pieces of 8 values
+    const size_t b = (size_t)moegg::lora_splits(T, L, R, C) * (size_t)T * (size_t)R * sizeof(float);
+    return T > 0 ? (b + 32 + 255) / 256 * 256 : 0;
 }
 
 size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
@@ -783,7 +785,7 @@ size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, in
         return 0;
     // dh, then the chunks' partial sums: adapters of more than one chunk hold
     // fewer than 2 T / chunk of them together
-    const int64_t chunk = moegg::lora_chunk(num_rows);
+    const int64_t chunk = moegg::lora_chunk(num_rows, R, K, N);
     const size_t parts = num_rows > chunk ? (size_t)(2 * num_rows / chunk) : 0;
     return lora_h_bytes(num_rows, num_adapters, R, N) +
            parts * (size_t)R * ((size_t)K + (size_t)N) * sizeof(float);
@@ -832,9 +834,9 @@ moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const voi
     p.T = num_rows;
     p.L = num_adapters;
     p.R = R;
-    p.splits = moegg::lora_splits(num_rows, num_adapters, K);
+    p.splits = moegg::lora_splits(num_rows, num_adapters, R, K);
     p.split_stride = num_rows * R;
-    p.h = H && p.splits == 1 ? H : static_cast<float *>(workspace);
+    p.h = static_cast<float *>(workspace);
     p.in = static_cast<const uint16_t *>(X);
     p.w = static_cast<const uint16_t *>(A);
     p.ld_in = ldx;
@@ -848,7 +850,7 @@ moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const voi
     p.out = static_cast<uint16_t *>(Y);
     p.ld_base = ld_base;
     p.ld_out = ldy;
-    p.h_out = p.splits > 1 ? H : nullptr;
+    p.h_out = H;
     return from_hip(
         moegg::lora_expand_launch(p, dtype, false, static_cast<hipStream_t>(stream)));
 }
@@ -906,7 +908,7 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     p.T = num_rows;
     p.L = num_adapters;
     p.R = R;
-    p.splits = moegg::lora_splits(num_rows, num_adapters, N);
+    p.splits = moegg::lora_splits(num_rows, num_adapters, R, N);
     p.split_stride = num_rows * R;
     p.h = static_cast<float *>(workspace);
     p.scale_shrink = true;
@@ -943,7 +945,7 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     g.K = K;
     g.N = N;
     g.splits = p.splits;
-    g.chunk = moegg::lora_chunk(num_rows);
+    g.chunk = moegg::lora_chunk(num_rows, R, K, N);
     g.col_tiles_a = (K + 127) / 128;
     g.col_tiles_b = (N + 127) / 128;
     g.fp32_out = flags & MOEGG_LORA_FP32_GRAD;

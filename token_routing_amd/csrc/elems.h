@@ -81,7 +81,7 @@ load16(const typename Elem<DT>::store_t *row, int col, int n)
     return v;
 }
 
-template <int DT>
+template <int DT, bool STREAM = true>
 __device__ __forceinline__ void store16(typename Elem<DT>::store_t *row, int col, int n,
                                         const float *f)
 {
@@ -92,7 +92,10 @@ __device__ __forceinline__ void store16(typename Elem<DT>::store_t *row, int col
     for (int i = 0; i < P; ++i)
         v[i] = Elem<DT>::narrow(f[i]);
     if (col + P <= n) {
-        __builtin_nontemporal_store(v, reinterpret_cast<vec_t *>(row + col));
+        if constexpr (STREAM)
+            __builtin_nontemporal_store(v, reinterpret_cast<vec_t *>(row + col));
+        else
+            *reinterpret_cast<vec_t *>(row + col) = v;
         return;
     }
 #pragma unroll

@@ -174,42 +174,41 @@ __device__ __forceinline__ f32x4_t mfma(const u32x4_t &a, const u32x4_t &b, cons
                                                       __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// Elements [col, col + 8) of a 16-bit row of n elements (0 past n; row may be null).
-__device__ __forceinline__ u32x4_t load8(const uint16_t *row, int col, int n)
+// 8 elements that are known to lie inside their array.
+__device__ __forceinline__ u32x4_t load8_in(const uint16_t *p)
 {
     typedef Pack16<kBf16>::vec_t vec_t;
-    if (!row)
-        return u32x4_t{};
-    const vec_t v = load16<kBf16>(row, col, n);
-    return __builtin_bit_cast(u32x4_t, v);
+    return __builtin_bit_cast(u32x4_t, *reinterpret_cast<const vec_t *>(p));
 }
 
-// Elements [col, col + W) as packed pairs; those at or past n read as 0.
-template <int W>
-__device__ __forceinline__ void load_pairs(uint32_t (&d)[W < 2 ? 1 : W / 2], const uint16_t *row,
-                                           int col, int n, bool on)
+// Elements [at, at + 8) of an array of n >= 8 elements, zero past its end:
+// the load is moved back inside and its elements shifted down.
+__device__ __forceinline__ u32x4_t load8_end(const uint16_t *p, int64_t at, int64_t n)
 {
-    typedef uint16_t vec_t __attribute__((ext_vector_type(W), aligned(2)));
-    constexpr int D = W < 2 ? 1 : W / 2;
-#pragma unroll
-    for (int i = 0; i < D; ++i)
-        d[i] = 0;
-    if (!on || col >= n)
-        return;
+    typedef unsigned long long u64x2_t __attribute__((ext_vector_type(2)));
+    const int64_t start = min(at, n - 8);
+    const u64x2_t v = __builtin_bit_cast(u64x2_t, load8_in(p + start));
+    const int64_t by = at - start;
+    const int s = ((int)by & 3) * 16;
+    const unsigned long long low = by >= 4 ? v[1] : v[0], high = by >= 4 ? 0 : v[1];
+    u64x2_t r;
+    r[0] = by >= 8 ? 0 : low >> s | (s ? high << (64 - s) : 0);
+    r[1] = by >= 8 ? 0 : high >> s;
+    return __builtin_bit_cast(u32x4_t, r);
+}
+
+// W elements that are known to lie inside their array, as packed pairs.
+template <int W>
+__device__ __forceinline__ void load_pairs(uint32_t (&d)[W < 2 ? 1 : W / 2], const uint16_t *p)
+{
+    typedef uint16_t vec_t __attribute__((ext_vector_type(W < 2 ? 2 : W), aligned(2)));
     if constexpr (W == 1) {
-        d[0] = row[col];
+        d[0] = *p;
     } else {
-        if (col + W <= n) {
-            const vec_t v = *reinterpret_cast<const vec_t *>(row + col);
+        const vec_t v = *reinterpret_cast<const vec_t *>(p);
 #pragma unroll
-            for (int i = 0; i < D; ++i)
-                d[i] = (uint32_t)v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-            if (col + i < n)
-                d[i / 2] |= (uint32_t)row[col + i] << (16 * (i & 1));
+        for (int i = 0; i < W / 2; ++i)
+            d[i] = (uint32_t)v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
     }
 }
 
@@ -264,95 +263,161 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4_t &hi, u32x4_t
     }
 }
 
-// h[p][col .. col + 8), the splits' partial sums added in order (0 past n).
+// h[p][col .. col + 8), the splits' partial sums added in order, 0 from n on.
+// May read up to 8 values past the row (h has that much room behind it).
 __device__ __forceinline__ void load_h(float (&v)[8], const float *h, int64_t p, int R, int col,
-                                       int n, int splits, int64_t split_stride, bool on)
+                                       int n, int splits, int64_t split_stride)
 {
+    const float *q = h + p * R + (col < n ? col : 0);
+    f32x4_t a = *reinterpret_cast<const f32x4u_t *>(q);
+    f32x4_t b = *reinterpret_cast<const f32x4u_t *>(q + 4);
+    for (int s = 1; s < splits; ++s) {
+        q += split_stride;
+        a += *reinterpret_cast<const f32x4u_t *>(q);
+        b += *reinterpret_cast<const f32x4u_t *>(q + 4);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = 0.0f;
-    if (!on || col >= n)
-        return;
-    const float *q = h + p * R + col;
-    for (int s = 0; s < splits; ++s, q += split_stride) {
-        if (col + 8 <= n) {
-            const f32x4u_t a = *reinterpret_cast<const f32x4u_t *>(q);
-            const f32x4u_t b = *reinterpret_cast<const f32x4u_t *>(q + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] += a[i];
-                v[4 + i] += b[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < n)
-                    v[i] += q[i];
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[i] = col + i < n ? a[i] : 0.0f;
+        v[4 + i] = col + 4 + i < n ? b[i] : 0.0f;
     }
 }
 
 // ---------------------------------------------------------------- shrink
 
-// h[p, r] = factor * sum_c in[src(p), c] * w(r, c) for a tile of 16 rows:
+// h[p, r] = factor * sum_c in[src(p), c] * w(r, c) for a tile of RT * 16 rows:
 // w(r, c) = W[r][c] (W [R, C], forward) or W[c][r] (W [C, R], TR).  A
 // workgroup of 8 waves takes 1 / splits of the reduction, each wave an equal
-// run of it, and adds the waves' sums through LDS in wave order.  Unsplit, the
-// sums go to H, else to the split's own copy.  RF: 16-row blocks of ranks.
+// run of it, and adds the waves' sums through LDS in wave order.  Each split
+// stores a copy of its own.  RF: 16-row blocks of ranks.
+//
+// A fragment load touches 16 rows at a time, one cache line each, so the lines
+// looked up are the bound before bytes are: RT > 1 uses the weights' fragments
+// for several blocks of rows.
+//
+// The loads of U whole 32-column steps are issued together, without branches:
+// lanes past the tile's rows load its first row again and lanes past the rank
+// another row of weights, since a matrix instruction keeps them in outputs of
+// their own, which are not stored.  EDGE: columns that are no whole steps, or
+// ranks that are no whole pieces of 4 or of a lane (TR).  Code is kept short
+// on purpose: a wave runs most of it once, and fetching it cost more than the
+// loads when every guarded element had its own branch.
 constexpr int kShrinkWaves = 8;
 
-template <int DT, bool TR, int RF>
+template <int DT, bool TR, int RF, int RT, bool EDGE>
 __global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams a)
 {
-    constexpr int W = RF;  // ranks a lane holds with TR: r = m * RF + j
-    __shared__ f32x4_t s_acc[kShrinkWaves / 2][RF][kWave];
+    // With TR a lane holds ranks m * RF + j, one piece of a row of weights;
+    // with EDGE ranks f * 16 + m, one element of a row at a time.
+    constexpr bool PIECES = TR && !EDGE;
+    constexpr int W = PIECES ? RF : 1;
+    constexpr int D = W < 2 ? 1 : W / 2;
+    constexpr int Q = TR ? (PIECES ? 1 : RF) : 1;  // loads of a row of weights (TR)
+    constexpr int U = RF <= 2 ? 4 : RF <= 8 ? 2 : 1;
+    __shared__ f32x4_t s_acc[kShrinkWaves / 2][RT * RF][kWave];
     check_sizes(a.m_sizes, a.ranks, a.L, a.T, a.R, a.err);
     const int split = blockIdx.x % a.splits;
     Tile tile;
-    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / a.splits, kShrinkRows, 0, false,
-                   tile))
+    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / a.splits, RT * 16, 0, false, tile))
         return;
     const int rank = rank_of(a.ranks, tile.a, a.R);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
     const int m = lane & 15, g = lane >> 4;
 
-    const uint16_t *row = nullptr;
-    if (m < tile.rows) {
-        const int64_t r = source_row(a, tile.p0 + m);
-        row = r < 0 ? nullptr : a.in + r * a.ld_in;
+    const uint16_t *row[RT];
+    bool bad_row[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int64_t src = source_row(a, tile.p0 + (t * 16 + m < tile.rows ? t * 16 + m : 0));
+        bad_row[t] = src < 0;
+        row[t] = a.in + (src < 0 ? 0 : src) * a.ld_in;
     }
     const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
 
-    f32x4_t acc[RF];
+    f32x4_t acc[RT][RF];
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
-        acc[f] = f32x4_t{};
-    const int steps = (a.C + 31) / 32;
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+            acc[t][f] = f32x4_t{};
+    const int whole = a.C / 32, steps = EDGE ? (a.C + 31) / 32 : whole;
     const int parts = a.splits * kShrinkWaves;
     const int part = split * kShrinkWaves + wave;
     const int s0 = (int)((int64_t)steps * part / parts);
     const int s1 = (int)((int64_t)steps * (part + 1) / parts);
+    const int full = EDGE ? min(s1, whole) : s1;
     if (rank > 0) {
-#pragma unroll 4
-        for (int s = s0; s < s1; ++s) {
-            const int c = s * 32 + g * 8;
-            const u32x4_t x = load8(row, c, a.C);
-            if constexpr (!TR) {
+        const uint16_t *wrow[TR ? Q : RF];
+#pragma unroll
+        for (int f = 0; f < (TR ? Q : RF); ++f) {
+            if constexpr (PIECES)
+                wrow[f] = w + min(m * W, a.R - W);
+            else if constexpr (TR)
+                wrow[f] = w + min(f * 16 + m, a.R - 1);
+            else
+                wrow[f] = w + (int64_t)min(f * 16 + m, rank - 1) * a.C;
+        }
+        for (int s = s0; s < full; s += U) {
+            u32x4_t x[U][RT], v[TR ? 1 : U][TR ? 1 : RF];
+            uint32_t q[TR ? U : 1][Q][8][D];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = min(s + u, full - 1) * 32 + g * 8;
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    x[u][t] = load8_in(row[t] + c);
+                if constexpr (!TR) {
+#pragma unroll
+                    for (int f = 0; f < RF; ++f)
+                        v[u][f] = load8_in(wrow[f] + c);
+                } else {
+#pragma unroll
+                    for (int f = 0; f < Q; ++f)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            load_pairs<W>(q[u][f][e], wrow[f] + (int64_t)(c + e) * a.R);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (s + u < full) {
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) {
+                        const u32x4_t b = TR ? column<W>(q[TR ? u : 0][PIECES ? 0 : TR ? f : 0],
+                                                         PIECES ? f : 0)
+                                             : v[TR ? 0 : u][TR ? 0 : f];
+#pragma unroll
+                        for (int t = 0; t < RT; ++t)
+                            acc[t][f] = mfma<DT>(b, x[u][t], acc[t][f]);
+                    }
+                }
+        }
+        if constexpr (EDGE) {
+            if (s1 > whole && s0 < s1) {  // the last, partial step
+                const int c = whole * 32 + g * 8;
+                u32x4_t x[RT];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    x[t] = load8_end(row[t], c, a.C);
 #pragma unroll
                 for (int f = 0; f < RF; ++f) {
-                    const int r = f * 16 + m;
-                    const u32x4_t v = load8(r < rank ? w + (int64_t)r * a.C : nullptr, c, a.C);
-                    acc[f] = mfma<DT>(v, x, acc[f]);
+                    u32x4_t b;
+                    if constexpr (TR) {
+                        uint32_t e8[8][1];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            load_pairs<1>(e8[e], wrow[f] + (int64_t)min(c + e, a.C - 1) * a.R);
+                            e8[e][0] = c + e < a.C ? e8[e][0] : 0;
+                        }
+                        b = column<1>(e8, 0);
+                    } else {
+                        b = load8_end(wrow[f], c, a.C);
+                    }
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        acc[t][f] = mfma<DT>(b, x[t], acc[t][f]);
                 }
-            } else {
-                uint32_t v[8][W < 2 ? 1 : W / 2];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    load_pairs<W>(v[e], w + (int64_t)(c + e) * a.R, m * W, rank, c + e < a.C);
-#pragma unroll
-                for (int f = 0; f < RF; ++f)
-                    acc[f] = mfma<DT>(column<W>(v, f), x, acc[f]);
             }
         }
     }
@@ -360,164 +425,299 @@ __global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams 
     for (int half = kShrinkWaves / 2; half > 0; half >>= 1) {
         if (wave >= half && wave < 2 * half)
 #pragma unroll
-            for (int f = 0; f < RF; ++f)
-                s_acc[wave - half][f][lane] = acc[f];
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int f = 0; f < RF; ++f)
+                    s_acc[wave - half][t * RF + f][lane] = acc[t][f];
         __syncthreads();
         if (wave < half)
 #pragma unroll
-            for (int f = 0; f < RF; ++f)
-                acc[f] += s_acc[wave][f][lane];
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int f = 0; f < RF; ++f)
+                    acc[t][f] += s_acc[wave][t * RF + f][lane];
         __syncthreads();
     }
-    if (wave != 0 || m >= tile.rows)
+    if (wave != 0)
         return;
     const float factor = a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
-    float *const h = a.h + split * a.split_stride + (int64_t)(tile.p0 + m) * a.R;
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
+    for (int t = 0; t < RT; ++t) {
+        if (t * 16 + m >= tile.rows)
+            continue;
+        float *const h = a.h + split * a.split_stride + (int64_t)(tile.p0 + t * 16 + m) * a.R;
+        // A lane's outputs: 4 ranks a block (f * 16 + 4 g + i), or with PIECES
+        // 4 * RF ranks in a row ((4 g + i) * RF + f).
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = TR ? (4 * g + i) * RF + f : f * 16 + 4 * g + i;
-            if (r < a.R)
-                h[r] = factor * acc[f][i];
+        for (int k = 0; k < RF; ++k) {
+            const int r = PIECES ? 4 * g * RF + 4 * k : k * 16 + 4 * g;
+            f32x4_t v;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float d = PIECES ? acc[t][(4 * k + i) % RF][(4 * k + i) / RF] : acc[t][k][i];
+                v[i] = r + i < rank && !bad_row[t] ? factor * d : 0.0f;
+            }
+            if constexpr (!EDGE) {
+                if (r < a.R)
+                    *reinterpret_cast<f32x4u_t *>(h + r) = v;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + i < a.R)
+                        h[r + i] = v[i];
+            }
         }
+    }
 }
 
 // ---------------------------------------------------------------- expand
 
 // out[src(p), c] = base[src(p), c] + factor * sum_r h[p, r] * w(r, c), w(r, c)
-// = W[c][r] (W [C, R], forward) or W[r][c] (W [R, C], TR).  A wave takes RT *
-// 16 rows of one adapter and F * 16 columns; its weights' fragments are loaded
-// once for all of its rows.  SMALL: ranks up to 16, both parts of h in one
-// instruction.
-template <int DT, bool TR, bool SMALL>
-__global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int col_tiles)
+// = W[c][r] (W [C, R], forward) or W[r][c] (W [R, C], TR).
+//
+// A workgroup takes up to 64 rows of one adapter and a run of columns, its
+// waves 64 columns each at a time.  h is split into its two parts once and
+// kept in LDS as fragments (NS steps of 32 ranks).  A wave's pass: the
+// weights' fragments (each used for all rows), the matrix instructions, and
+// the sums through a strip of LDS into row order, so that base is read and
+// out written in whole 128-byte lines: straight from the accumulators' layout
+// every 16 bytes of a line would be looked up apart, which took 1.7 times as
+// long.  Base is loaded one pass ahead.  SMALL: ranks up to 16, both parts of
+// h in one instruction.  EDGE: columns that are no whole passes (the last one
+// goes by single elements, a row at a time) or, forward, ranks that are no
+// whole pieces of 8.
+template <int DT, bool TR, int NS, bool SMALL, bool EDGE>
+__global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int groups, int group_cols)
 {
-    constexpr int F = TR ? 8 : 4;
-    constexpr int RT = TR ? kExpandRowsT / 16 : kExpandRows / 16;
-    constexpr int kRows = RT * 16;
+    constexpr int F = 4;
     constexpr int kCols = F * 16;
-    constexpr int kStep = SMALL ? 16 : 32;
-    check_sizes(a.m_sizes, a.ranks, a.L, a.T, a.R, a.err);
+    constexpr int RT = kExpandRows / 16;
+    constexpr int kPad = kCols + 4;
+    __shared__ u32x4_t s_h[NS][RT][SMALL ? 1 : 2][kWave];
+    __shared__ __attribute__((aligned(16))) float s_out[4][16][kPad];
+    __shared__ int s_src[kExpandRows];
+    __shared__ float s_factor[kExpandRows];
     Tile tile;
-    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / col_tiles, kRows, 0, false, tile))
+    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / groups, kExpandRows, 0, false,
+                   tile))
         return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
     const int m = lane & 15, g = lane >> 4;
-    const int col_tile = blockIdx.x % col_tiles;
-    const int c0 = (col_tile * 4 + wave) * kCols;
+    const int group = blockIdx.x % groups;
     const int rank = rank_of(a.ranks, tile.a, a.R);
     const int rg = SMALL ? (g & 1) * 8 : g * 8;  // this lane's ranks of a step
+    const int blocks = (tile.rows + 15) / 16;
 
-    // The summed h for the caller, by the first column tile.
-    if (a.h_out && col_tile == 0)
+    // In row order a lane holds 8 columns of rows lane / 8 and lane / 8 + 8 of
+    // a block.  A bad gather entry (shrink reports it) has no row.
+    const int row_lane = lane >> 3, col_lane = (lane & 7) * 8;
+    int src[RT][2];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = t * 16 + i * 8 + row_lane;
+            const int p = tile.p0 + min(r, tile.rows - 1);
+            const int x = a.gather ? a.gather[p] : p;
+            src[t][i] = r < tile.rows && x >= 0 && x < a.T ? x : -1;
+        }
+    const int c_end = min(a.C, (group + 1) * group_cols);
+    const int c_begin = group * group_cols + wave * kCols;
+    u32x4_t old[RT][2];
+    auto load_base = [&](int t, int c0) {
+        if (c0 < c_end && (!EDGE || c0 + kCols <= a.C) && t < blocks)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                old[t][i] = load8_in(a.base + (int64_t)max(src[t][i], 0) * a.ld_base + c0 + col_lane);
+    };
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        load_base(t, c_begin);
+
+    // The summed h for the caller, by the first column group.
+    if (a.h_out && group == 0)
         for (int i = threadIdx.x; i < tile.rows * a.R; i += 256) {
             const float *q = a.h + (int64_t)tile.p0 * a.R + i;
-            float v = 0.0f;
-            for (int s = 0; s < a.splits; ++s, q += a.split_stride)
+            float v = *q;
+            for (int s = 1; s < a.splits; ++s) {
+                q += a.split_stride;
                 v += *q;
+            }
             a.h_out[(int64_t)tile.p0 * a.R + i] = v;
         }
-    if (c0 >= a.C || (rank == 0 && a.base == a.out))
+    if (rank == 0 && a.base == a.out)
         return;
-    const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
-
-    f32x4_t acc[RT][F];
-    float fit[RT];
+    if (wave < blocks) {
+        const int t = wave * 16 + m;
+        const int p = tile.p0 + min(t, tile.rows - 1);
+        float factor = !a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
+        float v[NS][8];
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        fit[t] = 1.0f;
+        for (int s = 0; s < NS; ++s)
+            load_h(v[s], a.h, p, a.R, s * 32 + rg, rank, a.splits, a.split_stride);
+        if constexpr (DT == kFp16) {
+            float top = 0.0f;
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-            acc[t][f] = f32x4_t{};
-    }
-    if constexpr (DT == kFp16) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            float top = 0.0f, v[8];
-            for (int r = 0; r < rank; r += kStep) {
-                load_h(v, a.h, tile.p0 + t * 16 + m, a.R, r + rg, rank, a.splits, a.split_stride,
-                       t * 16 + m < tile.rows);
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    top = fmaxf(top, fabsf(v[i]));
-            }
+                    top = fmaxf(top, fabsf(v[s][i]));
             top = fmaxf(top, __shfl_xor(top, 16, kWave));
             top = fmaxf(top, __shfl_xor(top, 32, kWave));
-            fit[t] = fit_scale(top);
+            const float fit = fit_scale(top);
+            factor *= inverse_scale(fit);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[s][i] *= fit;
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            u32x4_t hi, lo;
+            split8<DT>(v[s], hi, lo);
+            if constexpr (SMALL) {
+                s_h[s][wave][0][lane] = g < 2 ? hi : lo;
+            } else {
+                s_h[s][wave][0][lane] = hi;
+                s_h[s][wave][SMALL ? 0 : 1][lane] = lo;
+            }
+        }
+        if (g == 0)
+            s_factor[t] = factor;
+        if constexpr (EDGE) {
+            const int x = a.gather ? a.gather[p] : p;
+            if (g == 0)
+                s_src[t] = t < tile.rows && x >= 0 && x < a.T ? x : -1;
         }
     }
-    for (int r0 = 0; r0 < rank; r0 += kStep) {
-        u32x4_t wf[F];
-        if constexpr (TR) {
-            uint32_t v[8][4];
-            const int c = c0 + ((m & 3) * 4 + (m >> 2)) * 8;
+    __syncthreads();
+
+    const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
+    for (int c0 = c_begin; c0 < c_end; c0 += 4 * kCols) {
+        const bool inside = !EDGE || c0 + kCols <= a.C;
+        f32x4_t acc[RT][F];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                load_pairs<8>(v[e], w + (int64_t)(r0 + rg + e) * a.C, c, a.C, r0 + rg + e < rank);
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
             for (int f = 0; f < F; ++f)
-                wf[f] = column<8>(v, f);
-        } else {
+                acc[t][f] = f32x4_t{};
 #pragma unroll
-            for (int f = 0; f < F; ++f) {
-                const int c = c0 + (f >> 1) * 32 + (m >> 2) * 8 + (f & 1) * 4 + (m & 3);
-                wf[f] = load8(c < a.C ? w + (int64_t)c * a.R : nullptr, r0 + rg, rank);
+        for (int s = 0; s < NS; ++s) {
+            if (s * 32 >= rank)
+                break;
+            const int r0 = s * 32 + rg;
+            u32x4_t wf[F];
+            if constexpr (TR) {
+                // 8 rows of 4 columns; the last lanes' are moved inside the row.
+                const int c = EDGE ? min(c0 + m * 4, a.C - 4) : c0 + m * 4;
+                uint32_t v[8][2];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    load_pairs<4>(v[e], w + (int64_t)min(r0 + e, rank - 1) * a.C + c);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        v[e][i] = r0 + e < rank ? v[e][i] : 0;
+                }
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    wf[f] = column<4>(v, f);
+            } else {
+                u32x4_t mask;  // ranks below the rank; others may hold anything
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mask[i] = r0 + 2 * i + 1 < rank ? ~0u : r0 + 2 * i < rank ? 0xffffu : 0u;
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const int c = c0 + f * 16 + m;
+                    const int64_t at =
+                        (int64_t)(EDGE ? min(c, a.C - 1) : c) * a.R + (r0 < rank ? r0 : 0);
+                    wf[f] = EDGE ? load8_end(w, at, (int64_t)a.C * a.R) : load8_in(w + at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        wf[f][i] &= mask[i];
+                }
             }
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                if (t < blocks) {
+                    const u32x4_t hi = s_h[s][t][0][lane];
+#pragma unroll
+                    for (int f = 0; f < F; ++f)
+                        acc[t][f] = mfma<DT>(wf[f], hi, acc[t][f]);
+                    if constexpr (!SMALL) {
+                        const u32x4_t lo = s_h[s][t][SMALL ? 0 : 1][lane];
+#pragma unroll
+                        for (int f = 0; f < F; ++f)
+                            acc[t][f] = mfma<DT>(wf[f], lo, acc[t][f]);
+                    }
+                }
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            if (t * 16 >= tile.rows)
-                break;
-            float v[8];
-            u32x4_t hi, lo;
-            load_h(v, a.h, tile.p0 + t * 16 + m, a.R, r0 + rg, rank, a.splits, a.split_stride,
-                   t * 16 + m < tile.rows);
-            if constexpr (DT == kFp16)
+            if (t >= blocks)
+                continue;
+            // A lane holds row m, columns f * 16 + 4 g + i (TR: (4 g + i) * 4 + f).
+            if (!TR || inside) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] *= fit[t];
-            split8<DT>(v, hi, lo);
-            if constexpr (SMALL) {
-                const u32x4_t both = g < 2 ? hi : lo;
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-                    acc[t][f] = mfma<DT>(wf[f], both, acc[t][f]);
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4_t v = TR ? f32x4_t{acc[t][0][i], acc[t][1][i], acc[t][2][i],
+                                                   acc[t][3][i]}
+                                         : acc[t][i];
+                    *reinterpret_cast<f32x4_t *>(
+                        &s_out[wave][m][TR ? (4 * g + i) * 4 : i * 16 + 4 * g]) = v;
+                }
             } else {
 #pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    acc[t][f] = mfma<DT>(wf[f], hi, acc[t][f]);
-                    acc[t][f] = mfma<DT>(wf[f], lo, acc[t][f]);
+                for (int i = 0; i < 4; ++i) {
+                    const int c = min(c0 + (4 * g + i) * 4, a.C - 4) - c0;
+#pragma unroll
+                    for (int f = 0; f < F; ++f)
+                        if (c + f >= 0)
+                            s_out[wave][m][c + f] = acc[t][f][i];
                 }
             }
-        }
-    }
-    const float factor = !a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (inside) {
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        if (t * 16 + m >= tile.rows)
-            continue;
-        const int64_t row = source_row(a, tile.p0 + t * 16 + m);
-        if (row < 0)
-            continue;
-        const uint16_t *const base = a.base + row * a.ld_base;
-        uint16_t *const out = a.out + row * a.ld_out;
-        const float k = DT == kFp16 ? factor * inverse_scale(fit[t]) : factor;
-        constexpr int kPieces = TR ? 4 : 2;
+                for (int i = 0; i < 2; ++i) {
+                    const int r = i * 8 + row_lane;
+                    const f32x4_t *const d =
+                        reinterpret_cast<const f32x4_t *>(&s_out[wave][r][col_lane]);
+                    const f32x4_t d0 = d[0], d1 = d[1];
+                    const float k = s_factor[t * 16 + r];
+                    float y[8];
+                    widen_all<DT>(y, __builtin_bit_cast(typename Pack16<DT>::vec_t, old[t][i]));
+                    typename Pack16<DT>::vec_t out;
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            const int c = TR ? c0 + (q * 4 + g) * 8 : c0 + q * 32 + g * 8;
-            float y[8];
-            if (c >= a.C)
-                continue;
-            widen_all<DT>(y, load16<DT>(base, c, a.C));
+                    for (int e = 0; e < 4; ++e) {
+                        y[e] += k * d0[e];
+                        y[4 + e] += k * d1[e];
+                    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = TR ? acc[t][TR ? i : 0][q] : acc[t][TR ? 0 : 2 * q + (i >> 2)][i & 3];
-                y[i] += k * d;
+                    for (int e = 0; e < 8; ++e)
+                        out[e] = Elem<DT>::narrow(y[e]);
+                    if (src[t][i] >= 0)
+                        __builtin_nontemporal_store(
+                            out, reinterpret_cast<typename Pack16<DT>::vec_t *>(
+                                     a.out + (int64_t)src[t][i] * a.ld_out + c0 + col_lane));
+                }
+                load_base(t, c0 + 4 * kCols);
+            } else {
+                for (int r = 0; r < min(16, tile.rows - t * 16); ++r) {
+                    const int64_t x = s_src[t * 16 + r];
+                    const int c = c0 + lane;
+                    if (x >= 0 && c < a.C) {
+                        const float y = Elem<DT>::widen(a.base[x * a.ld_base + c]) +
+                                        s_factor[t * 16 + r] * s_out[wave][r][lane];
+                        a.out[x * a.ld_out + c] = Elem<DT>::narrow(y);
+                    }
+                }
             }
-            store16<DT>(out, c, a.C, y);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
     }
 }
@@ -528,13 +728,21 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int col_tiles
 // adapter's rows: dA (big = x, small = dh; stored [r][c]) in the first
 // col_tiles_a column tiles, dB (big = dy, small = h; stored [c][r]) in the
 // rest.  A workgroup of 4 waves takes 128 columns and RG * 16 ranks; the waves
-// take turns at 32-row steps and add their sums through LDS.  A segment of
-// one chunk is finished here, the others leave fp32 partials.
+// take turns at 32-row steps, leave their sums in LDS, and all of them add and
+// store.  A segment of one chunk is finished here, the others leave fp32
+// partials, cut evenly and in whole steps.
+//
+// A step is 8 rows of 16 bytes a lane, issued together; the rows' numbers are
+// loaded a step ahead.  Rows past the chunk's end repeat its last row and are
+// set to zero.  Lanes past the last column load the row's last 8 elements and
+// store only what is their own.
 template <int DT, int RG>
 __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
 {
-    __shared__ f32x4_t s_acc[2][8 * RG][kWave];
-    const int rank_tiles = (a.R + RG * 16 - 1) / (RG * 16);
+    constexpr int kRanks = RG * 16;
+    constexpr int kPad = 128 + 4;
+    __shared__ __attribute__((aligned(16))) float s_sum[4][kRanks][kPad];
+    const int rank_tiles = (a.R + kRanks - 1) / kRanks;
     const int tiles = a.col_tiles_a + a.col_tiles_b;
     int b = blockIdx.x;
     const int rt = b % rank_tiles;
@@ -554,20 +762,13 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
     const int m = lane & 15, g = lane >> 4;
-    const int c_load = ct * 128 + ((m & 3) * 4 + (m >> 2)) * 8;
-    const int r0 = rt * RG * 16 + m;
+    const int r0 = rt * kRanks + m;
 
-    auto load_small = [&](float (&v)[8], int p, int end, int r) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = 0.0f;
-            if (r < rank && p + e < end) {
-                const float *q = small + (int64_t)(p + e) * a.R + r;
-                for (int s = 0; s < splits; ++s, q += a.split_stride)
-                    v[e] += *q;
-            }
-        }
-    };
+    const int chunks = tile.m > a.chunk ? (tile.m - 1) / a.chunk + 1 : 1;
+    const int per = chunks > 1 ? ((tile.m + chunks - 1) / chunks + 31) / 32 * 32 : a.chunk;
+    const int first = tile.p0 - tile.index * a.chunk;  // the segment's first position
+    const int begin = first + min(tile.index * per, tile.m);
+    const int end = first + min((tile.index + 1) * per, tile.m);
 
     f32x4_t acc[8][RG];
     float fit[RG];
@@ -578,113 +779,148 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
         for (int f = 0; f < 8; ++f)
             acc[f][q] = f32x4_t{};
     }
-    const int end = tile.p0 + max(tile.rows, 0);
-    if constexpr (DT == kFp16) {
-        float top[RG] = {};
-        for (int p = tile.p0 + wave * 32; p < end; p += 128)
-#pragma unroll
-            for (int q = 0; q < RG; ++q) {
-                float v[8];
-                load_small(v, p + g * 8, end, r0 + q * 16);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    top[q] = fmaxf(top[q], fabsf(v[e]));
-            }
-#pragma unroll
-        for (int q = 0; q < RG; ++q) {
-            top[q] = fmaxf(top[q], __shfl_xor(top[q], 16, kWave));
-            top[q] = fmaxf(top[q], __shfl_xor(top[q], 32, kWave));
-            fit[q] = fit_scale(top[q]);
-        }
-    }
-    for (int p = tile.p0 + wave * 32; p < end; p += 128) {
-        uint32_t v[8][4];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int at = p + g * 8 + e;
-            const int64_t row = at < end ? source_row(a.l, at) : -1;
-            load_pairs<8>(v[e], big + (row < 0 ? 0 : row) * ld, c_load, C, row >= 0);
-        }
-        u32x4_t hi[RG], lo[RG];
-#pragma unroll
-        for (int q = 0; q < RG; ++q) {
-            float s[8];
-            load_small(s, p + g * 8, end, r0 + q * 16);
-            if constexpr (DT == kFp16)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[e] *= fit[q];
-            split8<DT>(s, hi[q], lo[q]);
-        }
-#pragma unroll
-        for (int f = 0; f < 8; ++f) {
-            const u32x4_t bf = column<8>(v, f);
-#pragma unroll
-            for (int q = 0; q < RG; ++q) {
-                acc[f][q] = mfma<DT>(bf, hi[q], acc[f][q]);
-                acc[f][q] = mfma<DT>(bf, lo[q], acc[f][q]);
-            }
-        }
-    }
-    if constexpr (DT == kFp16) {
+    const int p_first = begin + wave * 32;
+    if (p_first < end && rt * kRanks < rank) {
+        const uint16_t *const big_c = big + min(ct * 128 + m * 8, C - 8);
+        const float *small_r[RG];
 #pragma unroll
         for (int q = 0; q < RG; ++q)
+            small_r[q] = small + min(r0 + q * 16, rank - 1);
+        auto rows_of = [&](int (&at)[8], int p) {
 #pragma unroll
-            for (int f = 0; f < 8; ++f)
-                acc[f][q] *= inverse_scale(fit[q]);
-    }
+            for (int e = 0; e < 8; ++e) {
+                const int i = min(p + g * 8 + e, end - 1);
+                at[e] = a.l.gather ? a.l.gather[i] : i;
+            }
+        };
+        auto load_small = [&](float (&v)[RG][8], int p) {
 #pragma unroll
-    for (int half = 2; half > 0; half >>= 1) {
-        if (wave >= half && wave < 2 * half)
-#pragma unroll
-            for (int f = 0; f < 8; ++f)
-#pragma unroll
-                for (int q = 0; q < RG; ++q)
-                    s_acc[wave - half][f * RG + q][lane] = acc[f][q];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int f = 0; f < 8; ++f)
+            for (int e = 0; e < 8; ++e) {
+                const int64_t o = (int64_t)min(p + g * 8 + e, end - 1) * a.R;
 #pragma unroll
                 for (int q = 0; q < RG; ++q)
-                    acc[f][q] += s_acc[wave][f * RG + q][lane];
-        __syncthreads();
-    }
-    if (wave != 0)
-        return;
-    const float factor = !is_a && a.l.scales ? a.l.scales[tile.a] : 1.0f;
-    const bool whole = tile.m <= a.chunk;
-    const int64_t size_a = (int64_t)a.R * a.K;
-    float *const part = a.partials + (int64_t)(tile.slot + tile.index) * ((a.K + (int64_t)a.N) * a.R) +
-                        (is_a ? 0 : size_a);
-    char *const out = static_cast<char *>(is_a ? a.dA : a.dB);
-    const int64_t out0 = (int64_t)tile.a * a.R * C;
+                    v[q][e] = small_r[q][o];
+            }
+            for (int s = 1; s < splits; ++s)
 #pragma unroll
-    for (int q = 0; q < RG; ++q) {
-        const int r = r0 + q * 16;
-        if (r >= a.R)
-            continue;
+                for (int e = 0; e < 8; ++e) {
+                    const int64_t o = (int64_t)min(p + g * 8 + e, end - 1) * a.R +
+                                      s * a.split_stride;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = ct * 128 + (i * 4 + g) * 8;
+                    for (int q = 0; q < RG; ++q)
+                        v[q][e] += small_r[q][o];
+                }
+        };
+        if constexpr (DT == kFp16) {
+            float top[RG] = {};
+            for (int p = p_first; p < end; p += 128) {
+                float v[RG][8];
+                load_small(v, p);
 #pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                if (c + f >= C)
-                    continue;
-                const int64_t at = is_a ? (int64_t)r * C + c + f : (int64_t)(c + f) * a.R + r;
-                const float v = factor * acc[f][q][i];
-                if (!whole)
-                    part[at] = v;
-                else if (a.fp32_out)
-                    reinterpret_cast<float *>(out)[out0 + at] = v;
-                else
-                    reinterpret_cast<uint16_t *>(out)[out0 + at] = Elem<DT>::narrow(v);
+                for (int q = 0; q < RG; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        top[q] = fmaxf(top[q], fabsf(v[q][e]));
+            }
+#pragma unroll
+            for (int q = 0; q < RG; ++q) {
+                top[q] = fmaxf(top[q], __shfl_xor(top[q], 16, kWave));
+                top[q] = fmaxf(top[q], __shfl_xor(top[q], 32, kWave));
+                fit[q] = fit_scale(top[q]);
             }
         }
+        int at[8];
+        rows_of(at, p_first);
+        for (int p = p_first; p < end; p += 128) {
+            u32x4_t v[8];
+            float h[RG][8];
+            uint32_t rows[8][4];
+            bool ok[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ok[e] = at[e] >= 0 && at[e] < a.l.T;
+                v[e] = load8_in(big_c + (int64_t)(ok[e] ? at[e] : 0) * ld);
+                ok[e] = ok[e] && p + g * 8 + e < end;
+            }
+            load_small(h, p);
+            rows_of(at, p + 128);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rows[e][i] = ok[e] ? v[e][i] : 0;
+            u32x4_t hi[RG], lo[RG];
+#pragma unroll
+            for (int q = 0; q < RG; ++q) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    h[q][e] = ok[e] && r0 + q * 16 < rank ? h[q][e] : 0.0f;
+                    if constexpr (DT == kFp16)
+                        h[q][e] *= fit[q];
+                }
+                split8<DT>(h[q], hi[q], lo[q]);
+            }
+#pragma unroll
+            for (int f = 0; f < 8; ++f) {
+                const u32x4_t bf = column<8>(rows, f);
+#pragma unroll
+                for (int q = 0; q < RG; ++q) {
+                    acc[f][q] = mfma<DT>(bf, hi[q], acc[f][q]);
+                    acc[f][q] = mfma<DT>(bf, lo[q], acc[f][q]);
+                }
+            }
+        }
+    }
+    // A lane holds rank m of each block, columns (4 g + i) * 8 + f.
+#pragma unroll
+    for (int q = 0; q < RG; ++q) {
+        const float k = DT == kFp16 ? inverse_scale(fit[q]) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *const d = &s_sum[wave][q * 16 + m][(4 * g + i) * 8];
+            *reinterpret_cast<f32x4_t *>(d) =
+                k * f32x4_t{acc[0][q][i], acc[1][q][i], acc[2][q][i], acc[3][q][i]};
+            *reinterpret_cast<f32x4_t *>(d + 4) =
+                k * f32x4_t{acc[4][q][i], acc[5][q][i], acc[6][q][i], acc[7][q][i]};
+        }
+    }
+    __syncthreads();
+    const float factor = !is_a && a.l.scales ? a.l.scales[tile.a] : 1.0f;
+    const int64_t size_a = (int64_t)a.R * a.K;
+    float *part = nullptr;  // fp32 output: partials, or the caller's
+    uint16_t *out16 = nullptr;
+    const int64_t out0 = (int64_t)tile.a * a.R * C;
+    if (chunks > 1)
+        part = a.partials + (int64_t)(tile.slot + tile.index) * ((a.K + (int64_t)a.N) * a.R) +
+               (is_a ? 0 : size_a);
+    else if (a.fp32_out)
+        part = static_cast<float *>(is_a ? a.dA : a.dB) + out0;
+    else
+        out16 = static_cast<uint16_t *>(is_a ? a.dA : a.dB) + out0;
+    // The columns that LDS column x stands for, and where its own begin.
+    const int ranks_here = min(kRanks, a.R - rt * kRanks);
+    const int cols_here = min(128, C - ct * 128);
+    for (int i = threadIdx.x; i < kRanks * 128; i += 256) {
+        // dA: columns run fastest, dB: ranks.
+        const int x = is_a ? i % 128 : i / kRanks;
+        const int r = is_a ? i / 128 : i % kRanks;
+        if (x >= cols_here || r >= ranks_here)
+            continue;
+        // The piece of 8 that holds column x was moved back to the row's end.
+        const int back = max(ct * 128 + x / 8 * 8 - (C - 8), 0);
+        const float v = factor * (((s_sum[0][r][x + back] + s_sum[1][r][x + back]) +
+                                   s_sum[2][r][x + back]) + s_sum[3][r][x + back]);
+        const int64_t to = is_a ? (int64_t)(rt * kRanks + r) * C + ct * 128 + x
+                                : (int64_t)(ct * 128 + x) * a.R + rt * kRanks + r;
+        if (part)
+            part[to] = v;
+        else
+            out16[to] = Elem<DT>::narrow(v);
     }
 }
 
-// Adds the partials of adapters with several chunks, in chunk order.
+// Adds the partials of adapters with several chunks, in chunk order, 4
+// elements a thread (one where K or N times R is no multiple of 4).
 template <int DT>
 __global__ __launch_bounds__(256) void grad_join_kernel(GradParams a, int blocks)
 {
@@ -696,54 +932,105 @@ __global__ __launch_bounds__(256) void grad_join_kernel(GradParams a, int blocks
     const int chunks = (tile.m - 1) / a.chunk + 1;
     const int64_t size_a = (int64_t)a.R * a.K, size = size_a + (int64_t)a.R * a.N;
     const float *const part = a.partials + (int64_t)tile.slot * size;
-    for (int64_t i = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x; i < size;
-         i += (int64_t)blocks * 256) {
+    const int step = (size_a | size) % 4 == 0 ? 4 : 1;
+    for (int64_t i = ((int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x) * step; i < size;
+         i += (int64_t)blocks * 256 * step) {
         const bool is_a = i < size_a;
         void *const out = is_a ? a.dA : a.dB;
-        float v = 0.0f;
-        for (int c = 0; c < chunks; ++c)
-            v += part[c * size + i];
-        const int64_t at = is_a ? (int64_t)tile.a * size_a + i
+        const int64_t to = is_a ? (int64_t)tile.a * size_a + i
                                 : (int64_t)tile.a * a.R * a.N + (i - size_a);
-        if (a.fp32_out)
-            static_cast<float *>(out)[at] = v;
-        else
-            static_cast<uint16_t *>(out)[at] = Elem<DT>::narrow(v);
+        f32x4_t v = {};
+        if (step == 4) {
+            for (int c = 0; c < chunks; ++c)
+                v += *reinterpret_cast<const f32x4u_t *>(part + c * size + i);
+        } else {
+            for (int c = 0; c < chunks; ++c)
+                v[0] += part[c * size + i];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e >= step)
+                break;
+            if (a.fp32_out)
+                static_cast<float *>(out)[to + e] = v[e];
+            else
+                static_cast<uint16_t *>(out)[to + e] = Elem<DT>::narrow(v[e]);
+        }
     }
 }
 
 // ---------------------------------------------------------------- launches
 
+template <int DT, bool TR, int RF, int RT>
+hipError_t shrink_rt(const LoraParams &p, int64_t tiles, hipStream_t stream)
+{
+    const dim3 grid((unsigned)(tiles * p.splits)), block(kShrinkWaves * kWave);
+    if (p.C % 32 || p.R % 4 || (TR && p.R % RF))
+        hipLaunchKernelGGL((shrink_kernel<DT, TR, RF, RT, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((shrink_kernel<DT, TR, RF, RT, false>), grid, block, 0, stream, p);
+    return hipGetLastError();
+}
+
+template <int DT, bool TR, int RF> hipError_t shrink_rf(const LoraParams &p, hipStream_t stream)
+{
+    constexpr int kMany = shrink_blocks(RF * 16);
+    const int rows = lora_shrink_rows(p.T, p.L, p.R);
+    const int64_t tiles = (p.T + rows - 1) / rows + (p.T < p.L ? p.T : p.L);
+    if (rows > 16)
+        return shrink_rt<DT, TR, RF, kMany>(p, tiles, stream);
+    return shrink_rt<DT, TR, RF, 1>(p, tiles, stream);
+}
+
 template <int DT, bool TR> hipError_t shrink_go(const LoraParams &p, hipStream_t stream)
 {
-    const int64_t tiles = (p.T + kShrinkRows - 1) / kShrinkRows + (p.T < p.L ? p.T : p.L);
-    const dim3 grid((unsigned)(tiles * p.splits)), block(kShrinkWaves * kWave);
     if (p.R <= 16)
-        hipLaunchKernelGGL((shrink_kernel<DT, TR, 1>), grid, block, 0, stream, p);
-    else if (p.R <= 32)
-        hipLaunchKernelGGL((shrink_kernel<DT, TR, 2>), grid, block, 0, stream, p);
-    else if (p.R <= 64)
-        hipLaunchKernelGGL((shrink_kernel<DT, TR, 4>), grid, block, 0, stream, p);
-    else if (p.R <= 128)
-        hipLaunchKernelGGL((shrink_kernel<DT, TR, 8>), grid, block, 0, stream, p);
+        return shrink_rf<DT, TR, 1>(p, stream);
+    if (p.R <= 32)
+        return shrink_rf<DT, TR, 2>(p, stream);
+    if (p.R <= 64)
+        return shrink_rf<DT, TR, 4>(p, stream);
+    if (p.R <= 128)
+        return shrink_rf<DT, TR, 8>(p, stream);
+    return shrink_rf<DT, TR, 16>(p, stream);
+}
+
+template <int DT, bool TR, int NS, bool SMALL>
+hipError_t expand_ns(const LoraParams &p, int64_t tiles, hipStream_t stream)
+{
+    // A column group is at least one pass of a workgroup whose waves deal out
+    // the columns; groups are added until the launch has 8 workgroups a compute
+    // unit, in multiples of the 8 XCDs, so that a group's weights stay in the
+    // L2 of one.
+    const int pass = 4 * 64;
+    const int most = (p.C + pass - 1) / pass;
+    int groups = (int)((2048 + tiles - 1) / tiles);
+    groups = (groups + kXcds - 1) / kXcds * kXcds;
+    groups = groups < most ? groups : most;
+    const int group_cols = ((p.C + groups - 1) / groups + pass - 1) / pass * pass;
+    groups = (p.C + group_cols - 1) / group_cols;
+    const dim3 grid((unsigned)(tiles * groups)), block(256);
+    if (p.C % 64 || (!TR && p.R % 8))
+        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, true>), grid, block, 0, stream, p,
+                           groups, group_cols);
     else
-        hipLaunchKernelGGL((shrink_kernel<DT, TR, 16>), grid, block, 0, stream, p);
+        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, false>), grid, block, 0, stream, p,
+                           groups, group_cols);
     return hipGetLastError();
 }
 
 template <int DT, bool TR> hipError_t expand_go(const LoraParams &p, hipStream_t stream)
 {
-    const int rows = TR ? kExpandRowsT : kExpandRows;
-    const int cols = 4 * (TR ? 128 : 64);
-    const int64_t tiles = (p.T + rows - 1) / rows + (p.T < p.L ? p.T : p.L);
-    const int col_tiles = (p.C + cols - 1) / cols;
-    const dim3 grid((unsigned)(tiles * col_tiles));
+    const int64_t tiles = (p.T + kExpandRows - 1) / kExpandRows + (p.T < p.L ? p.T : p.L);
     if (p.R <= 16)
-        hipLaunchKernelGGL((expand_kernel<DT, TR, true>), grid, dim3(256), 0, stream, p, col_tiles);
-    else
-        hipLaunchKernelGGL((expand_kernel<DT, TR, false>), grid, dim3(256), 0, stream, p,
-                           col_tiles);
-    return hipGetLastError();
+        return expand_ns<DT, TR, 1, true>(p, tiles, stream);
+    if (p.R <= 32)
+        return expand_ns<DT, TR, 1, false>(p, tiles, stream);
+    if (p.R <= 64)
+        return expand_ns<DT, TR, 2, false>(p, tiles, stream);
+    if (p.R <= 128)
+        return expand_ns<DT, TR, 4, false>(p, tiles, stream);
+    return expand_ns<DT, TR, 8, false>(p, tiles, stream);
 }
 
 template <int DT> hipError_t grad_go(const GradParams &p, hipStream_t stream)
@@ -758,9 +1045,14 @@ template <int DT> hipError_t grad_go(const GradParams &p, hipStream_t stream)
         hipLaunchKernelGGL((grad_kernel<DT, 2>), grid, dim3(256), 0, stream, p);
     if (p.l.T <= p.chunk)
         return hipGetLastError();
-    const int blocks = 64;
+    // Up to 1024 elements a workgroup and adapter, at most about 16 workgroups
+    // a compute unit.
+    const int64_t size = (int64_t)p.R * ((int64_t)p.K + p.N);
+    int64_t blocks = (size + 1023) / 1024;
+    const int64_t most = (4096 + p.l.L - 1) / p.l.L;
+    blocks = blocks < most ? blocks : most;
     hipLaunchKernelGGL((grad_join_kernel<DT>), dim3((unsigned)(p.l.L * blocks)), dim3(256), 0,
-                       stream, p, blocks);
+                       stream, p, (int)blocks);
     return hipGetLastError();
 }
 

@@ -7,9 +7,7 @@
 
 namespace moegg {
 
-constexpr int kShrinkRows = 16;   // rows of a shrink tile
-constexpr int kExpandRows = 64;   // rows of an expand tile, forward
-constexpr int kExpandRowsT = 32;  // and with transposed weights (dx)
+constexpr int kExpandRows = 64;   // rows of an expand tile
 
 // Shrink (in, w -> h) and expand (h, w, base -> out) of T rows; C is the wide
 // dimension: columns of `in` or of `out`.
@@ -22,7 +20,7 @@ struct LoraParams {
     const float *scales;
     const uint16_t *base;
     uint16_t *out;
-    float *h;      // [splits][T][R]
+    float *h;      // [splits][T][R], 8 more values behind
     float *h_out;  // [T][R] the caller's sum of the splits, or null
     int32_t *err;
     int64_t T, ld_in, ld_base, ld_out, split_stride;
@@ -45,23 +43,43 @@ struct GradParams {
     bool fp32_out;
 };
 
+// 16-row blocks of a large shrink tile for ranks up to R: as many as keep the
+// sums of the tile in 64 registers.
+__host__ __device__ constexpr int shrink_blocks(int R)
+{
+    return R <= 64 ? 4 : R <= 128 ? 2 : 1;
+}
+
+// Rows of a shrink tile: one block of 16, or a large tile where an adapter has
+// 32 rows or more on average.
+inline int lora_shrink_rows(int64_t T, int L, int R)
+{
+    const int64_t n = T < L ? T : L;
+    return T >= 32 * n ? 16 * shrink_blocks(R) : 16;
+}
+
 // Shrink splits: how many workgroups share a tile's reduction of C columns.
 // One workgroup a compute unit (256) is aimed at; a wave's share stays at 64
 // columns or more, and at most 16 partial sums are left to add.
-inline int lora_splits(int64_t T, int L, int C)
+inline int lora_splits(int64_t T, int L, int R, int C)
 {
-    const int64_t tiles = (T + kShrinkRows - 1) / kShrinkRows + (T < L ? T : L);
+    const int rows = lora_shrink_rows(T, L, R);
+    const int64_t tiles = (T + rows - 1) / rows + (T < L ? T : L);
     int64_t n = tiles > 0 ? (256 + tiles - 1) / tiles : 1;
     n = n < C / 512 ? n : C / 512;
     return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
 }
 
-// Rows of one chunk of the gradients' reduction: 512, more when that would
-// leave over 16 chunks to add.
-inline int lora_chunk(int64_t T)
+// Rows of one chunk of the gradients' reduction, a multiple of 32: such that
+// chunks, column tiles and rank tiles make about 384 workgroups (two fit a
+// compute unit at a time, and segments that are no whole chunks add some), but
+// no fewer than one 32-row step for each of a workgroup's waves.
+inline int lora_chunk(int64_t T, int R, int K, int N)
 {
-    const int64_t c = ((T + 15) / 16 + 127) / 128 * 128;
-    return (int)(c < 512 ? 512 : c);
+    const int64_t tiles = (((int64_t)K + 127) / 128 + ((int64_t)N + 127) / 128) *
+                          (R <= 16 ? 1 : (R + 31) / 32);
+    const int64_t c = (T * tiles / 384 + 31) / 32 * 32;
+    return (int)(c < 128 ? 128 : c < T ? c : (T + 31) / 32 * 32 + 128);
 }
 
 hipError_t lora_shrink_launch(const LoraParams &p, int dtype, bool transposed, hipStream_t stream);
