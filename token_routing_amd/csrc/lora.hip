@@ -482,12 +482,14 @@ __global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams 
 // the sums through a strip of LDS into row order, so that base is read and
 // out written in whole 128-byte lines: straight from the accumulators' layout
 // every 16 bytes of a line would be looked up apart, which took 1.7 times as
-// long.  Base is loaded one pass ahead.  SMALL: ranks up to 16, both parts of
+// long.  The next pass's weights are issued after this one's matrix
+// instructions and its base as this one's is used, in the order in which they
+// are waited for.  SMALL: ranks up to 16, both parts of
 // h in one instruction.  EDGE: columns that are no whole passes (the last one
 // goes by single elements, a row at a time) or, forward, ranks that are no
 // whole pieces of 8.
 template <int DT, bool TR, int NS, bool SMALL, bool EDGE>
-__global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int groups, int group_cols)
+__global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups, int group_cols)
 {
     constexpr int F = 4;
     constexpr int kCols = F * 16;
@@ -531,9 +533,32 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int groups, i
             for (int i = 0; i < 2; ++i)
                 old[t][i] = load8_in(a.base + (int64_t)max(src[t][i], 0) * a.ld_base + c0 + col_lane);
     };
+
+    // A step's weights of the lane, as loaded: forward 4 fragments, TR 8 rows
+    // of 4 columns.  Every address lies inside the adapter's weights.
+    const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
+    uint32_t raw[NS][8][2];
+    auto load_weights = [&](uint32_t (&v)[8][2], int s, int c0) {
+        const int r0 = s * 32 + rg;
+        if constexpr (TR) {
+            // The last lanes' columns are moved inside the row.
+            const int c = EDGE ? min(c0 + m * 4, a.C - 4) : c0 + m * 4;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-        load_base(t, c_begin);
+            for (int e = 0; e < 8; ++e)
+                load_pairs<4>(v[e], w + (int64_t)min(r0 + e, a.R - 1) * a.C + c);
+        } else {
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int c = c0 + f * 16 + m;
+                const int64_t at =
+                    (int64_t)(EDGE ? min(c, a.C - 1) : c) * a.R + (r0 < a.R ? r0 : 0);
+                const u32x4_t b = EDGE ? load8_end(w, at, (int64_t)a.C * a.R) : load8_in(w + at);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[(4 * f + i) / 2][(4 * f + i) % 2] = b[i];
+            }
+        }
+    };
 
     // The summed h for the caller, by the first column group.
     if (a.h_out && group == 0)
@@ -592,79 +617,65 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int groups, i
                 s_src[t] = t < tile.rows && x >= 0 && x < a.T ? x : -1;
         }
     }
-    __syncthreads();
-
-    const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
-    for (int c0 = c_begin; c0 < c_end; c0 += 4 * kCols) {
-        const bool inside = !EDGE || c0 + kCols <= a.C;
-        f32x4_t acc[RT][F];
+    if (c_begin < c_end) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            load_weights(raw[s], s, c_begin);
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-                acc[t][f] = f32x4_t{};
+            load_base(t, c_begin);
+    }
+    __syncthreads();
+
+    for (int c0 = c_begin; c0 < c_end; c0 += 4 * kCols) {
+        const bool inside = !EDGE || c0 + kCols <= a.C;
+        // Fragments; ranks at or past the rank may hold anything.
+        u32x4_t wf[NS][F];
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            if (s * 32 >= rank)
-                break;
-            const int r0 = s * 32 + rg;
-            u32x4_t wf[F];
-            if constexpr (TR) {
-                // 8 rows of 4 columns; the last lanes' are moved inside the row.
-                const int c = EDGE ? min(c0 + m * 4, a.C - 4) : c0 + m * 4;
-                uint32_t v[8][2];
+            const int left = rank - (s * 32 + rg);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    load_pairs<4>(v[e], w + (int64_t)min(r0 + e, rank - 1) * a.C + c);
+            for (int f = 0; f < F; ++f) {
+                if constexpr (TR)
+                    wf[s][f] = column<4>(raw[s], f);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        v[e][i] = r0 + e < rank ? v[e][i] : 0;
-                }
-#pragma unroll
-                for (int f = 0; f < F; ++f)
-                    wf[f] = column<4>(v, f);
-            } else {
-                u32x4_t mask;  // ranks below the rank; others may hold anything
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mask[i] = r0 + 2 * i + 1 < rank ? ~0u : r0 + 2 * i < rank ? 0xffffu : 0u;
-#pragma unroll
-                for (int f = 0; f < F; ++f) {
-                    const int c = c0 + f * 16 + m;
-                    const int64_t at =
-                        (int64_t)(EDGE ? min(c, a.C - 1) : c) * a.R + (r0 < rank ? r0 : 0);
-                    wf[f] = EDGE ? load8_end(w, at, (int64_t)a.C * a.R) : load8_in(w + at);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        wf[f][i] &= mask[i];
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (!TR)
+                        wf[s][f][i] = raw[s][(4 * f + i) / 2][(4 * f + i) % 2];
+                    wf[s][f][i] &= left > 2 * i + 1 ? ~0u : left > 2 * i ? 0xffffu : 0u;
                 }
             }
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-                if (t < blocks) {
-                    const u32x4_t hi = s_h[s][t][0][lane];
-#pragma unroll
-                    for (int f = 0; f < F; ++f)
-                        acc[t][f] = mfma<DT>(wf[f], hi, acc[t][f]);
-                    if constexpr (!SMALL) {
-                        const u32x4_t lo = s_h[s][t][SMALL ? 0 : 1][lane];
-#pragma unroll
-                        for (int f = 0; f < F; ++f)
-                            acc[t][f] = mfma<DT>(wf[f], lo, acc[t][f]);
-                    }
-                }
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             if (t >= blocks)
-                continue;
+                break;
+            f32x4_t acc[F];
+#pragma unroll
+            for (int f = 0; f < F; ++f)
+                acc[f] = f32x4_t{};
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (s * 32 >= rank)
+                    break;
+#pragma unroll
+                for (int part = 0; part < (SMALL ? 1 : 2); ++part) {
+                    const u32x4_t h = s_h[s][t][part][lane];
+#pragma unroll
+                    for (int f = 0; f < F; ++f)
+                        acc[f] = mfma<DT>(wf[s][f], h, acc[f]);
+                }
+            }
+            if (t == blocks - 1 && c0 + 4 * kCols < c_end)
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    load_weights(raw[s], s, c0 + 4 * kCols);
             // A lane holds row m, columns f * 16 + 4 g + i (TR: (4 g + i) * 4 + f).
             if (!TR || inside) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4_t v = TR ? f32x4_t{acc[t][0][i], acc[t][1][i], acc[t][2][i],
-                                                   acc[t][3][i]}
-                                         : acc[t][i];
+                    const f32x4_t v = TR ? f32x4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]}
+                                         : acc[i];
                     *reinterpret_cast<f32x4_t *>(
                         &s_out[wave][m][TR ? (4 * g + i) * 4 : i * 16 + 4 * g]) = v;
                 }
@@ -675,7 +686,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraParams a, int groups, i
 #pragma unroll
                     for (int f = 0; f < F; ++f)
                         if (c + f >= 0)
-                            s_out[wave][m][c + f] = acc[t][f][i];
+                            s_out[wave][m][c + f] = acc[f][i];
                 }
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
