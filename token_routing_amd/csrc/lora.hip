@@ -30,6 +30,8 @@
 // Rows go by tiles inside one adapter's segment; each wave finds its tile by
 // a scan of m_sizes in registers (64 segments a step), so no launch depends
 // on the host knowing the sizes.
+#include <type_traits>
+
 #include "elems.h"
 
 #include "lora_params.h"
@@ -528,10 +530,10 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
     const int c_begin = group * group_cols + wave * kCols;
     u32x4_t old[RT][2];
     auto load_base = [&](int t, int c0) {
-        if (c0 < c_end && (!EDGE || c0 + kCols <= a.C) && t < blocks)
+        const int c = EDGE ? min(c0 + col_lane, a.C - 8) : c0 + col_lane;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                old[t][i] = load8_in(a.base + (int64_t)max(src[t][i], 0) * a.ld_base + c0 + col_lane);
+        for (int i = 0; i < 2; ++i)
+            old[t][i] = load8_in(a.base + (int64_t)max(src[t][i], 0) * a.ld_base + c);
     };
 
     // A step's weights of the lane, as loaded: forward 4 fragments, TR 8 rows
@@ -623,12 +625,18 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
             load_weights(raw[s], s, c_begin);
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-            load_base(t, c_begin);
+            if (t < blocks)
+                load_base(t, c_begin);
     }
     __syncthreads();
+    if (c_begin >= c_end)
+        return;
 
-    for (int c0 = c_begin; c0 < c_end; c0 += 4 * kCols) {
-        const bool inside = !EDGE || c0 + kCols <= a.C;
+    // One pass.  FULL: all row blocks are there; MORE: another pass follows.
+    // Both are fixed at compile time, since a load under a branch makes every
+    // later wait count as if it had not been issued.
+    auto pass = [&](int c0, auto full_c, auto more_c) {
+        constexpr bool FULL = decltype(full_c)::value, MORE = decltype(more_c)::value;
         // Fragments; ranks at or past the rank may hold anything.
         u32x4_t wf[NS][F];
 #pragma unroll
@@ -648,16 +656,14 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            if (t >= blocks)
+            if (!FULL && t >= blocks)
                 break;
             f32x4_t acc[F];
 #pragma unroll
             for (int f = 0; f < F; ++f)
                 acc[f] = f32x4_t{};
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                if (s * 32 >= rank)
-                    break;
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int part = 0; part < (SMALL ? 1 : 2); ++part) {
                     const u32x4_t h = s_h[s][t][part][lane];
@@ -665,17 +671,17 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
                     for (int f = 0; f < F; ++f)
                         acc[f] = mfma<DT>(wf[s][f], h, acc[f]);
                 }
-            }
-            if (t == blocks - 1 && c0 + 4 * kCols < c_end)
+            if (MORE && t == (FULL ? RT : blocks) - 1)
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
                     load_weights(raw[s], s, c0 + 4 * kCols);
             // A lane holds row m, columns f * 16 + 4 g + i (TR: (4 g + i) * 4 + f).
+            const bool inside = !EDGE || MORE || c0 + kCols <= a.C;
             if (!TR || inside) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4_t v = TR ? f32x4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]}
-                                         : acc[i];
+                    const f32x4_t v =
+                        TR ? f32x4_t{acc[0][i], acc[1][i], acc[2][i], acc[3][i]} : acc[i];
                     *reinterpret_cast<f32x4_t *>(
                         &s_out[wave][m][TR ? (4 * g + i) * 4 : i * 16 + 4 * g]) = v;
                 }
@@ -715,7 +721,8 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
                             out, reinterpret_cast<typename Pack16<DT>::vec_t *>(
                                      a.out + (int64_t)src[t][i] * a.ld_out + c0 + col_lane));
                 }
-                load_base(t, c0 + 4 * kCols);
+                if constexpr (MORE)
+                    load_base(t, c0 + 4 * kCols);
             } else {
                 for (int r = 0; r < min(16, tile.rows - t * 16); ++r) {
                     const int64_t x = s_src[t * 16 + r];
@@ -730,6 +737,16 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
+    };
+    int c0 = c_begin;
+    if (blocks == RT) {
+        for (; c0 + 4 * kCols < c_end; c0 += 4 * kCols)
+            pass(c0, std::true_type{}, std::true_type{});
+        pass(c0, std::true_type{}, std::false_type{});
+    } else {
+        for (; c0 + 4 * kCols < c_end; c0 += 4 * kCols)
+            pass(c0, std::false_type{}, std::true_type{});
+        pass(c0, std::false_type{}, std::false_type{});
     }
 }
 
