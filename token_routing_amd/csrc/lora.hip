@@ -58,33 +58,29 @@ struct Tile {
     int slot;   // partial sums' first place (segments of several tiles only)
 };
 
-// Sums saturate at S, so that bad sizes cannot wrap around.
-__device__ __forceinline__ uint32_t scan_rows(uint32_t v, uint32_t S)
+// Inclusive scan over the wave by data-parallel moves inside the registers (a
+// lane shift through LDS costs ten times as much, and every launch waits for
+// its scans first).  add(x, 0) has to be x.
+template <class Add> __device__ __forceinline__ uint32_t wave_scan(uint32_t v, Add add)
 {
-    const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint32_t o = __shfl_up(v, d, kWave);
-        if (lane >= d)
-            v = min(v + o, S);
-    }
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // row_shr:1
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));  // row_shr:2
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));  // row_shr:4
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));  // row_shr:8
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // row_bcast:15
+    v = add(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // row_bcast:31
     return v;
 }
-__device__ __forceinline__ int scan_sum(int v)
+
+__device__ __forceinline__ int lane_of(uint32_t v, int lane)
 {
-    const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(v, d, kWave);
-        if (lane >= d)
-            v += o;
-    }
-    return v;
+    return __builtin_amdgcn_readlane((int)v, lane);
 }
 
 // The tile `want` of all segments' tiles of `per` rows (empty segments have
 // `empty` tiles); false past the last one.  By adapter with by_adapter: the
-// segment of adapter `want`.  All lanes of the wave call it.
+// segment of adapter `want`.  All lanes of the wave call it.  Row sums
+// saturate at S, so that bad sizes cannot wrap around.
 __device__ __forceinline__ bool find_tile(const int32_t *m_sizes, int L, uint32_t S, int want,
                                           int per, int empty, bool by_adapter, Tile &t)
 {
@@ -93,31 +89,32 @@ __device__ __forceinline__ bool find_tile(const int32_t *m_sizes, int L, uint32_
     int tile0 = 0, slot0 = 0;
     for (int c = 0; c < L; c += kWave) {
         const int a = c + lane;
-        const int raw = a < L ? m_sizes[a] : 0;
-        const uint32_t v = min((uint32_t)max(raw, 0), S);
-        const uint32_t end = min(scan_rows(v, S) + row0, S);
-        uint32_t start = __shfl_up(end, 1, kWave);
-        if (lane == 0)
-            start = row0;
+        const int raw = m_sizes[min(a, L - 1)];
+        const uint32_t v = a < L ? min((uint32_t)max(raw, 0), S) : 0;
+        const uint32_t end = min(
+            wave_scan(v, [S](uint32_t x, uint32_t y) { return min(x + y, S); }) + row0, S);
+        // The row before a segment: the lane below's end (the first lane's is row0).
+        uint32_t start = __builtin_amdgcn_update_dpp(row0, end, 0x138, 0xf, 0xf, false);  // wave_shr:1
         const int m = (int)(end - start);
         const int n = m > 0 ? (m - 1) / per + 1 : (a < L ? empty : 0);
-        const int tiles = scan_sum(n);
-        const int slots = scan_sum(n > 1 ? n : 0);
+        const auto sum = [](uint32_t x, uint32_t y) { return x + y; };
+        const int tiles = (int)wave_scan(n, sum);
+        const int slots = (int)wave_scan(n > 1 ? n : 0, sum);
         const uint64_t hit =
             __ballot(by_adapter ? a == want : a < L && tile0 + tiles > want);
         if (hit) {
             const int l = __ffsll((unsigned long long)hit) - 1;
             t.a = c + l;
-            t.m = __shfl(m, l, kWave);
-            t.index = by_adapter ? 0 : want - (tile0 + __shfl(tiles - n, l, kWave));
-            t.p0 = (int)__shfl(start, l, kWave) + t.index * per;
+            t.m = lane_of(m, l);
+            t.index = by_adapter ? 0 : want - (tile0 + lane_of(tiles - n, l));
+            t.p0 = lane_of(start, l) + t.index * per;
             t.rows = min(per, t.m - t.index * per);
-            t.slot = slot0 + __shfl(slots, l, kWave) - (t.m > per ? (t.m - 1) / per + 1 : 0);
+            t.slot = slot0 + lane_of(slots, l) - (t.m > per ? (t.m - 1) / per + 1 : 0);
             return true;
         }
-        row0 = __shfl(end, kWave - 1, kWave);
-        tile0 += __shfl(tiles, kWave - 1, kWave);
-        slot0 += __shfl(slots, kWave - 1, kWave);
+        row0 = lane_of(end, kWave - 1);
+        tile0 += lane_of(tiles, kWave - 1);
+        slot0 += lane_of(slots, kWave - 1);
     }
     return false;
 }
@@ -273,10 +270,20 @@ __device__ __forceinline__ void load_h(float (&v)[8], const float *h, int64_t p,
     const float *q = h + p * R + (col < n ? col : 0);
     f32x4_t a = *reinterpret_cast<const f32x4u_t *>(q);
     f32x4_t b = *reinterpret_cast<const f32x4u_t *>(q + 4);
-    for (int s = 1; s < splits; ++s) {
-        q += split_stride;
-        a += *reinterpret_cast<const f32x4u_t *>(q);
-        b += *reinterpret_cast<const f32x4u_t *>(q + 4);
+    for (int s = 1; s < splits; s += 4) {
+        f32x4_t c[4], d[4];  // four splits' loads at once, the last one's again past the end
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float *const r = q + min(s + u, splits - 1) * split_stride;
+            c[u] = *reinterpret_cast<const f32x4u_t *>(r);
+            d[u] = *reinterpret_cast<const f32x4u_t *>(r + 4);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s + u < splits) {
+                a += c[u];
+                b += d[u];
+            }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -307,7 +314,7 @@ __device__ __forceinline__ void load_h(float (&v)[8], const float *h, int64_t p,
 constexpr int kShrinkWaves = 8;
 
 template <int DT, bool TR, int RF, int RT, bool EDGE>
-__global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams a)
+__global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_kernel(LoraParams a)
 {
     // With TR a lane holds ranks m * RF + j, one piece of a row of weights;
     // with EDGE ranks f * 16 + m, one element of a row at a time.
@@ -316,7 +323,7 @@ __global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams 
     constexpr int D = W < 2 ? 1 : W / 2;
     constexpr int Q = TR ? (PIECES ? 1 : RF) : 1;  // loads of a row of weights (TR)
     constexpr int U = RF <= 2 ? 4 : RF <= 8 ? 2 : 1;
-    __shared__ f32x4_t s_acc[kShrinkWaves / 2][RT * RF][kWave];
+    __shared__ f32x4_t s_acc[kShrinkWaves][RT * RF < kShrinkWaves ? RT * RF : kShrinkWaves][kWave];
     check_sizes(a.m_sizes, a.ranks, a.L, a.T, a.R, a.err);
     const int split = blockIdx.x % a.splits;
     Tile tile;
@@ -423,52 +430,45 @@ __global__ __launch_bounds__(kShrinkWaves *kWave) void shrink_kernel(LoraParams 
             }
         }
     }
-#pragma unroll
-    for (int half = kShrinkWaves / 2; half > 0; half >>= 1) {
-        if (wave >= half && wave < 2 * half)
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int f = 0; f < RF; ++f)
-                    s_acc[wave - half][t * RF + f][lane] = acc[t][f];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-#pragma unroll
-                for (int f = 0; f < RF; ++f)
-                    acc[t][f] += s_acc[wave][t * RF + f][lane];
-        __syncthreads();
-    }
-    if (wave != 0)
-        return;
+    // Every wave adds, in wave order, and stores the blocks of sums that are its
+    // share: 8 blocks at a time, one a wave.
     const float factor = a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
+    constexpr int kBlocks = RT * RF, kTurn = kBlocks < kShrinkWaves ? kBlocks : kShrinkWaves;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
+    for (int turn = 0; turn < kBlocks; turn += kTurn) {
+        if (turn > 0)
+            __syncthreads();
+#pragma unroll
+        for (int b = 0; b < kTurn; ++b)
+            s_acc[wave][b][lane] = acc[(turn + b) / RF][(turn + b) % RF];
+        __syncthreads();
+        if (wave >= kTurn)
+            continue;
+        f32x4_t sum = s_acc[0][wave][lane];
+#pragma unroll
+        for (int i = 1; i < kShrinkWaves; ++i)
+            sum += s_acc[i][wave][lane];
+        // A block's outputs: row t * 16 + m, and ranks f * 16 + 4 g + i or, with
+        // PIECES, (4 g + i) * RF + f.
+        const int t = (turn + wave) / RF, f = (turn + wave) % RF;
+        const int p = tile.p0 + t * 16 + m;
         if (t * 16 + m >= tile.rows)
             continue;
-        float *const h = a.h + split * a.split_stride + (int64_t)(tile.p0 + t * 16 + m) * a.R;
-        // A lane's outputs: 4 ranks a block (f * 16 + 4 g + i), or with PIECES
-        // 4 * RF ranks in a row ((4 g + i) * RF + f).
+        bool bad = false;
 #pragma unroll
-        for (int k = 0; k < RF; ++k) {
-            const int r = PIECES ? 4 * g * RF + 4 * k : k * 16 + 4 * g;
-            f32x4_t v;
+        for (int i = 0; i < RT; ++i)
+            bad |= i == t && bad_row[i];
+        float *const h = a.h + split * a.split_stride + (int64_t)p * a.R;
+        f32x4_t v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float d = PIECES ? acc[t][(4 * k + i) % RF][(4 * k + i) / RF] : acc[t][k][i];
-                v[i] = r + i < rank && !bad_row[t] ? factor * d : 0.0f;
-            }
-            if constexpr (!EDGE) {
-                if (r < a.R)
-                    *reinterpret_cast<f32x4u_t *>(h + r) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (r + i < a.R)
-                        h[r + i] = v[i];
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int r = PIECES ? (4 * g + i) * RF + f : f * 16 + 4 * g + i;
+            v[i] = r < rank && !bad ? factor * sum[i] : 0.0f;
+            if ((EDGE || PIECES) && r < a.R)
+                h[r] = v[i];
         }
+        if (!EDGE && !PIECES && f * 16 + 4 * g < a.R)
+            *reinterpret_cast<f32x4u_t *>(h + f * 16 + 4 * g) = v;
     }
 }
 
@@ -1026,15 +1026,15 @@ template <int DT, bool TR> hipError_t shrink_go(const LoraParams &p, hipStream_t
 template <int DT, bool TR, int NS, bool SMALL>
 hipError_t expand_ns(const LoraParams &p, int64_t tiles, hipStream_t stream)
 {
-    // A column group is at least one pass of a workgroup whose waves deal out
-    // the columns; groups are added until the launch has 8 workgroups a compute
-    // unit, in multiples of the 8 XCDs, so that a group's weights stay in the
-    // L2 of one.
+    // As many passes a workgroup as leave one workgroup for each place on the
+    // chip (its registers allow 3 a compute unit with ranks up to 32, 2 above):
+    // a workgroup takes 5 us before its first pass, and a second, short round
+    // of workgroups would cost a whole one.
     const int pass = 4 * 64;
     const int most = (p.C + pass - 1) / pass;
-    int groups = (int)((2048 + tiles - 1) / tiles);
-    groups = (groups + kXcds - 1) / kXcds * kXcds;
-    groups = groups < most ? groups : most;
+    const int64_t places = 256 * (NS == 1 ? 3 : 2);
+    const int64_t passes = (most * tiles + places - 1) / places;
+    int groups = (int)((most + passes - 1) / passes);
     const int group_cols = ((p.C + groups - 1) / groups + pass - 1) / pass * pass;
     groups = (p.C + group_cols - 1) / group_cols;
     const dim3 grid((unsigned)(tiles * groups)), block(256);
