@@ -199,7 +199,7 @@ def test_lora_workspace_sizes(lib):
     # dh alone up to one chunk of rows, then at most 2 T / chunk partial sums
     assert b(128, 1, 16, 64, 96) == area(128 * 16)
     chunk = 4096 * 64 // 384 // 32 * 32 + 32
-    assert b(4096, 4, 32, 4096, 4096) == (area(4 * 4096 * 32)
+    assert b(4096, 4, 32, 4096, 4096) == (area(4 * 4096 * 32) + 4096 * 32 * 4
                                           + 2 * 4096 // chunk * 32 * 8192 * 4)
     # a size just below what is needed
     need = f(64, 32, 16, 4096, 4096)

@@ -760,7 +760,7 @@ static moegg_status check_lora_sizes(int64_t T, int32_t L, int32_t R, int32_t K,
 // Row stride of a matrix of T rows of n elements.
 static bool stride_ok(int64_t ld, int64_t n, int64_t T)
 {
-    return ld >= n && (T == 0 || ld <= ((int64_t)1 << 39) / T);
+    return ld >= n && ld <= INT32_MAX && (T == 0 || ld <= ((int64_t)1 << 39) / T);
 }
 
 static size_t lora_h_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
@@ -768,6 +768,13 @@ static size_t lora_h_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
     // 32 bytes behind the last row: it is read in pieces of 8 values
     const size_t b = (size_t)moegg::lora_splits(T, L, R, C) * (size_t)T * (size_t)R * sizeof(float);
     return T > 0 ? (b + 32 + 255) / 256 * 256 : 0;
+}
+
+// dh summed over the splits, for the weight gradients.
+static size_t lora_sum_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
+{
+    const size_t b = (size_t)T * (size_t)R * sizeof(float);
+    return moegg::lora_splits(T, L, R, C) > 1 ? (b + 255) / 256 * 256 : 0;
 }
 
 size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
@@ -783,11 +790,12 @@ size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, in
 {
     if (check_lora_sizes(num_rows, num_adapters, R, K, N) != MOEGG_OK)
         return 0;
-    // dh, then the chunks' partial sums: adapters of more than one chunk hold
+    // dh (and its sum over splits), then the chunks' partial sums: adapters of more than one chunk hold
     // fewer than 2 T / chunk of them together
     const int64_t chunk = moegg::lora_chunk(num_rows, R, K, N);
     const size_t parts = num_rows > chunk ? (size_t)(2 * num_rows / chunk) : 0;
     return lora_h_bytes(num_rows, num_adapters, R, N) +
+           lora_sum_bytes(num_rows, num_adapters, R, N) +
            parts * (size_t)R * ((size_t)K + (size_t)N) * sizeof(float);
 }
 
@@ -916,7 +924,12 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     p.w = static_cast<const uint16_t *>(B);
     p.ld_in = lddy;
     p.C = N;
-    hipError_t e = moegg::lora_shrink_launch(p, dtype, true, static_cast<hipStream_t>(stream));
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    hipError_t e = moegg::lora_shrink_launch(p, dtype, true, hs);
+    // dh for the weight gradients: dX's launch adds the splits on its way.
+    char *const after_h = static_cast<char *>(workspace) + lora_h_bytes(num_rows, num_adapters, R, N);
+    const bool split = num_rows > 0 && p.splits > 1;
+    float *const dh = split ? reinterpret_cast<float *>(after_h) : p.h;
     if (e == hipSuccess && dX) {
         p.w = static_cast<const uint16_t *>(A);
         p.C = K;
@@ -924,7 +937,10 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
         p.out = static_cast<uint16_t *>(dX);
         p.ld_base = ld_base;
         p.ld_out = lddx;
-        e = moegg::lora_expand_launch(p, dtype, true, static_cast<hipStream_t>(stream));
+        p.h_out = dA && split ? dh : nullptr;
+        e = moegg::lora_expand_launch(p, dtype, true, hs);
+    } else if (e == hipSuccess && split) {
+        e = moegg::lora_sum_launch(p.h, dh, num_rows * R, p.splits, hs);
     }
     if (e != hipSuccess || !dA)
         return from_hip(e);
@@ -933,23 +949,20 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     g.x = static_cast<const uint16_t *>(X);
     g.dy = static_cast<const uint16_t *>(dY);
     g.h = H;
-    g.dh = p.h;
+    g.dh = dh;
     g.dA = dA;
     g.dB = dB;
-    g.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                           lora_h_bytes(num_rows, num_adapters, R, N));
+    g.partials = reinterpret_cast<float *>(after_h + lora_sum_bytes(num_rows, num_adapters, R, N));
     g.ld_x = ldx;
     g.ld_dy = lddy;
-    g.split_stride = p.split_stride;
     g.R = R;
     g.K = K;
     g.N = N;
-    g.splits = p.splits;
     g.chunk = moegg::lora_chunk(num_rows, R, K, N);
     g.col_tiles_a = (K + 127) / 128;
     g.col_tiles_b = (N + 127) / 128;
     g.fp32_out = flags & MOEGG_LORA_FP32_GRAD;
-    return from_hip(moegg::lora_grad_launch(g, dtype, static_cast<hipStream_t>(stream)));
+    return from_hip(moegg::lora_grad_launch(g, dtype, hs));
 }
 
 }  // extern "C"

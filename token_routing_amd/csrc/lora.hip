@@ -762,7 +762,7 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
 //
 // A step is 8 rows of 16 bytes a lane, issued together; the rows' numbers are
 // loaded a step ahead.  Rows past the chunk's end repeat its last row and are
-// set to zero.  Lanes past the last column load the row's last 8 elements and
+// set to zero.  dh comes summed over shrink's splits.  Lanes past the last column load the row's last 8 elements and
 // store only what is their own.
 template <int DT, int RG>
 __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
@@ -785,7 +785,6 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
     const uint16_t *const big = is_a ? a.x : a.dy;
     const int64_t ld = is_a ? a.ld_x : a.ld_dy;
     const float *const small = is_a ? a.dh : a.h;
-    const int splits = is_a ? a.splits : 1;
     const int rank = rank_of(a.l.ranks, tile.a, a.R);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
@@ -810,34 +809,38 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
     const int p_first = begin + wave * 32;
     if (p_first < end && rt * kRanks < rank) {
         const uint16_t *const big_c = big + min(ct * 128 + m * 8, C - 8);
-        const float *small_r[RG];
+        // Offsets of the lane's 8 rows of `small` in a step, ranks past the
+        // rank clamped; the step's own start is the same for the wave.
+        uint32_t small_at[8];
 #pragma unroll
-        for (int q = 0; q < RG; ++q)
-            small_r[q] = small + min(r0 + q * 16, rank - 1);
+        for (int e = 0; e < 8; ++e)
+            small_at[e] = (uint32_t)((g * 8 + e) * a.R + min(r0, rank - 1));
+        const uint32_t next_block = (uint32_t)(min(r0 + 16, rank - 1) - min(r0, rank - 1));
         auto rows_of = [&](int (&at)[8], int p) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int i = min(p + g * 8 + e, end - 1);
-                at[e] = a.l.gather ? a.l.gather[i] : i;
-            }
+            for (int e = 0; e < 8; ++e)
+                at[e] = min(p + g * 8 + e, end - 1);
+            if (a.l.gather)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    at[e] = a.l.gather[at[e]];
         };
         auto load_small = [&](float (&v)[RG][8], int p) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t o = (int64_t)min(p + g * 8 + e, end - 1) * a.R;
+            const float *const s = small + (int64_t)p * a.R;
+            if (p + 32 <= end) {
 #pragma unroll
                 for (int q = 0; q < RG; ++q)
-                    v[q][e] = small_r[q][o];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[q][e] = s[small_at[e] + (q ? next_block : 0)];
+            } else {
+#pragma unroll
+                for (int q = 0; q < RG; ++q)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[q][e] = s[min(g * 8 + e, end - 1 - p) * a.R +
+                                    min(r0 + q * 16, rank - 1)];
             }
-            for (int s = 1; s < splits; ++s)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t o = (int64_t)min(p + g * 8 + e, end - 1) * a.R +
-                                      s * a.split_stride;
-#pragma unroll
-                    for (int q = 0; q < RG; ++q)
-                        v[q][e] += small_r[q][o];
-                }
         };
         if constexpr (DT == kFp16) {
             float top[RG] = {};
@@ -860,32 +863,43 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
         int at[8];
         rows_of(at, p_first);
         for (int p = p_first; p < end; p += 128) {
-            u32x4_t v[8];
-            float h[RG][8];
             uint32_t rows[8][4];
-            bool ok[8];
+            float h[RG][8];
+            bool ok[8], odd = p + 32 > end;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                ok[e] = at[e] >= 0 && at[e] < a.l.T;
-                v[e] = load8_in(big_c + (int64_t)(ok[e] ? at[e] : 0) * ld);
-                ok[e] = ok[e] && p + g * 8 + e < end;
+                ok[e] = (uint32_t)at[e] < (uint32_t)a.l.T;
+                odd |= !ok[e];
+                // ld is below 2^31: one multiply-add a row
+                const uint16_t *const q =
+                    big_c + (uint64_t)(ok[e] ? (uint32_t)at[e] : 0) * (uint32_t)ld;
+                const u32x4_t v = load8_in(q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rows[e][i] = v[i];
             }
             load_small(h, p);
             rows_of(at, p + 128);
+            if (__ballot(odd))
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 8; ++e) {
+                    ok[e] = ok[e] && p + g * 8 + e < end;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rows[e][i] = ok[e] ? v[e][i] : 0;
+                    for (int i = 0; i < 4; ++i)
+                        rows[e][i] = ok[e] ? rows[e][i] : 0;
+#pragma unroll
+                    for (int q = 0; q < RG; ++q)
+                        h[q][e] = ok[e] ? h[q][e] : 0.0f;
+                }
             u32x4_t hi[RG], lo[RG];
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
+                // Columns of sums past the rank come from a clamped rank and are
+                // set to zero when they are stored.
+                if constexpr (DT == kFp16)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    h[q][e] = ok[e] && r0 + q * 16 < rank ? h[q][e] : 0.0f;
-                    if constexpr (DT == kFp16)
+                    for (int e = 0; e < 8; ++e)
                         h[q][e] *= fit[q];
-                }
                 split8<DT>(h[q], hi[q], lo[q]);
             }
 #pragma unroll
@@ -925,26 +939,88 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
         part = static_cast<float *>(is_a ? a.dA : a.dB) + out0;
     else
         out16 = static_cast<uint16_t *>(is_a ? a.dA : a.dB) + out0;
-    // The columns that LDS column x stands for, and where its own begin.
-    const int ranks_here = min(kRanks, a.R - rt * kRanks);
-    const int cols_here = min(128, C - ct * 128);
-    for (int i = threadIdx.x; i < kRanks * 128; i += 256) {
-        // dA: columns run fastest, dB: ranks.
-        const int x = is_a ? i % 128 : i / kRanks;
-        const int r = is_a ? i / 128 : i % kRanks;
-        if (x >= cols_here || r >= ranks_here)
-            continue;
-        // The piece of 8 that holds column x was moved back to the row's end.
-        const int back = max(ct * 128 + x / 8 * 8 - (C - 8), 0);
-        const float v = factor * (((s_sum[0][r][x + back] + s_sum[1][r][x + back]) +
-                                   s_sum[2][r][x + back]) + s_sum[3][r][x + back]);
-        const int64_t to = is_a ? (int64_t)(rt * kRanks + r) * C + ct * 128 + x
-                                : (int64_t)(ct * 128 + x) * a.R + rt * kRanks + r;
+    auto sum_of = [&](int r, int x) {
+        const float v = ((s_sum[0][r][x] + s_sum[1][r][x]) + s_sum[2][r][x]) + s_sum[3][r][x];
+        return rt * kRanks + r < rank ? factor * v : 0.0f;
+    };
+    auto put = [&](int64_t to, float v) {
         if (part)
             part[to] = v;
         else
             out16[to] = Elem<DT>::narrow(v);
+    };
+    // A thread takes pieces of 8 columns of dA's rows, of 4 ranks of dB's.  The
+    // piece that reaches past column C was moved back: its own columns begin at
+    // `back`, in LDS as everywhere.
+    const int ranks_here = min(kRanks, a.R - rt * kRanks);
+    if (is_a) {
+        for (int i = threadIdx.x; i < kRanks * 16; i += 256) {
+            const int r = i / 16, x = i % 16 * 8;
+            const int c = ct * 128 + x;
+            if (r >= ranks_here || c >= C)
+                continue;
+            const int64_t to = (int64_t)(rt * kRanks + r) * C + min(c, C - 8);
+            const int back = max(c - (C - 8), 0);
+            if (back == 0) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = sum_of(r, x + e);
+                if (part) {
+                    *reinterpret_cast<f32x4u_t *>(part + to) = f32x4_t{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<f32x4u_t *>(part + to + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+                } else {
+                    typename Pack16<DT>::vec_t o;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = Elem<DT>::narrow(v[e]);
+                    *reinterpret_cast<typename Pack16<DT>::vec_t *>(out16 + to) = o;
+                }
+            } else {
+                for (int e = back; e < 8; ++e)
+                    put(to + e, sum_of(r, x + e));
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < kRanks / 4 * 128; i += 256) {
+            const int r = i % (kRanks / 4) * 4, x = i / (kRanks / 4);
+            const int c = ct * 128 + x;
+            if (r >= ranks_here || c >= C)
+                continue;
+            const int back = max(ct * 128 + x / 8 * 8 - (C - 8), 0);
+            const int64_t to = (int64_t)c * a.R + rt * kRanks + r;
+            if (r + 4 <= ranks_here) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = sum_of(r + e, x + back);
+                if (part) {
+                    *reinterpret_cast<f32x4u_t *>(part + to) = f32x4_t{v[0], v[1], v[2], v[3]};
+                } else {
+                    typedef uint16_t half_t __attribute__((ext_vector_type(4), aligned(2)));
+                    *reinterpret_cast<half_t *>(out16 + to) =
+                        half_t{Elem<DT>::narrow(v[0]), Elem<DT>::narrow(v[1]),
+                               Elem<DT>::narrow(v[2]), Elem<DT>::narrow(v[3])};
+                }
+            } else {
+                for (int e = 0; r + e < ranks_here; ++e)
+                    put(to + e, sum_of(r + e, x + back));
+            }
+        }
     }
+}
+
+// h summed over the splits (dh for the gradients, where no expand sums it).
+__global__ __launch_bounds__(256) void sum_splits_kernel(const float *h, float *out, int64_t n,
+                                                         int splits)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n)
+        return;
+    float v = h[i];
+    for (int s = 1; s < splits; ++s)
+        v += h[s * n + i];
+    out[i] = v;
 }
 
 // Adds the partials of adapters with several chunks, in chunk order, 4
@@ -1102,6 +1178,13 @@ hipError_t lora_expand_launch(const LoraParams &p, int dtype, bool transposed, h
     if (dtype == kBf16)
         return transposed ? expand_go<kBf16, true>(p, stream) : expand_go<kBf16, false>(p, stream);
     return transposed ? expand_go<kFp16, true>(p, stream) : expand_go<kFp16, false>(p, stream);
+}
+
+hipError_t lora_sum_launch(const float *h, float *out, int64_t n, int splits, hipStream_t stream)
+{
+    hipLaunchKernelGGL(sum_splits_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
+                       h, out, n, splits);
+    return hipGetLastError();
 }
 
 hipError_t lora_grad_launch(const GradParams &p, int dtype, hipStream_t stream)

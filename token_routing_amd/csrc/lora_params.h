@@ -37,8 +37,8 @@ struct GradParams {
     void *dA;
     void *dB;
     float *partials;
-    int64_t ld_x, ld_dy, split_stride;
-    int R, K, N, splits, chunk;
+    int64_t ld_x, ld_dy;
+    int R, K, N, chunk;
     int col_tiles_a, col_tiles_b;  // 128-column tiles of dA and dB (0: not wanted)
     bool fp32_out;
 };
@@ -47,7 +47,7 @@ struct GradParams {
 // sums of the tile in 64 registers.
 __host__ __device__ constexpr int shrink_blocks(int R)
 {
-    return R <= 64 ? 4 : R <= 128 ? 2 : 1;
+    return R <= 32 ? 2 : R <= 64 ? 4 : R <= 128 ? 2 : 1;
 }
 
 // Rows of a shrink tile: one block of 16, or a large tile where an adapter has
@@ -84,6 +84,7 @@ inline int lora_chunk(int64_t T, int R, int K, int N)
 
 hipError_t lora_shrink_launch(const LoraParams &p, int dtype, bool transposed, hipStream_t stream);
 hipError_t lora_expand_launch(const LoraParams &p, int dtype, bool transposed, hipStream_t stream);
+hipError_t lora_sum_launch(const float *h, float *out, int64_t n, int splits, hipStream_t stream);
 hipError_t lora_grad_launch(const GradParams &p, int dtype, hipStream_t stream);
 
 }  // namespace moegg
