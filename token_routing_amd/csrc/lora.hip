@@ -270,16 +270,16 @@ __device__ __forceinline__ void load_h(float (&v)[8], const float *h, int64_t p,
     const float *q = h + p * R + (col < n ? col : 0);
     f32x4_t a = *reinterpret_cast<const f32x4u_t *>(q);
     f32x4_t b = *reinterpret_cast<const f32x4u_t *>(q + 4);
-    for (int s = 1; s < splits; s += 4) {
-        f32x4_t c[4], d[4];  // four splits' loads at once, the last one's again past the end
+    for (int s = 1; s < splits; s += 2) {
+        f32x4_t c[2], d[2];  // two splits' loads at once, the last one's again past the end
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
             const float *const r = q + min(s + u, splits - 1) * split_stride;
             c[u] = *reinterpret_cast<const f32x4u_t *>(r);
             d[u] = *reinterpret_cast<const f32x4u_t *>(r + 4);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u)
             if (s + u < splits) {
                 a += c[u];
                 b += d[u];
@@ -488,15 +488,16 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // instructions and its base as this one's is used, in the order in which they
 // are waited for.  SMALL: ranks up to 16, both parts of
 // h in one instruction.  EDGE: columns that are no whole passes (the last one
-// goes by single elements, a row at a time) or, forward, ranks that are no
-// whole pieces of 8.
+// goes by single elements, a row at a time) or ranks that are no whole pieces
+// of 8.
 template <int DT, bool TR, int NS, bool SMALL, bool EDGE>
-__global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups, int group_cols)
+__global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams a, int groups, int group_cols)
 {
     constexpr int F = 4;
     constexpr int kCols = F * 16;
     constexpr int RT = kExpandRows / 16;
     constexpr int kPad = kCols + 4;
+    constexpr bool STEPWISE = NS > 2;
     __shared__ u32x4_t s_h[NS][RT][SMALL ? 1 : 2][kWave];
     __shared__ __attribute__((aligned(16))) float s_out[4][16][kPad];
     __shared__ int s_src[kExpandRows];
@@ -539,7 +540,7 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
     // A step's weights of the lane, as loaded: forward 4 fragments, TR 8 rows
     // of 4 columns.  Every address lies inside the adapter's weights.
     const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
-    uint32_t raw[NS][8][2];
+    uint32_t raw[STEPWISE ? 2 : NS][8][2];
     auto load_weights = [&](uint32_t (&v)[8][2], int s, int c0) {
         const int r0 = s * 32 + rg;
         if constexpr (TR) {
@@ -562,19 +563,22 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
         }
     };
 
-    // The summed h for the caller, by the first column group.
-    if (a.h_out && group == 0)
-        for (int i = threadIdx.x; i < tile.rows * a.R; i += 256) {
-            const float *q = a.h + (int64_t)tile.p0 * a.R + i;
-            float v = *q;
-            for (int s = 1; s < a.splits; ++s) {
-                q += a.split_stride;
-                v += *q;
-            }
-            a.h_out[(int64_t)tile.p0 * a.R + i] = v;
-        }
-    if (rank == 0 && a.base == a.out)
-        return;
+    // Weights first, then base, then h: all in flight together, and base does
+    // not wait for the conversion of h.  (Above rank 64 the registers hold
+    // only one of them at a time.)
+    auto load_first = [&] {
+        if (c_begin >= c_end)
+            return;
+#pragma unroll
+        for (int s = 0; s < (STEPWISE ? 1 : NS); ++s)
+            load_weights(raw[s], s, c_begin);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+            if (t < blocks)
+                load_base(t, c_begin);
+    };
+    if constexpr (!STEPWISE)
+        load_first();
     if (wave < blocks) {
         const int t = wave * 16 + m;
         const int p = tile.p0 + min(t, tile.rows - 1);
@@ -583,6 +587,23 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
 #pragma unroll
         for (int s = 0; s < NS; ++s)
             load_h(v[s], a.h, p, a.R, s * 32 + rg, rank, a.splits, a.split_stride);
+        // The summed h for the caller, by the first column group.
+        if (a.h_out && group == 0 && t < tile.rows && (!SMALL || g < 2))
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const int r = s * 32 + rg;
+                float *const q = a.h_out + (int64_t)p * a.R + r;
+                if (!EDGE && r < a.R) {
+                    *reinterpret_cast<f32x4u_t *>(q) = f32x4_t{v[s][0], v[s][1], v[s][2], v[s][3]};
+                    *reinterpret_cast<f32x4u_t *>(q + 4) =
+                        f32x4_t{v[s][4], v[s][5], v[s][6], v[s][7]};
+                } else if (EDGE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (r + i < a.R)
+                            q[i] = v[s][i];
+                }
+            }
         if constexpr (DT == kFp16) {
             float top = 0.0f;
 #pragma unroll
@@ -619,17 +640,10 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
                 s_src[t] = t < tile.rows && x >= 0 && x < a.T ? x : -1;
         }
     }
-    if (c_begin < c_end) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-            load_weights(raw[s], s, c_begin);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-            if (t < blocks)
-                load_base(t, c_begin);
-    }
+    if constexpr (STEPWISE)
+        load_first();
     __syncthreads();
-    if (c_begin >= c_end)
+    if (c_begin >= c_end || (rank == 0 && a.base == a.out))
         return;
 
     // One pass.  FULL: all row blocks are there; MORE: another pass follows.
@@ -637,44 +651,78 @@ __global__ __launch_bounds__(256, 2) void expand_kernel(LoraParams a, int groups
     // later wait count as if it had not been issued.
     auto pass = [&](int c0, auto full_c, auto more_c) {
         constexpr bool FULL = decltype(full_c)::value, MORE = decltype(more_c)::value;
-        // Fragments; ranks at or past the rank may hold anything.
-        u32x4_t wf[NS][F];
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        // Fragments of a step; ranks at or past the rank may hold anything.
+        auto fragments = [&](u32x4_t (&wf)[F], const uint32_t (&v)[8][2], int s) {
             const int left = rank - (s * 32 + rg);
 #pragma unroll
             for (int f = 0; f < F; ++f) {
                 if constexpr (TR)
-                    wf[s][f] = column<4>(raw[s], f);
+                    wf[f] = column<4>(v, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if constexpr (!TR)
-                        wf[s][f][i] = raw[s][(4 * f + i) / 2][(4 * f + i) % 2];
-                    wf[s][f][i] &= left > 2 * i + 1 ? ~0u : left > 2 * i ? 0xffffu : 0u;
+                        wf[f][i] = v[(4 * f + i) / 2][(4 * f + i) % 2];
+                    wf[f][i] &= left > 2 * i + 1 ? ~0u : left > 2 * i ? 0xffffu : 0u;
                 }
             }
+        };
+        auto multiply = [&](f32x4_t (&acc)[F], const u32x4_t (&wf)[F], int s, int t) {
+#pragma unroll
+            for (int part = 0; part < (SMALL ? 1 : 2); ++part) {
+                const u32x4_t h = s_h[s][t][part][lane];
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    acc[f] = mfma<DT>(wf[f], h, acc[f]);
+            }
+        };
+        // Up to rank 64 a pass's weights are all in registers, and one block's
+        // sums at a time; above, all blocks' sums, and two steps' weights.
+        u32x4_t wf[STEPWISE ? 1 : NS][F];
+        f32x4_t acc_all[STEPWISE ? RT : 1][F];
+        if constexpr (STEPWISE) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int f = 0; f < F; ++f)
+                    acc_all[t][f] = f32x4_t{};
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                if (s + 1 < NS)
+                    load_weights(raw[(s + 1) & 1], s + 1, c0);
+                fragments(wf[0], raw[s & 1], s);
+                if (MORE && s + 1 == NS)
+                    load_weights(raw[0], 0, c0 + 4 * kCols);
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+                    if (FULL || t < blocks)
+                        multiply(acc_all[t], wf[0], s, t);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+                fragments(wf[s], raw[s], s);
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             if (!FULL && t >= blocks)
                 break;
             f32x4_t acc[F];
+            if constexpr (STEPWISE) {
 #pragma unroll
-            for (int f = 0; f < F; ++f)
-                acc[f] = f32x4_t{};
+                for (int f = 0; f < F; ++f)
+                    acc[f] = acc_all[t][f];
+            } else {
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int part = 0; part < (SMALL ? 1 : 2); ++part) {
-                    const u32x4_t h = s_h[s][t][part][lane];
-#pragma unroll
-                    for (int f = 0; f < F; ++f)
-                        acc[f] = mfma<DT>(wf[s][f], h, acc[f]);
-                }
-            if (MORE && t == (FULL ? RT : blocks) - 1)
+                for (int f = 0; f < F; ++f)
+                    acc[f] = f32x4_t{};
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
-                    load_weights(raw[s], s, c0 + 4 * kCols);
+                    multiply(acc, wf[s], s, t);
+                if (MORE && t == (FULL ? RT : blocks) - 1)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        load_weights(raw[s], s, c0 + 4 * kCols);
+            }
             // A lane holds row m, columns f * 16 + 4 g + i (TR: (4 g + i) * 4 + f).
             const bool inside = !EDGE || MORE || c0 + kCols <= a.C;
             if (!TR || inside) {
@@ -1114,7 +1162,7 @@ hipError_t expand_ns(const LoraParams &p, int64_t tiles, hipStream_t stream)
     const int group_cols = ((p.C + groups - 1) / groups + pass - 1) / pass * pass;
     groups = (p.C + group_cols - 1) / group_cols;
     const dim3 grid((unsigned)(tiles * groups)), block(256);
-    if (p.C % 64 || (!TR && p.R % 8))
+    if (p.C % 64 || p.R % 8)
         hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, true>), grid, block, 0, stream, p,
                            groups, group_cols);
     else
