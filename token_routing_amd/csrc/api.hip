@@ -750,7 +750,7 @@ static moegg_status check_lora_sizes(int64_t T, int32_t L, int32_t R, int32_t K,
     if ((int64_t)L * R > kMax / wide || (T > 0 && wide > kMax / T))
         return MOEGG_ESHAPE;
     const int64_t cols = wide / 128 + 1;
-    const int64_t shrink = (T / 16 + 1 + L) * 16, expand = (T / 64 + 1 + L) * cols;
+    const int64_t shrink = (T / 16 + 1 + L) * 16, expand = (T / 16 + 1 + L) * cols;
     const int64_t grad = (L + T / moegg::lora_chunk(T, R, K, N)) * (2 * cols) * ((R + 15) / 16);
     if (shrink > INT32_MAX || expand > INT32_MAX || grad > INT32_MAX)
         return MOEGG_ESHAPE;

@@ -477,8 +477,9 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // out[src(p), c] = base[src(p), c] + factor * sum_r h[p, r] * w(r, c), w(r, c)
 // = W[c][r] (W [C, R], forward) or W[r][c] (W [R, C], TR).
 //
-// A workgroup takes up to 64 rows of one adapter and a run of columns, its
-// waves 64 columns each at a time.  h is split into its two parts once and
+// A workgroup takes up to RT * 16 rows of one adapter and a run of columns, its
+// waves 64 columns each at a time; rows past the tile's repeat its last one and
+// are not stored.  h is split into its two parts once and
 // kept in LDS as fragments (NS steps of 32 ranks).  A wave's pass: the
 // weights' fragments (each used for all rows), the matrix instructions, and
 // the sums through a strip of LDS into row order, so that base is read and
@@ -490,21 +491,20 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // h in one instruction.  EDGE: columns that are no whole passes (the last one
 // goes by single elements, a row at a time) or ranks that are no whole pieces
 // of 8.
-template <int DT, bool TR, int NS, bool SMALL, bool EDGE>
-__global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams a, int groups, int group_cols)
+template <int DT, bool TR, int NS, bool SMALL, int RT, bool EDGE>
+__global__ __launch_bounds__(256, RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 ? 3 : 2) void expand_kernel(LoraParams a, int groups, int group_cols)
 {
     constexpr int F = 4;
     constexpr int kCols = F * 16;
-    constexpr int RT = kExpandRows / 16;
+    constexpr int kRows = RT * 16;
     constexpr int kPad = kCols + 4;
     constexpr bool STEPWISE = NS > 2;
     __shared__ u32x4_t s_h[NS][RT][SMALL ? 1 : 2][kWave];
     __shared__ __attribute__((aligned(16))) float s_out[4][16][kPad];
-    __shared__ int s_src[kExpandRows];
-    __shared__ float s_factor[kExpandRows];
+    __shared__ int s_src[kRows];
+    __shared__ float s_factor[kRows];
     Tile tile;
-    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / groups, kExpandRows, 0, false,
-                   tile))
+    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / groups, kRows, 0, false, tile))
         return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
@@ -512,7 +512,6 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
     const int group = blockIdx.x % groups;
     const int rank = rank_of(a.ranks, tile.a, a.R);
     const int rg = SMALL ? (g & 1) * 8 : g * 8;  // this lane's ranks of a step
-    const int blocks = (tile.rows + 15) / 16;
 
     // In row order a lane holds 8 columns of rows lane / 8 and lane / 8 + 8 of
     // a block.  A bad gather entry (shrink reports it) has no row.
@@ -574,12 +573,11 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
             load_weights(raw[s], s, c_begin);
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-            if (t < blocks)
-                load_base(t, c_begin);
+            load_base(t, c_begin);
     };
     if constexpr (!STEPWISE)
         load_first();
-    if (wave < blocks) {
+    if (wave < RT) {
         const int t = wave * 16 + m;
         const int p = tile.p0 + min(t, tile.rows - 1);
         float factor = !a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
@@ -646,11 +644,10 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
     if (c_begin >= c_end || (rank == 0 && a.base == a.out))
         return;
 
-    // One pass.  FULL: all row blocks are there; MORE: another pass follows.
-    // Both are fixed at compile time, since a load under a branch makes every
-    // later wait count as if it had not been issued.
-    auto pass = [&](int c0, auto full_c, auto more_c) {
-        constexpr bool FULL = decltype(full_c)::value, MORE = decltype(more_c)::value;
+    // One pass.  MORE: another one follows, fixed at compile time, since a load
+    // under a branch makes every later wait count as if it had not been issued.
+    auto pass = [&](int c0, auto more_c) {
+        constexpr bool MORE = decltype(more_c)::value;
         // Fragments of a step; ranks at or past the rank may hold anything.
         auto fragments = [&](u32x4_t (&wf)[F], const uint32_t (&v)[8][2], int s) {
             const int left = rank - (s * 32 + rg);
@@ -694,8 +691,7 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
                     load_weights(raw[0], 0, c0 + 4 * kCols);
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    if (FULL || t < blocks)
-                        multiply(acc_all[t], wf[0], s, t);
+                    multiply(acc_all[t], wf[0], s, t);
             }
         } else {
 #pragma unroll
@@ -704,8 +700,6 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            if (!FULL && t >= blocks)
-                break;
             f32x4_t acc[F];
             if constexpr (STEPWISE) {
 #pragma unroll
@@ -718,7 +712,7 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
                     multiply(acc, wf[s], s, t);
-                if (MORE && t == (FULL ? RT : blocks) - 1)
+                if (MORE && t == RT - 1)
 #pragma unroll
                     for (int s = 0; s < NS; ++s)
                         load_weights(raw[s], s, c0 + 4 * kCols);
@@ -787,15 +781,9 @@ __global__ __launch_bounds__(256, NS == 1 ? 3 : 2) void expand_kernel(LoraParams
         }
     };
     int c0 = c_begin;
-    if (blocks == RT) {
-        for (; c0 + 4 * kCols < c_end; c0 += 4 * kCols)
-            pass(c0, std::true_type{}, std::true_type{});
-        pass(c0, std::true_type{}, std::false_type{});
-    } else {
-        for (; c0 + 4 * kCols < c_end; c0 += 4 * kCols)
-            pass(c0, std::false_type{}, std::true_type{});
-        pass(c0, std::false_type{}, std::false_type{});
-    }
+    for (; c0 + 4 * kCols < c_end; c0 += 4 * kCols)
+        pass(c0, std::true_type{});
+    pass(c0, std::false_type{});
 }
 
 // ---------------------------------------------------------------- grad
@@ -1147,42 +1135,49 @@ template <int DT, bool TR> hipError_t shrink_go(const LoraParams &p, hipStream_t
     return shrink_rf<DT, TR, 16>(p, stream);
 }
 
-template <int DT, bool TR, int NS, bool SMALL>
-hipError_t expand_ns(const LoraParams &p, int64_t tiles, hipStream_t stream)
+template <int DT, bool TR, int NS, bool SMALL, int RT>
+hipError_t expand_rt(const LoraParams &p, hipStream_t stream)
 {
     // As many passes a workgroup as leave one workgroup for each place on the
-    // chip (its registers allow 3 a compute unit with ranks up to 32, 2 above):
-    // a workgroup takes 5 us before its first pass, and a second, short round
-    // of workgroups would cost a whole one.
+    // chip (its registers allow 3 a compute unit with ranks up to 32, 2 above,
+    // 4 and 3 with one block of rows): a workgroup takes 4 us before its first
+    // pass, and a second, short round of workgroups would cost a whole one.
+    const int64_t tiles = (p.T + RT * 16 - 1) / (RT * 16) + (p.T < p.L ? p.T : p.L);
     const int pass = 4 * 64;
     const int most = (p.C + pass - 1) / pass;
-    const int64_t places = 256 * (NS == 1 ? 3 : 2);
+    const int64_t places = 256 * (RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 ? 3 : 2);
     const int64_t passes = (most * tiles + places - 1) / places;
     int groups = (int)((most + passes - 1) / passes);
     const int group_cols = ((p.C + groups - 1) / groups + pass - 1) / pass * pass;
     groups = (p.C + group_cols - 1) / group_cols;
     const dim3 grid((unsigned)(tiles * groups)), block(256);
     if (p.C % 64 || p.R % 8)
-        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, true>), grid, block, 0, stream, p,
+        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, RT, true>), grid, block, 0, stream, p,
                            groups, group_cols);
     else
-        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, false>), grid, block, 0, stream, p,
+        hipLaunchKernelGGL((expand_kernel<DT, TR, NS, SMALL, RT, false>), grid, block, 0, stream, p,
                            groups, group_cols);
     return hipGetLastError();
 }
 
+template <int DT, bool TR, int NS, bool SMALL>
+hipError_t expand_ns(const LoraParams &p, hipStream_t stream)
+{
+    return lora_many_rows(p.T, p.L) ? expand_rt<DT, TR, NS, SMALL, 4>(p, stream)
+                                    : expand_rt<DT, TR, NS, SMALL, 1>(p, stream);
+}
+
 template <int DT, bool TR> hipError_t expand_go(const LoraParams &p, hipStream_t stream)
 {
-    const int64_t tiles = (p.T + kExpandRows - 1) / kExpandRows + (p.T < p.L ? p.T : p.L);
     if (p.R <= 16)
-        return expand_ns<DT, TR, 1, true>(p, tiles, stream);
+        return expand_ns<DT, TR, 1, true>(p, stream);
     if (p.R <= 32)
-        return expand_ns<DT, TR, 1, false>(p, tiles, stream);
+        return expand_ns<DT, TR, 1, false>(p, stream);
     if (p.R <= 64)
-        return expand_ns<DT, TR, 2, false>(p, tiles, stream);
+        return expand_ns<DT, TR, 2, false>(p, stream);
     if (p.R <= 128)
-        return expand_ns<DT, TR, 4, false>(p, tiles, stream);
-    return expand_ns<DT, TR, 8, false>(p, tiles, stream);
+        return expand_ns<DT, TR, 4, false>(p, stream);
+    return expand_ns<DT, TR, 8, false>(p, stream);
 }
 
 template <int DT> hipError_t grad_go(const GradParams &p, hipStream_t stream)

@@ -7,8 +7,6 @@
 
 namespace moegg {
 
-constexpr int kExpandRows = 64;   // rows of an expand tile
-
 // Shrink (in, w -> h) and expand (h, w, base -> out) of T rows; C is the wide
 // dimension: columns of `in` or of `out`.
 struct LoraParams {
@@ -50,12 +48,16 @@ __host__ __device__ constexpr int shrink_blocks(int R)
     return R <= 32 ? 2 : R <= 64 ? 4 : R <= 128 ? 2 : 1;
 }
 
-// Rows of a shrink tile: one block of 16, or a large tile where an adapter has
-// 32 rows or more on average.
+// Tiles are one block of 16 rows, or large where an adapter has 32 rows or more
+// on average.
+inline bool lora_many_rows(int64_t T, int L)
+{
+    return T >= 32 * (T < L ? T : L);
+}
+
 inline int lora_shrink_rows(int64_t T, int L, int R)
 {
-    const int64_t n = T < L ? T : L;
-    return T >= 32 * n ? 16 * shrink_blocks(R) : 16;
+    return lora_many_rows(T, L) ? 16 * shrink_blocks(R) : 16;
 }
 
 // Shrink splits: how many workgroups share a tile's reduction of C columns.
