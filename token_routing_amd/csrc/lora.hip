@@ -491,8 +491,13 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // h in one instruction.  EDGE: columns that are no whole passes (the last one
 // goes by single elements, a row at a time) or ranks that are no whole pieces
 // of 8.
+constexpr int expand_places(bool TR, int NS, int RT)
+{
+    return RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 || (NS == 2 && !TR) ? 3 : 2;
+}
+
 template <int DT, bool TR, int NS, bool SMALL, int RT, bool EDGE>
-__global__ __launch_bounds__(256, RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 ? 3 : 2) void expand_kernel(LoraParams a, int groups, int group_cols)
+__global__ __launch_bounds__(256, expand_places(TR, NS, RT)) void expand_kernel(LoraParams a, int groups, int group_cols)
 {
     constexpr int F = 4;
     constexpr int kCols = F * 16;
@@ -1139,13 +1144,12 @@ template <int DT, bool TR, int NS, bool SMALL, int RT>
 hipError_t expand_rt(const LoraParams &p, hipStream_t stream)
 {
     // As many passes a workgroup as leave one workgroup for each place on the
-    // chip (its registers allow 3 a compute unit with ranks up to 32, 2 above,
-    // 4 and 3 with one block of rows): a workgroup takes 4 us before its first
+    // chip (expand_places a compute unit, by its registers): a workgroup takes 4 us before its first
     // pass, and a second, short round of workgroups would cost a whole one.
     const int64_t tiles = (p.T + RT * 16 - 1) / (RT * 16) + (p.T < p.L ? p.T : p.L);
     const int pass = 4 * 64;
     const int most = (p.C + pass - 1) / pass;
-    const int64_t places = 256 * (RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 ? 3 : 2);
+    const int64_t places = 256 * expand_places(TR, NS, RT);
     const int64_t passes = (most * tiles + places - 1) / places;
     int groups = (int)((most + passes - 1) / passes);
     const int group_cols = ((p.C + groups - 1) / groups + pass - 1) / pass * pass;
