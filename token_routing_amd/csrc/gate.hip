@@ -9,7 +9,8 @@
 //
 // A token is held by G = 8 to 64 lanes of one wave, V logits a lane, all in
 // registers: the logits are read once, and maxima, sums and the k picks are
-// reductions over the G lanes.  Both scores rise with the logit, so without
+// reductions over the G lanes, which bound the kernel (its bytes would take a
+// tenth of the time).  Both scores rise with the logit, so without
 // bias and groups the picks compare the logits themselves and need no exp;
 // with them the keys are computed and compared in 64 bits, because keys of
 // different experts come as close as a rounding of 32 bits and the pick must
@@ -34,14 +35,56 @@ constexpr int kGateThreads = 256;
 constexpr int kErrLogit = 8;  // MOEGG_DERR_LOGIT
 constexpr float kNegInf = -__builtin_huge_valf();
 
-template <int G> __device__ __forceinline__ float lanes_max(float v)
+// Every lane of a group of G combined with op (commutative), all lanes ending
+// with the result: moves inside the registers (quad and mirror moves up to 16
+// lanes, row and half exchanges above).  The same through LDS shifts took four
+// fifths of a call's time.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
-#pragma unroll
-    for (int d = G / 2; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor(v, d, kWave));
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
+}
+template <int G, class Op> __device__ __forceinline__ uint32_t lanes_combine(uint32_t v, Op op)
+{
+    v = op(v, dpp<0xb1>(v));   // quad_perm [1,0,3,2]
+    v = op(v, dpp<0x4e>(v));   // quad_perm [2,3,0,1]
+    v = op(v, dpp<0x141>(v));  // row_half_mirror
+    if constexpr (G >= 16)
+        v = op(v, dpp<0x140>(v));  // row_mirror
+    if constexpr (G >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+    }
+    if constexpr (G >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+    }
     return v;
 }
-template <int G, class T> __device__ __forceinline__ T lanes_sum(T v)
+template <int G> __device__ __forceinline__ uint32_t lanes_umax(uint32_t v)
+{
+    return lanes_combine<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int G> __device__ __forceinline__ uint32_t lanes_umin(uint32_t v)
+{
+    return lanes_combine<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int G> __device__ __forceinline__ float lanes_max(float v)
+{
+    return __builtin_bit_cast(
+        float, lanes_combine<G>(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+            return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a),
+                                                      __builtin_bit_cast(float, b)));
+        }));
+}
+template <int G> __device__ __forceinline__ float lanes_sum(float v)
+{
+    return __builtin_bit_cast(
+        float, lanes_combine<G>(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+            return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, a) +
+                                                    __builtin_bit_cast(float, b));
+        }));
+}
+template <int G> __device__ __forceinline__ double lanes_sum(double v)
 {
 #pragma unroll
     for (int d = G / 2; d > 0; d >>= 1)
@@ -181,6 +224,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
     constexpr int kSlots = V == 1 ? 1 : 64 / G;  // picks a lane can hold
     __shared__ double s_key[WIDE ? kTokens * G * V : 1];
     __shared__ double s_group[WIDE ? kTokens * 64 : 1];
+    __shared__ int s_keep[WIDE ? kTokens * 64 : 1];
     const int lane = threadIdx.x % G;
     const int slot = threadIdx.x / G;
     const int64_t t = (int64_t)blockIdx.x * kTokens + slot;
@@ -222,16 +266,13 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
             store_row_f32<V>(a.scores + t * a.E, p, lane, a.E);
     }
 
-    // Keys: 0 cannot be picked.  Without WIDE a key holds the logit's order
-    // bits and the complement of the expert's index: one maximum finds the
-    // largest logit and, among equals, the lowest index.
-    uint64_t key[V];
+    // Keys as order bits; 0 cannot be picked.  Without WIDE they are the
+    // logits' and fit the high word.
+    uint32_t key[V], low[WIDE ? V : 1];
     if constexpr (!WIDE) {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            key[v] = l[v] > kNegInf
-                         ? (uint64_t)order_bits(l[v]) << 32 | (uint32_t)~(uint32_t)(lane * V + v)
-                         : 0;
+            key[v] = l[v] > kNegInf ? order_bits(l[v]) : 0;
     } else {
         double d[V], dsum = 1.0;
         if (a.sigmoid) {
@@ -261,35 +302,49 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
                 ok &= fabsf(b) < __builtin_huge_valf();
                 d[v] += (double)b;
             }
-            key[v] = ok ? order_bits(d[v]) : 0;
+            const uint64_t bits = ok ? order_bits(d[v]) : 0;
+            key[v] = (uint32_t)(bits >> 32);
+            low[v] = (uint32_t)bits;
             my[e] = ok ? d[v] : -__builtin_huge_val();
         }
         if (a.n_groups > 1) {
             const int per = a.E / a.n_groups;
             double *const val = s_group + slot * 64;
+            int *const keep = s_keep + slot * 64;
             __syncthreads();
             for (int g = lane; g < a.n_groups; g += G) {
                 double first = -__builtin_huge_val(), second = first;
-                for (int i = 0; i < per; ++i) {
-                    const double x = my[g * per + i];
-                    second = fmax(second, fmin(first, x));
-                    first = fmax(first, x);
+                for (int i = 0; i < per; i += 4) {
+                    double x[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        x[u] = i + u < per ? my[g * per + i + u] : -__builtin_huge_val();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        second = fmax(second, fmin(first, x[u]));
+                        first = fmax(first, x[u]);
+                    }
                 }
                 val[g] = second > -__builtin_huge_val() ? first + second : first;
             }
             __syncthreads();
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = lane * V + v;
-                if (e >= a.E)
-                    continue;
-                const int g = e / per;
+            for (int g = lane; g < a.n_groups; g += G) {
                 const double mine = val[g];
                 int ahead = 0;  // groups that come before this one
                 for (int h = 0; h < a.n_groups; ++h)
                     ahead += val[h] > mine || (val[h] == mine && h < g);
-                if (ahead >= a.topk_groups)
+                keep[g] = ahead < a.topk_groups;
+            }
+            __syncthreads();
+            int g = lane * V / per, at = lane * V - g * per;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (lane * V + v < a.E && !keep[g])
                     key[v] = 0;
+                if (++at == per) {
+                    at = 0;
+                    ++g;
+                }
             }
         }
     }
@@ -304,55 +359,42 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
         pick_l[s] = kNegInf;
     }
     for (int j = 0; j < a.topk; ++j) {
-        uint64_t best = 0;
-        int id = -1;
+        // The largest key, then the lowest index among those that have it.
+        uint32_t best = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            best = key[v] > best ? key[v] : best;
+        best = lanes_umax<G>(best);
+        uint32_t best_low = 0;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                best_low = key[v] == best && low[v] > best_low ? low[v] : best_low;
+            best_low = lanes_umax<G>(best_low);
+        }
+        uint32_t at = 0xffffffffu;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+            if (key[v] == best && (!WIDE || low[WIDE ? v : 0] == best_low))
+                at = lane * V + v;
+        at = lanes_umin<G>(at);
+        const int id = best ? (int)at : -1;
         float lv = kNegInf;
         if constexpr (!WIDE) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                best = key[v] > best ? key[v] : best;
-#pragma unroll
-            for (int d = G / 2; d > 0; d >>= 1) {
-                const uint64_t o = __shfl_xor((unsigned long long)best, d, kWave);
-                best = o > best ? o : best;
-            }
-            if (best) {
-                id = (int)~(uint32_t)best;
-                lv = from_order_bits((uint32_t)(best >> 32));
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (key[v] == best)
-                    key[v] = 0;
+            lv = best ? from_order_bits(best) : kNegInf;
         } else {
-            int at = 0x7fffffff;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (key[v] > best) {
-                    best = key[v];
-                    at = lane * V + v;
-                    lv = l[v];
-                }
-#pragma unroll
-            for (int d = G / 2; d > 0; d >>= 1) {
-                const uint64_t o = __shfl_xor((unsigned long long)best, d, kWave);
-                const int oat = __shfl_xor(at, d, kWave);
-                const float ol = __shfl_xor(lv, d, kWave);
-                if (o > best || (o == best && oat < at)) {
-                    best = o;
-                    at = oat;
-                    lv = ol;
-                }
-            }
-            if (best)
-                id = at;
-            else
-                lv = kNegInf;
+            uint32_t mine = 0;  // the owner's logit, found by all
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (lane * V + v == id)
-                    key[v] = 0;
+                    mine = __builtin_bit_cast(uint32_t, l[v]);
+            mine = lanes_combine<G>(mine, [](uint32_t a, uint32_t b) { return a | b; });
+            lv = best ? __builtin_bit_cast(float, mine) : kNegInf;
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane * V + v == id)
+                key[v] = 0;
 #pragma unroll
         for (int s = 0; s < kSlots; ++s)
             if (j == s * G + lane) {
@@ -493,20 +535,24 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd_kernel(GateBwdParams a)
     for (int v = 0; v < V; ++v)
         add[v] = 0.0f;
     const int base = (threadIdx.x & (kWave - 1)) - lane;
-    for (int j = 0; j < a.topk; ++j) {
-        int e = -1;
-        float c = 0.0f;
+    // Pick j's expert and share from its lane; the picks past topk hold -1.
 #pragma unroll
-        for (int s = 0; s < kSlots; ++s)
-            if (j / G == s) {
-                e = __shfl(id[s], base + j % G, kWave);
-                c = __shfl(into[s], base + j % G, kWave);
+    for (int s = 0; s < kSlots; ++s)
+        for (int j0 = 0; j0 < min(G, a.topk - s * G); j0 += 4) {
+            int e[4];
+            float c[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                e[u] = __shfl(id[s], base + j0 + u, kWave);
+                c[u] = __shfl(into[s], base + j0 + u, kWave);
             }
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane * V + v == e)
-                add[v] += c;
-    }
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (lane * V + v == e[u])
+                        add[v] += c[u];
+        }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (a.renorm)
