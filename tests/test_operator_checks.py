@@ -192,14 +192,15 @@ def test_lora_workspace_sizes(lib):
 
     # 64 rows over 32 adapters: 36 tiles of 16 rows, 8 workgroups a tile
     assert f(64, 32, 16, 4096, 4096) == area(8 * 64 * 16)
-    # 136 tiles of 64 rows: two workgroups a tile
-    assert f(8192, 8, 64, 4096, 4096) == area(2 * 8192 * 64)
+    # 72 tiles of 32 rows: four workgroups a tile; 264 of them: one each
+    assert f(2048, 8, 64, 4096, 4096) == area(4 * 2048 * 64)
+    assert f(8192, 8, 64, 4096, 4096) == area(8192 * 64)
     assert f(0, 4, 16, 64, 64) == 0 and b(0, 4, 16, 64, 64) == 0
     assert f(-1, 4, 16, 64, 64) == 0 and b(10, 4, 300, 64, 64) == 0 and f(10, 4, 16, 7, 64) == 0
     # dh alone up to one chunk of rows, then at most 2 T / chunk partial sums
     assert b(128, 1, 16, 64, 96) == area(128 * 16)
     chunk = 4096 * 64 // 384 // 32 * 32 + 32
-    assert b(4096, 4, 32, 4096, 4096) == (area(4 * 4096 * 32) + 4096 * 32 * 4
+    assert b(4096, 4, 32, 4096, 4096) == (area(2 * 4096 * 32) + 4096 * 32 * 4
                                           + 2 * 4096 // chunk * 32 * 8192 * 4)
     # a size just below what is needed
     need = f(64, 32, 16, 4096, 4096)

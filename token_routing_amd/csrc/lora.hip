@@ -300,9 +300,10 @@ __device__ __forceinline__ void load_h(float (&v)[8], const float *h, int64_t p,
 // run of it, and adds the waves' sums through LDS in wave order.  Each split
 // stores a copy of its own.  RF: 16-row blocks of ranks.
 //
-// A fragment load touches 16 rows at a time, one cache line each, so the lines
-// looked up are the bound before bytes are: RT > 1 uses the weights' fragments
-// for several blocks of rows.
+// Loaded in the layout of a fragment, 16 neighbouring lanes on 16 rows, every
+// 16 bytes would be a cache lookup of their own, and the lookups the bound;
+// rows are loaded 64 bytes at a time instead and reach their lanes through
+// LDS.  RT > 1 uses the weights' fragments for several blocks of rows.
 //
 // The loads of U whole 32-column steps are issued together, without branches:
 // lanes past the tile's rows load its first row again and lanes past the rank
@@ -322,8 +323,9 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
     constexpr int W = PIECES ? RF : 1;
     constexpr int D = W < 2 ? 1 : W / 2;
     constexpr int Q = TR ? (PIECES ? 1 : RF) : 1;  // loads of a row of weights (TR)
-    constexpr int U = RF <= 2 ? 4 : RF <= 8 ? 2 : 1;
-    __shared__ f32x4_t s_acc[kShrinkWaves][RT * RF < kShrinkWaves ? RT * RF : kShrinkWaves][kWave];
+    constexpr int U = TR && EDGE ? (RF <= 2 ? 2 : 1) : RF <= 2 ? 4 : RF <= 8 ? 2 : 1;
+    constexpr int kBlocks = RT * RF, kTurn = kBlocks < kShrinkWaves ? kBlocks : kShrinkWaves;
+    __shared__ f32x4_t s_acc[kShrinkWaves][kTurn][kWave];
     check_sizes(a.m_sizes, a.ranks, a.L, a.T, a.R, a.err);
     const int split = blockIdx.x % a.splits;
     Tile tile;
@@ -334,12 +336,18 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
     const int lane = threadIdx.x & (kWave - 1);
     const int m = lane & 15, g = lane >> 4;
 
+    // Rows are loaded four lanes to a row, 64 bytes of it, and change lanes
+    // through LDS: lane 4 r + q loads piece q of row r, lane 16 g + m needs
+    // piece g of row m.  The pieces of a row are exchanged so that neither
+    // access has two lanes on one bank.
+    const int rl = lane >> 2, ql = lane & 3;
+    const int put_at = rl * 4 + (ql ^ ((rl >> 1) & 3)), get_at = m * 4 + (g ^ ((m >> 1) & 3));
     const uint16_t *row[RT];
-    bool bad_row[RT];
+    uint32_t bad_rows = 0;  // bit t: the lane's row of block t has a bad gather entry
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-        const int64_t src = source_row(a, tile.p0 + (t * 16 + m < tile.rows ? t * 16 + m : 0));
-        bad_row[t] = src < 0;
+        const int64_t src = source_row(a, tile.p0 + (t * 16 + rl < tile.rows ? t * 16 + rl : 0));
+        bad_rows |= (uint32_t)(src < 0) << t;
         row[t] = a.in + (src < 0 ? 0 : src) * a.ld_in;
     }
     const uint16_t *const w = a.w + (int64_t)tile.a * a.R * a.C;
@@ -365,79 +373,107 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
             else if constexpr (TR)
                 wrow[f] = w + min(f * 16 + m, a.R - 1);
             else
-                wrow[f] = w + (int64_t)min(f * 16 + m, rank - 1) * a.C;
+                wrow[f] = w + (int64_t)min(f * 16 + rl, rank - 1) * a.C;
         }
+        u32x4_t *const stage = reinterpret_cast<u32x4_t *>(&s_acc[wave][0][0]);
+        // One step from its loaded rows: x into LDS and back, then the weights,
+        // kTurn blocks (the room a wave has) at a time.
+        auto step = [&](const u32x4_t (&x)[RT], auto &&weights) {
+            u32x4_t xf[RT];
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                stage[t * kWave + put_at] = x[t];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                xf[t] = stage[t * kWave + get_at];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int f0 = 0; f0 < RF; f0 += kTurn) {
+                if constexpr (!TR) {
+#pragma unroll
+                    for (int f = 0; f < kTurn && f0 + f < RF; ++f)
+                        stage[f * kWave + put_at] = weights(f0 + f);
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                }
+#pragma unroll
+                for (int f = 0; f < kTurn && f0 + f < RF; ++f) {
+                    const u32x4_t b = TR ? weights(f0 + f) : stage[f * kWave + get_at];
+#pragma unroll
+                    for (int t = 0; t < RT; ++t)
+                        acc[t][f0 + f] = mfma<DT>(b, xf[t], acc[t][f0 + f]);
+                }
+                if constexpr (!TR) {
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
+        };
         for (int s = s0; s < full; s += U) {
             u32x4_t x[U][RT], v[TR ? 1 : U][TR ? 1 : RF];
             uint32_t q[TR ? U : 1][Q][8][D];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = min(s + u, full - 1) * 32 + g * 8;
+                const int c0 = min(s + u, full - 1) * 32;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    x[u][t] = load8_in(row[t] + c);
+                    x[u][t] = load8_in(row[t] + c0 + ql * 8);
                 if constexpr (!TR) {
 #pragma unroll
                     for (int f = 0; f < RF; ++f)
-                        v[u][f] = load8_in(wrow[f] + c);
+                        v[u][f] = load8_in(wrow[f] + c0 + ql * 8);
                 } else {
 #pragma unroll
                     for (int f = 0; f < Q; ++f)
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            load_pairs<W>(q[u][f][e], wrow[f] + (int64_t)(c + e) * a.R);
+                            load_pairs<W>(q[u][f][e], wrow[f] + (int64_t)(c0 + g * 8 + e) * a.R);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (s + u < full) {
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) {
-                        const u32x4_t b = TR ? column<W>(q[TR ? u : 0][PIECES ? 0 : TR ? f : 0],
-                                                         PIECES ? f : 0)
-                                             : v[TR ? 0 : u][TR ? 0 : f];
-#pragma unroll
-                        for (int t = 0; t < RT; ++t)
-                            acc[t][f] = mfma<DT>(b, x[u][t], acc[t][f]);
-                    }
-                }
+                if (s + u < full)
+                    step(x[u], [&](int f) {
+                        return TR ? column<W>(q[TR ? u : 0][PIECES ? 0 : TR ? f : 0],
+                                              PIECES ? f : 0)
+                                  : v[TR ? 0 : u][TR ? 0 : f];
+                    });
         }
         if constexpr (EDGE) {
             if (s1 > whole && s0 < s1) {  // the last, partial step
-                const int c = whole * 32 + g * 8;
+                const int c0 = whole * 32;
                 u32x4_t x[RT];
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
-                    x[t] = load8_end(row[t], c, a.C);
-#pragma unroll
-                for (int f = 0; f < RF; ++f) {
-                    u32x4_t b;
+                    x[t] = load8_end(row[t], c0 + ql * 8, a.C);
+                step(x, [&](int f) {
                     if constexpr (TR) {
                         uint32_t e8[8][1];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            load_pairs<1>(e8[e], wrow[f] + (int64_t)min(c + e, a.C - 1) * a.R);
-                            e8[e][0] = c + e < a.C ? e8[e][0] : 0;
+                            const int c = c0 + g * 8 + e;
+                            load_pairs<1>(e8[e], wrow[f] + (int64_t)min(c, a.C - 1) * a.R);
+                            e8[e][0] = c < a.C ? e8[e][0] : 0;
                         }
-                        b = column<1>(e8, 0);
+                        return column<1>(e8, 0);
                     } else {
-                        b = load8_end(wrow[f], c, a.C);
+                        return load8_end(wrow[f], c0 + ql * 8, a.C);
                     }
-#pragma unroll
-                    for (int t = 0; t < RT; ++t)
-                        acc[t][f] = mfma<DT>(b, x[t], acc[t][f]);
-                }
+                });
             }
         }
     }
     // Every wave adds, in wave order, and stores the blocks of sums that are its
     // share: 8 blocks at a time, one a wave.
     const float factor = a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
-    constexpr int kBlocks = RT * RF, kTurn = kBlocks < kShrinkWaves ? kBlocks : kShrinkWaves;
+    // The lane that loaded row m knows whether it was bad.
+    bad_rows = __shfl(bad_rows, m * 4, kWave);
 #pragma unroll
     for (int turn = 0; turn < kBlocks; turn += kTurn) {
-        if (turn > 0)
-            __syncthreads();
+        __syncthreads();
 #pragma unroll
         for (int b = 0; b < kTurn; ++b)
             s_acc[wave][b][lane] = acc[(turn + b) / RF][(turn + b) % RF];
@@ -454,10 +490,7 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
         const int p = tile.p0 + t * 16 + m;
         if (t * 16 + m >= tile.rows)
             continue;
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            bad |= i == t && bad_row[i];
+        const bool bad = bad_rows >> t & 1;
         float *const h = a.h + split * a.split_stride + (int64_t)p * a.R;
         f32x4_t v;
 #pragma unroll

@@ -41,11 +41,11 @@ struct GradParams {
     bool fp32_out;
 };
 
-// 16-row blocks of a large shrink tile for ranks up to R: as many as keep the
-// sums of the tile in 64 registers.
+// 16-row blocks of a large shrink tile for ranks up to R: two while the sums
+// and the loads in flight fit 128 registers (two workgroups a compute unit).
 __host__ __device__ constexpr int shrink_blocks(int R)
 {
-    return R <= 32 ? 2 : R <= 64 ? 4 : R <= 128 ? 2 : 1;
+    return R <= 64 ? 2 : 1;
 }
 
 // Tiles are one block of 16 rows, or large where an adapter has 32 rows or more
