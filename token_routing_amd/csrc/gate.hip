@@ -155,6 +155,13 @@ __device__ __forceinline__ void load_row(float (&l)[V], const void *logits, int 
         load_row<V, kFp32>(l, logits, row, lane, E, live);
 }
 
+__device__ __forceinline__ float load_one(const void *logits, int dtype, int64_t at)
+{
+    return dtype == kBf16   ? Elem<kBf16>::widen(static_cast<const uint16_t *>(logits)[at])
+           : dtype == kFp16 ? Elem<kFp16>::widen(static_cast<const uint16_t *>(logits)[at])
+                            : static_cast<const float *>(logits)[at];
+}
+
 template <int V>
 __device__ __forceinline__ void store_row_f32(float *p, const float (&f)[V], int lane, int E)
 {
@@ -222,7 +229,9 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
 {
     constexpr int kTokens = kGateThreads / G;
     constexpr int kSlots = V == 1 ? 1 : 64 / G;  // picks a lane can hold
-    __shared__ double s_key[WIDE ? kTokens * G * V : 1];
+    // One more place a group, so that the groups' scans start on different banks.
+    constexpr int kKeys = G * V + 64;
+    __shared__ double s_key[WIDE ? kTokens * kKeys : 1];
     __shared__ double s_group[WIDE ? kTokens * 64 : 1];
     __shared__ int s_keep[WIDE ? kTokens * 64 : 1];
     const int lane = threadIdx.x % G;
@@ -289,7 +298,10 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
             part = lanes_sum<G>(part);
             dsum = part > 0.0 ? part : 1.0;
         }
-        double *const my = s_key + slot * (G * V);
+        double *const my = s_key + slot * kKeys;
+        const int per = a.E / a.n_groups;
+        const int g0 = lane * V / per, at0 = lane * V - g0 * per;
+        int g = g0, at = at0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = lane * V + v;
@@ -305,10 +317,14 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
             const uint64_t bits = ok ? order_bits(d[v]) : 0;
             key[v] = (uint32_t)(bits >> 32);
             low[v] = (uint32_t)bits;
-            my[e] = ok ? d[v] : -__builtin_huge_val();
+            if (e < a.E)
+                my[e + g] = ok ? d[v] : -__builtin_huge_val();
+            if (++at == per) {
+                at = 0;
+                ++g;
+            }
         }
         if (a.n_groups > 1) {
-            const int per = a.E / a.n_groups;
             double *const val = s_group + slot * 64;
             int *const keep = s_keep + slot * 64;
             __syncthreads();
@@ -318,7 +334,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
                     double x[4];
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        x[u] = i + u < per ? my[g * per + i + u] : -__builtin_huge_val();
+                        x[u] = i + u < per ? my[g * (per + 1) + i + u] : -__builtin_huge_val();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         second = fmax(second, fmin(first, x[u]));
@@ -336,7 +352,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
                 keep[g] = ahead < a.topk_groups;
             }
             __syncthreads();
-            int g = lane * V / per, at = lane * V - g * per;
+            g = g0;
+            at = at0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (lane * V + v < a.E && !keep[g])
@@ -379,18 +396,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
                 at = lane * V + v;
         at = lanes_umin<G>(at);
         const int id = best ? (int)at : -1;
-        float lv = kNegInf;
-        if constexpr (!WIDE) {
-            lv = best ? from_order_bits(best) : kNegInf;
-        } else {
-            uint32_t mine = 0;  // the owner's logit, found by all
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (lane * V + v == id)
-                    mine = __builtin_bit_cast(uint32_t, l[v]);
-            mine = lanes_combine<G>(mine, [](uint32_t a, uint32_t b) { return a | b; });
-            lv = best ? __builtin_bit_cast(float, mine) : kNegInf;
-        }
+        const float lv = !WIDE && best ? from_order_bits(best) : kNegInf;
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (lane * V + v == id)
@@ -401,6 +407,14 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateParams a)
                 pick_id[s] = id;
                 pick_l[s] = lv;
             }
+    }
+
+    if constexpr (WIDE) {
+        // The picks' logits again, each by the lane that holds the pick.
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            if (pick_id[s] >= 0 && live)
+                pick_l[s] = load_one(a.logits, a.dtype, t * a.ld + pick_id[s]);
     }
 
     float w[kSlots];
@@ -473,13 +487,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_bwd_kernel(GateBwdParams a)
             const int i = a.ids[t * a.topk + j];
             bad |= i >= a.E;
             if (i >= 0 && i < a.E) {
-                float one;
-                if (a.dtype == kBf16)
-                    one = Elem<kBf16>::widen(static_cast<const uint16_t *>(a.logits)[t * a.ld + i]);
-                else if (a.dtype == kFp16)
-                    one = Elem<kFp16>::widen(static_cast<const uint16_t *>(a.logits)[t * a.ld + i]);
-                else
-                    one = static_cast<const float *>(a.logits)[t * a.ld + i];
+                const float one = load_one(a.logits, a.dtype, t * a.ld + i);
                 if (fabsf(one) < __builtin_huge_valf()) {
                     id[s] = i;
                     x[s] = one;
