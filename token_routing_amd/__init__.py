@@ -456,6 +456,14 @@ def _arg(t, name, dtype, shape, index):
     _refuse(t, name, dtype, shape, index)
 
 
+def _out(t, name, dtype, shape, device):
+    """An output tensor, allocated unless given, and its address."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, device.index)
+
+
 def _slots_arg(t, name, dtype, slots, index):
     """Address of a contiguous per-slot tensor: [slots] or [T, topk]."""
     if t is None:
@@ -464,6 +472,15 @@ def _slots_arg(t, name, dtype, slots, index):
             and t.is_contiguous()):
         return t.data_ptr()
     _refuse(t, name, dtype, (slots,), index)
+
+
+def _dw_out(dw, wanted, slots, device):
+    """The slots' weight gradient and its address, or None twice."""
+    if not wanted:
+        return None, None
+    if dw is None:
+        return _out(None, "dw", torch.float32, (slots,), device)
+    return dw, _slots_arg(dw, "dw", torch.float32, slots, device.index)
 
 
 def _rows_arg(t, name, dtype, shape, index):
@@ -507,19 +524,16 @@ def moe_gate(logits, topk: int, *, bias=None, n_groups: int = 1, topk_groups: in
     topk = int(topk)
 
     def call(stream_ptr):
-        i = torch.empty(T, topk, dtype=torch.int32, device=dev) if ids is None else ids
-        w = torch.empty(T, topk, dtype=torch.float32, device=dev) if weights is None else weights
-        s = scores
-        if s is None and want_scores:
-            s = torch.empty(T, E, dtype=torch.float32, device=dev)
+        i, i_ptr = _out(ids, "ids", torch.int32, (T, topk), dev)
+        w, w_ptr = _out(weights, "weights", torch.float32, (T, topk), dev)
+        s = s_ptr = None
+        if want_scores or scores is not None:
+            s, s_ptr = _out(scores, "scores", torch.float32, (T, E), dev)
         _check(lib.moegg_gate(
             ptr, code, ld, _arg(bias, "bias", torch.float32, (E,), index), T, E, topk, int(n_groups),
             int(topk_groups), float(scale),
             (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
-            _arg(i, "ids", torch.int32, (T, topk), index),
-            _arg(w, "weights", torch.float32, (T, topk), index),
-            _arg(s, "scores", torch.float32, (T, E), index), _flag_arg(error_flags, index),
-            stream_ptr), "moegg_gate")
+            i_ptr, w_ptr, s_ptr, _flag_arg(error_flags, index), stream_ptr), "moegg_gate")
         return i, w, s
 
     if topk < 1 or topk > E:
@@ -542,13 +556,13 @@ def moe_gate_bwd(logits, ids, dweights, *, dscores=None, scale: float = 1.0,
     topk = ids.shape[-1]
 
     def call(stream_ptr):
-        d = torch.empty(T, E, dtype=logits.dtype, device=dev) if dlogits is None else dlogits
+        d, d_ptr = _out(dlogits, "dlogits", logits.dtype, (T, E), dev)
         _check(lib.moegg_gate_bwd(
             ptr, code, ld, _arg(ids, "ids", torch.int32, (T, topk), index),
             _arg(dweights, "dweights", torch.float32, (T, topk), index),
             _arg(dscores, "dscores", torch.float32, (T, E), index), T, E, topk, float(scale),
             (GATE_SIGMOID if sigmoid else 0) | (GATE_RENORM if renorm else 0),
-            _arg(d, "dlogits", logits.dtype, (T, E), index), _flag_arg(error_flags, index),
+            d_ptr, _flag_arg(error_flags, index),
             stream_ptr), "moegg_gate_bwd")
         return d
 
@@ -581,17 +595,15 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
         rows = S + (E * (int(block_m) - 1) if padded_offsets is not None else 0)
 
     def call(stream_ptr):
-        out = torch.empty(rows, K, dtype=X.dtype, device=dev) if Xs is None else Xs
-        m = torch.empty(S, dtype=torch.int32, device=dev) if row_map is None else row_map
+        out, out_ptr = _out(Xs, "Xs", X.dtype, (rows, K), dev)
+        m, m_ptr = _out(row_map, "row_map", torch.int32, (S,), dev)
         _check(lib.moegg_permute(
             _arg(X, "X", X.dtype, (T, K), index), code,
             _slots_arg(scatter_idx, "scatter_idx", torch.int32, S, index),
             _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
             _arg(offsets, "offsets", torch.int32, (E + 1,), index),
             _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), index), T, topk, E, K,
-            rows, _arg(out, "Xs", X.dtype, (rows, K), index),
-            _arg(m, "row_map", torch.int32, (S,), index), _flag_arg(error_flags, index), stream_ptr),
-            "moegg_permute")
+            rows, out_ptr, m_ptr, _flag_arg(error_flags, index), stream_ptr), "moegg_permute")
         return out, m
 
     return _run(dev, stream, call)
@@ -610,19 +622,15 @@ def permute_bwd(dXs, X, topk: int, row_map, topk_weights=None, *, want_dw: bool 
     code = _dtype_code(dXs, "dXs")
 
     def call(stream_ptr):
-        out = torch.empty(T, K, dtype=dXs.dtype, device=dev) if dX is None else dX
-        g = dw
-        if want_dw and g is None:
-            g = torch.empty(S, dtype=torch.float32, device=dev)
+        out, out_ptr = _out(dX, "dX", dXs.dtype, (T, K), dev)
+        g, g_ptr = _dw_out(dw, want_dw, S, dev)
         _check(lib.moegg_permute_bwd(
             _arg(dXs, "dXs", dXs.dtype, (rows, K), index), code,
             _arg(X, "X", dXs.dtype, (T, K), index),
             _slots_arg(row_map, "row_map", torch.int32, T * topk, index),
             _slots_arg(topk_weights, "topk_weights", torch.float32, S, index), T, topk, K, rows,
-            _arg(out, "dX", dXs.dtype, (T, K), index),
-            _slots_arg(g if want_dw else None, "dw", torch.float32, S, index),
-            _flag_arg(error_flags, index), stream_ptr), "moegg_permute_bwd")
-        return out, (g if want_dw else None)
+            out_ptr, g_ptr, _flag_arg(error_flags, index), stream_ptr), "moegg_permute_bwd")
+        return out, g
 
     return _run(dev, stream, call)
 
@@ -640,14 +648,13 @@ def unpermute(Y, topk: int, row_map, topk_weights=None, *, base=None, out=None, 
     code = _dtype_code(Y, "Y")
 
     def call(stream_ptr):
-        o = torch.empty(T, K, dtype=Y.dtype, device=dev) if out is None else out
+        o, o_ptr = _out(out, "out", Y.dtype, (T, K), dev)
         _check(lib.moegg_unpermute(
             _arg(Y, "Y", Y.dtype, (rows, K), index), code,
             _slots_arg(row_map, "row_map", torch.int32, T * topk, index),
             _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
             _arg(base, "base", Y.dtype, (T, K), index), T, topk, K, rows,
-            _arg(o, "out", Y.dtype, (T, K), index), _flag_arg(error_flags, index), stream_ptr),
-            "moegg_unpermute")
+            o_ptr, _flag_arg(error_flags, index), stream_ptr), "moegg_unpermute")
         return o
 
     return _run(dev, stream, call)
@@ -678,10 +685,8 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
         raise ValueError("without Y and dY, rows is needed")
 
     def call(stream_ptr):
-        out = torch.empty(rows, K, dtype=dOut.dtype, device=dev) if dY is None else dY
-        g = dw
-        if want_dw and g is None:
-            g = torch.empty(S, dtype=torch.float32, device=dev)
+        out, out_ptr = _out(dY, "dY", dOut.dtype, (rows, K), dev)
+        g, g_ptr = _dw_out(dw, want_dw, S, dev)
         _check(lib.moegg_unpermute_bwd(
             _arg(dOut, "dOut", dOut.dtype, (T, K), index), code,
             _arg(Y, "Y", dOut.dtype, (rows, K), index),
@@ -689,10 +694,9 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
             _slots_arg(topk_weights, "topk_weights", torch.float32, S, index),
             _arg(offsets, "offsets", torch.int32, (E + 1,), index),
             _arg(padded_offsets, "padded_offsets", torch.int32, (E + 1,), index), T, topk, E, K,
-            rows, _arg(out, "dY", dOut.dtype, (rows, K), index),
-            _slots_arg(g if want_dw else None, "dw", torch.float32, S, index),
-            _flag_arg(error_flags, index), stream_ptr), "moegg_unpermute_bwd")
-        return out, (g if want_dw else None)
+            rows, out_ptr, g_ptr, _flag_arg(error_flags, index), stream_ptr),
+            "moegg_unpermute_bwd")
+        return out, g
 
     return _run(dev, stream, call)
 
@@ -710,6 +714,7 @@ def lora_bwd_workspace_bytes(num_rows: int, num_adapters: int, R: int, K: int, N
 def _workspace_arg(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr()
     return workspace, _slots_arg(workspace, "workspace", torch.uint8, workspace.numel(),
                                  device.index)
 
@@ -738,9 +743,9 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
 
     def call(stream_ptr):
         y = torch.empty(T, N, dtype=dt, device=dev) if Y is None else Y
-        h = H
-        if h is None and want_h:
-            h = torch.empty(T, R, dtype=torch.float32, device=dev)
+        h = h_ptr = None
+        if want_h or H is not None:
+            h, h_ptr = _out(H, "H", torch.float32, (T, R), dev)
         need = lib.moegg_lora_workspace_bytes(T, L, R, K, N)
         ws, ws_ptr = _workspace_arg(workspace, need, dev)
         x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), index)
@@ -752,7 +757,7 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
             _arg(gather_idx, "gather_idx", torch.int32, (T,), index),
             _arg(ranks, "ranks", torch.int32, (L,), index),
             _arg(scales, "scales", torch.float32, (L,), index), code, T, L, R, K, N, b_ptr, ldb,
-            y_ptr, ldy, _arg(h, "H", torch.float32, (T, R), index), ws_ptr, ws.numel(),
+            y_ptr, ldy, h_ptr, ws_ptr, ws.numel(),
             _flag_arg(error_flags, index), stream_ptr), "moegg_lora_fwd")
         return y, h
 
@@ -781,15 +786,15 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
 
     def call(stream_ptr):
         dx, x_ptr, ldx, dx_ptr, lddx, b_ptr, ldb = None, None, K, None, K, None, K
-        da = db = None
+        da = db = da_ptr = db_ptr = None
         if want_dx:
             dx = torch.empty(T, K, dtype=dt, device=dev) if dX is None else dX
             dx_ptr, lddx = _rows_arg(dx, "dX", dt, (T, K), index)
             if base is not None:
                 b_ptr, ldb = _rows_arg(base, "base", dt, (T, K), index)
         if want_weights:
-            da = torch.empty(L, R, K, dtype=wt, device=dev) if dA is None else dA
-            db = torch.empty(L, N, R, dtype=wt, device=dev) if dB is None else dB
+            da, da_ptr = _out(dA, "dA", wt, (L, R, K), dev)
+            db, db_ptr = _out(dB, "dB", wt, (L, N, R), dev)
             x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), index)
         dy_ptr, lddy = _rows_arg(dY, "dY", dt, (T, N), index)
         need = lib.moegg_lora_bwd_workspace_bytes(T, L, R, K, N)
@@ -802,7 +807,7 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
             _arg(gather_idx, "gather_idx", torch.int32, (T,), index),
             _arg(ranks, "ranks", torch.int32, (L,), index),
             _arg(scales, "scales", torch.float32, (L,), index), code, T, L, R, K, N, b_ptr, ldb,
-            dx_ptr, lddx, _arg(da, "dA", wt, (L, R, K), index), _arg(db, "dB", wt, (L, N, R), index),
+            dx_ptr, lddx, da_ptr, db_ptr,
             LORA_FP32_GRAD if fp32_grads else 0, ws_ptr, ws.numel(), _flag_arg(error_flags, index),
             stream_ptr), "moegg_lora_bwd")
         return dx, da, db
