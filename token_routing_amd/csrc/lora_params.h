@@ -61,13 +61,16 @@ inline int lora_shrink_rows(int64_t T, int L, int R)
 }
 
 // Shrink splits: how many workgroups share a tile's reduction of C columns.
-// One workgroup a compute unit (256) is aimed at; a wave's share stays at 64
-// columns or more, and at most 16 partial sums are left to add.
+// One workgroup a compute unit (256) is aimed at, two with ranks above 64, whose
+// weights make the reduction longer (rank 128, 4096 rows: 68.7 -> 61.8 us with
+// two; 2048 rows at rank 64: 39.7 -> 41.1 us, so one there); a wave's share
+// stays at 64 columns or more, and at most 16 partial sums are left to add.
 inline int lora_splits(int64_t T, int L, int R, int C)
 {
     const int rows = lora_shrink_rows(T, L, R);
     const int64_t tiles = (T + rows - 1) / rows + (T < L ? T : L);
-    int64_t n = tiles > 0 ? (256 + tiles - 1) / tiles : 1;
+    const int64_t aim = R > 64 ? 512 : 256;
+    int64_t n = tiles > 0 ? (aim + tiles - 1) / tiles : 1;
     n = n < C / 512 ? n : C / 512;
     return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
 }
