@@ -858,6 +858,7 @@ moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const voi
     p.out = static_cast<uint16_t *>(Y);
     p.ld_base = ld_base;
     p.ld_out = ldy;
+    p.stream_base = moegg::lora_streams(num_rows, N);
     p.h_out = H;
     return from_hip(
         moegg::lora_expand_launch(p, dtype, false, static_cast<hipStream_t>(stream)));
@@ -937,6 +938,7 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
         p.out = static_cast<uint16_t *>(dX);
         p.ld_base = ld_base;
         p.ld_out = lddx;
+        p.stream_base = moegg::lora_streams(num_rows, K);
         p.h_out = dA && split ? dh : nullptr;
         e = moegg::lora_expand_launch(p, dtype, true, hs);
     } else if (e == hipSuccess && split) {

@@ -180,6 +180,14 @@ __device__ __forceinline__ u32x4_t load8_in(const uint16_t *p)
     return __builtin_bit_cast(u32x4_t, *reinterpret_cast<const vec_t *>(p));
 }
 
+// The same with the nontemporal hint: the line is not kept for a later read.
+__device__ __forceinline__ u32x4_t load8_stream(const uint16_t *p)
+{
+    typedef Pack16<kBf16>::vec_t vec_t;
+    return __builtin_bit_cast(
+        u32x4_t, __builtin_nontemporal_load(reinterpret_cast<const vec_t *>(p)));
+}
+
 // Elements [at, at + 8) of an array of n >= 8 elements, zero past its end:
 // the load is moved back inside and its elements shifted down.
 __device__ __forceinline__ u32x4_t load8_end(const uint16_t *p, int64_t at, int64_t n)
@@ -569,9 +577,19 @@ __global__ __launch_bounds__(256, expand_places(TR, NS, RT)) void expand_kernel(
     u32x4_t old[RT][2];
     auto load_base = [&](int t, int c0) {
         const int c = EDGE ? min(c0 + col_lane, a.C - 8) : c0 + col_lane;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            old[t][i] = load8_in(a.base + (int64_t)max(src[t][i], 0) * a.ld_base + c);
+        const uint16_t *const q0 = a.base + (int64_t)max(src[t][0], 0) * a.ld_base + c;
+        const uint16_t *const q1 = a.base + (int64_t)max(src[t][1], 0) * a.ld_base + c;
+        // The empty statements keep the compiler from making one pair of loads
+        // of the two, without the hint.
+        if (a.stream_base) {
+            asm volatile("");
+            old[t][0] = load8_stream(q0);
+            old[t][1] = load8_stream(q1);
+            asm volatile("");
+        } else {
+            old[t][0] = load8_in(q0);
+            old[t][1] = load8_in(q1);
+        }
     };
 
     // A step's weights of the lane, as loaded: forward 4 fragments, TR 8 rows

@@ -24,6 +24,7 @@ struct LoraParams {
     int64_t T, ld_in, ld_base, ld_out, split_stride;
     int L, R, C, splits;
     bool scale_shrink;  // the adapter's scale belongs to h (backward), not to out
+    bool stream_base;   // base is too large to be worth a place in the caches
 };
 
 struct GradParams {
@@ -40,6 +41,15 @@ struct GradParams {
     int col_tiles_a, col_tiles_b;  // 128-column tiles of dA and dB (0: not wanted)
     bool fp32_out;
 };
+
+// Base and out together past the 256 MB last-level cache: base is then read
+// with the nontemporal hint (4096 rows of 28672 columns: 148 -> 138 us the
+// call; at 4096 columns, where a projection's output is still cached, the hint
+// costs 27.5 -> 32.3 us).
+inline bool lora_streams(int64_t T, int C)
+{
+    return T * C * 4 > ((int64_t)256 << 20);
+}
 
 // 16-row blocks of a large shrink tile for ranks up to R: two while the sums
 // and the loads in flight fit 128 registers (two workgroups a compute unit).
