@@ -482,12 +482,13 @@ moegg_status moegg_gate_bwd(const void *logits, int32_t dtype, int64_t ld_logits
  *                  that are no pad rows are left as they were.
  *   row_map        out [T*topk] int32: row(s), -1 for a dropped slot.  What
  *                  the other three entry points (and moegg_combine, as its
- *                  scatter_idx) take.  Required in the padded layout,
- *                  optional without (it then repeats scatter_idx).
+ *                  scatter_idx) take.  Required in the padded layout, where it
+ *                  may not be scatter_idx; optional without (it then repeats
+ *                  scatter_idx).
  * A row at or past `rows` raises MOEGG_DERR_GATHER and is skipped.  Products
  * in fp32, rounded once.  T = 0 writes the pad rows alone.
- * Errors: ESHAPE for T < 0, topk < 1, K < 1, rows < 0, sizes past 2^40 bytes,
- * E outside [1, MOEGG_MAX_EXPERTS] in the padded layout; EINVAL for an unknown
+ * Errors: ESHAPE for T < 0 or past 16 million, topk < 1, K < 1, rows < 0,
+ * sizes past 2^40 bytes, E outside [1, MOEGG_MAX_EXPERTS] in the padded layout; EINVAL for an unknown
  * dtype, one of offsets / padded_offsets without the other, NULL or
  * misaligned pointers (rows need the alignment of one element only).
  */
@@ -526,7 +527,8 @@ moegg_status moegg_unpermute(const void *Y, int32_t dtype, const int32_t *row_ma
 
 /*
  * moegg_unpermute_bwd -- gradient of moegg_unpermute (base's is dOut itself):
- *   dY[row_map[s]] = w[s] * dOut[t]                (rounded once)
+ *   dY[row_map[s]] = w[s] * dOut[t]                (rounded once; the rows of
+ *                                                   row_map are distinct)
  *   dw[s] = sum_n dOut[t, n] * Y[row_map[s], n]    (fp32), when dw is not NULL
  * With offsets and padded_offsets the pad rows of dY are set to zero, so that
  * products over the padded rows read no stale values; other rows no slot maps
@@ -577,8 +579,8 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
  * Bit-for-bit deterministic.  Any K and N from 8 on and any strides; rows need
  * the alignment of one element.  T = 0 is a no-op.
  * Errors: ESHAPE for T < 0, L outside [1, MOEGG_MAX_EXPERTS], R outside
- * [1, MOEGG_MAX_LORA_RANK], K or N < 8, a row stride below its row, sizes past
- * 2^40 bytes; EUNSUPPORTED for MOEGG_FP32; EINVAL for an unknown dtype, NULL
+ * [1, MOEGG_MAX_LORA_RANK], K or N < 8, a row stride below its row or past
+ * 2^31, sizes past 2^40 bytes or past what a launch holds (2^27 rows); EUNSUPPORTED for MOEGG_FP32; EINVAL for an unknown dtype, NULL
  * or misaligned pointers, base = Y with different strides; EWORKSPACE.
  */
 moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const void *B,
@@ -601,7 +603,8 @@ size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_
  *   dB[a, n, r] = scales[a] * sum_{p of a} dY[i, n] * H[p, r]
  *   H          the forward's H.
  *   base, dX   as base and Y in the forward (base: the shared projection's
- *              input gradient); dX NULL skips it.
+ *              input gradient); dX NULL skips it.  dX may not be X when dA is
+ *              asked for: X is read after dX is written.
  *   dA, dB     out [L, R, K] and [L, N, R] of `dtype`, fp32 with
  *              MOEGG_LORA_FP32_GRAD; every element is written, zeros for
  *              adapters without rows and past an adapter's rank.  Both NULL

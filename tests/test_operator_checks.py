@@ -10,6 +10,7 @@ import pytest
 EINVAL, ESHAPE = 1, 2
 BF16, FP16, FP32 = 0, 1, 2
 P = ctypes.c_void_p(1 << 20)             # never dereferenced
+P2 = ctypes.c_void_p(1 << 21)
 ODD = ctypes.c_void_p((1 << 20) + 1)
 TWO = ctypes.c_void_p((1 << 20) + 2)
 
@@ -33,6 +34,7 @@ def gate(lib, logits=P, dtype=BF16, ld=64, bias=None, T=10, E=64, k=4, groups=1,
     (dict(T=-1), ESHAPE), (dict(E=0), ESHAPE), (dict(E=1025, ld=1025), ESHAPE),
     (dict(k=0), ESHAPE), (dict(k=65, E=128, ld=128), ESHAPE), (dict(E=3, k=4), ESHAPE),
     (dict(ld=63), ESHAPE), (dict(ld=1 << 50), ESHAPE), (dict(T=1 << 30), ESHAPE),
+    (dict(T=1 << 26, k=1), ESHAPE),
     (dict(groups=0), ESHAPE), (dict(groups=5), ESHAPE), (dict(groups=65, E=130, ld=130), ESHAPE),
     (dict(groups=8, top=9), ESHAPE), (dict(groups=8, top=0), ESHAPE),
     (dict(groups=32, top=1), ESHAPE),          # two experts a group, four picks
@@ -81,6 +83,8 @@ def permute(lib, X=P, dtype=BF16, sc=P, w=None, off=None, pad=None, T=10, k=2, E
     (dict(X=None), EINVAL), (dict(X=ODD), EINVAL), (dict(X=TWO, dtype=FP32), EINVAL),
     (dict(sc=None), EINVAL), (dict(Xs=None), EINVAL), (dict(w=TWO), EINVAL),
     (dict(row_map=TWO), EINVAL),
+    (dict(off=P, pad=P, sc=P, row_map=P), EINVAL),              # the map over its own input
+    (dict(T=1 << 24, k=1, K=1), ESHAPE),                        # more workgroups than a launch
 ])
 def test_permute_refusals(lib, kw, want):
     assert permute(lib, **kw) == want
@@ -145,7 +149,8 @@ EUNSUP, EWS = 3, 4
     (dict(T=-1), ESHAPE), (dict(T=1 << 31), ESHAPE), (dict(L=0), ESHAPE), (dict(L=1025), ESHAPE),
     (dict(R=0), ESHAPE), (dict(R=257), ESHAPE), (dict(K=7), ESHAPE), (dict(N=7), ESHAPE),
     (dict(ldx=63), ESHAPE), (dict(ldy=95), ESHAPE), (dict(ldb=95, Y=ODD), ESHAPE),
-    (dict(ldx=1 << 40), ESHAPE), (dict(L=1024, R=256, K=1 << 30, ldx=1 << 30), ESHAPE),
+    (dict(ldx=1 << 40), ESHAPE), (dict(T=1, ldx=1 << 31), ESHAPE),
+    (dict(T=1 << 28), ESHAPE), (dict(L=1024, R=256, K=1 << 30, ldx=1 << 30), ESHAPE),
     (dict(T=(1 << 31) - 1, N=1 << 20, ldy=1 << 20, ldb=1 << 20), ESHAPE),
     (dict(dtype=FP32), EUNSUP), (dict(dtype=5), EINVAL),
     (dict(X=None), EINVAL), (dict(A=None), EINVAL), (dict(B=None), EINVAL), (dict(m=None), EINVAL),
@@ -164,7 +169,7 @@ def test_lora_no_rows(lib):
 
 
 def lora_bwd(lib, X=P, ldx=64, dY=P, lddy=96, A=P, B=P, H=P, m=P, gather=P, ranks=None, scales=None,
-             dtype=BF16, T=10, L=4, R=16, K=64, N=96, base=P, ldb=64, dX=P, lddx=64, dA=P, dB=P,
+             dtype=BF16, T=10, L=4, R=16, K=64, N=96, base=P2, ldb=64, dX=P2, lddx=64, dA=P, dB=P,
              flags=0, ws=P, size=1 << 20):
     return lib.moegg_lora_bwd(X, ldx, dY, lddy, A, B, H, m, gather, ranks, scales, dtype, T, L, R,
                               K, N, base, ldb, dX, lddx, dA, dB, flags, ws, size, None, None)
@@ -178,7 +183,7 @@ def lora_bwd(lib, X=P, ldx=64, dY=P, lddy=96, A=P, B=P, H=P, m=P, gather=P, rank
     (dict(dY=None), EINVAL), (dict(A=None), EINVAL), (dict(B=None), EINVAL), (dict(m=None), EINVAL),
     (dict(dX=ODD, base=None), EINVAL), (dict(base=ODD), EINVAL), (dict(dA=ODD), EINVAL),
     (dict(dB=TWO, flags=1), EINVAL), (dict(H=TWO), EINVAL), (dict(ldb=80), EINVAL),
-    (dict(ws=None), EWS), (dict(size=100), EWS),
+    (dict(ws=None), EWS), (dict(size=100), EWS), (dict(X=P, dX=P, base=TWO), EINVAL),
 ])
 def test_lora_bwd_refusals(lib, kw, want):
     assert lora_bwd(lib, **kw) == want

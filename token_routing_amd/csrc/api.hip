@@ -51,6 +51,9 @@ bool aligned4(const void *p)
     return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
 }
 
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;
+
 bool known_dtype(int32_t dtype)
 {
     return dtype == MOEGG_BF16 || dtype == MOEGG_FP16 || dtype == MOEGG_FP32;
@@ -121,7 +124,7 @@ const char *moegg_status_string(moegg_status s)
 
 int32_t moegg_version(void)
 {
-    return 100;
+    return 101;
 }
 
 size_t moegg_route_workspace_bytes(int64_t num_slots, int32_t num_experts)
@@ -508,7 +511,8 @@ static moegg_status check_gate(const void *logits, int32_t dtype, int64_t ld, in
     if (num_tokens < 0 || E < 1 || E > MOEGG_MAX_EXPERTS || topk < 1 || topk > E ||
         topk > MOEGG_MAX_TOPK || ld < E)
         return MOEGG_ESHAPE;
-    if (num_tokens > INT32_MAX / topk || ld > ((int64_t)1 << 40) / (num_tokens + 1) / 4)
+    if (num_tokens > INT32_MAX / topk || num_tokens >= kMaxThreads / 64 ||
+        ld > ((int64_t)1 << 40) / (num_tokens + 1) / 4)
         return MOEGG_ESHAPE;
     if (!known_dtype(dtype) || (flags & ~(uint32_t)(MOEGG_GATE_SIGMOID | MOEGG_GATE_RENORM)) ||
         !(scale - scale == 0.0f))
@@ -596,7 +600,9 @@ static moegg_status check_sort(const void *tok, const void *sorted, int32_t dtyp
     constexpr int64_t kMax = (int64_t)1 << 38;  // elements: 2^40 bytes of fp32
     if (num_tokens < 0 || topk < 1 || K < 1 || K > (1 << 30) || rows < 0 || rows > INT32_MAX)
         return MOEGG_ESHAPE;
-    if (num_tokens > INT32_MAX / topk || num_tokens > kMax / K || rows > kMax / K)
+    // a workgroup of 256 threads a token, and up to 1088 for pad rows
+    if (num_tokens > INT32_MAX / topk || num_tokens >= kMaxThreads / 256 - 2048 ||
+        num_tokens > kMax / K || rows > kMax / K)
         return MOEGG_ESHAPE;
     if (!known_dtype(dtype))
         return MOEGG_EINVAL;
@@ -637,7 +643,8 @@ moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_
         st = check_padded(offsets, padded_offsets, num_experts, Xs, dtype, rows);
     if (st != MOEGG_OK)
         return st;
-    if (num_tokens > 0 && ((padded_offsets && !row_map) || !aligned4(row_map)))
+    if (num_tokens > 0 &&
+        ((padded_offsets && (!row_map || row_map == scatter_idx)) || !aligned4(row_map)))
         return MOEGG_EINVAL;
     moegg::SpreadParams p = {};
     p.src = X;
@@ -749,10 +756,14 @@ static moegg_status check_lora_sizes(int64_t T, int32_t L, int32_t R, int32_t K,
     const int64_t wide = K > N ? K : N;
     if ((int64_t)L * R > kMax / wide || (T > 0 && wide > kMax / T))
         return MOEGG_ESHAPE;
-    const int64_t cols = wide / 128 + 1;
-    const int64_t shrink = (T / 16 + 1 + L) * 16, expand = (T / 16 + 1 + L) * cols;
-    const int64_t grad = (L + T / moegg::lora_chunk(T, R, K, N)) * (2 * cols) * ((R + 15) / 16);
-    if (shrink > INT32_MAX || expand > INT32_MAX || grad > INT32_MAX)
+    // Launch sizes: shrink's workgroups have 512 threads, the others 256;
+    // expand has at most its places (1024) and one workgroup a tile.
+    const int64_t tiles = T / 16 + 1 + L;
+    const int wide_splits = moegg::lora_splits(T, L, R, (int32_t)wide);
+    const int64_t cols = ((int64_t)K + 127) / 128 + ((int64_t)N + 127) / 128;
+    const int64_t grad = (L + T / moegg::lora_chunk(T, R, K, N)) * cols * ((R + 15) / 16);
+    if (tiles * wide_splits >= kMaxThreads / 512 || tiles + 1024 >= kMaxThreads / 256 ||
+        grad >= kMaxThreads / 256)
         return MOEGG_ESHAPE;
     return MOEGG_OK;
 }
@@ -898,8 +909,8 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     if (num_rows > 0 && (!dY || !A || !B || !aligned2(dY) || !aligned2(A) || !aligned2(B)))
         return MOEGG_EINVAL;
     if (dA) {
-        if (num_rows > 0 && (!X || !H || !aligned2(X) || !aligned4(H)))
-            return MOEGG_EINVAL;
+        if (num_rows > 0 && (!X || !H || !aligned2(X) || !aligned4(H) || X == dX))
+            return MOEGG_EINVAL;  // dX is written before X is read for dA
         if ((flags & MOEGG_LORA_FP32_GRAD) ? !aligned4(dA) || !aligned4(dB)
                                            : !aligned2(dA) || !aligned2(dB))
             return MOEGG_EINVAL;
