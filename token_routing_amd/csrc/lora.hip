@@ -861,7 +861,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
 {
     constexpr int kRanks = RG * 16;
     constexpr int kPad = 128 + 4;
-    __shared__ __attribute__((aligned(16))) float s_sum[4][kRanks][kPad];
+    __shared__ __attribute__((aligned(16))) float s_sum[2][kRanks][kPad];
     const int rank_tiles = (a.R + kRanks - 1) / kRanks;
     const int tiles = a.col_tiles_a + a.col_tiles_b;
     int b = blockIdx.x;
@@ -907,7 +907,10 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             small_at[e] = (uint32_t)((g * 8 + e) * a.R + min(r0, rank - 1));
-        const uint32_t next_block = (uint32_t)(min(r0 + 16, rank - 1) - min(r0, rank - 1));
+        uint32_t block_at[RG];
+#pragma unroll
+        for (int q = 0; q < RG; ++q)
+            block_at[q] = (uint32_t)(min(r0 + q * 16, rank - 1) - min(r0, rank - 1));
         auto rows_of = [&](int (&at)[8], int p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -924,7 +927,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
                 for (int q = 0; q < RG; ++q)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        v[q][e] = s[small_at[e] + (q ? next_block : 0)];
+                        v[q][e] = s[small_at[e] + block_at[q]];
             } else {
 #pragma unroll
                 for (int q = 0; q < RG; ++q)
@@ -1005,20 +1008,30 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
             }
         }
     }
-    // A lane holds rank m of each block, columns (4 g + i) * 8 + f.
+    // A lane holds rank m of each block, columns (4 g + i) * 8 + f.  Waves 2 and
+    // 3 leave their sums, waves 0 and 1 add theirs, and every thread adds the
+    // two: (0 + 2) + (1 + 3).
 #pragma unroll
-    for (int q = 0; q < RG; ++q) {
-        const float k = DT == kFp16 ? inverse_scale(fit[q]) : 1.0f;
+    for (int turn = 0; turn < 2; ++turn) {
+        if (turn == (wave < 2))
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float *const d = &s_sum[wave][q * 16 + m][(4 * g + i) * 8];
-            *reinterpret_cast<f32x4_t *>(d) =
-                k * f32x4_t{acc[0][q][i], acc[1][q][i], acc[2][q][i], acc[3][q][i]};
-            *reinterpret_cast<f32x4_t *>(d + 4) =
-                k * f32x4_t{acc[4][q][i], acc[5][q][i], acc[6][q][i], acc[7][q][i]};
-        }
+            for (int q = 0; q < RG; ++q) {
+                const float k = DT == kFp16 ? inverse_scale(fit[q]) : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        f32x4_t *const d = reinterpret_cast<f32x4_t *>(
+                            &s_sum[wave & 1][q * 16 + m][(4 * g + i) * 8 + half * 4]);
+                        f32x4_t v = k * f32x4_t{acc[4 * half][q][i], acc[4 * half + 1][q][i],
+                                                acc[4 * half + 2][q][i], acc[4 * half + 3][q][i]};
+                        if (turn == 1)
+                            v += *d;
+                        *d = v;
+                    }
+            }
+        __syncthreads();
     }
-    __syncthreads();
     const float factor = !is_a && a.l.scales ? a.l.scales[tile.a] : 1.0f;
     const int64_t size_a = (int64_t)a.R * a.K;
     float *part = nullptr;  // fp32 output: partials, or the caller's
@@ -1032,7 +1045,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
     else
         out16 = static_cast<uint16_t *>(is_a ? a.dA : a.dB) + out0;
     auto sum_of = [&](int r, int x) {
-        const float v = ((s_sum[0][r][x] + s_sum[1][r][x]) + s_sum[2][r][x]) + s_sum[3][r][x];
+        const float v = s_sum[0][r][x] + s_sum[1][r][x];
         return rt * kRanks + r < rank ? factor * v : 0.0f;
     };
     auto put = [&](int64_t to, float v) {
@@ -1238,10 +1251,9 @@ template <int DT, bool TR> hipError_t expand_go(const LoraParams &p, hipStream_t
 template <int DT> hipError_t grad_go(const GradParams &p, hipStream_t stream)
 {
     const int64_t items = p.l.L + p.l.T / p.chunk;
-    const int rg = p.R <= 16 ? 1 : 2;
-    const int64_t rank_tiles = (p.R + rg * 16 - 1) / (rg * 16);
+    const int64_t rank_tiles = lora_rank_tiles(p.R);
     const dim3 grid((unsigned)(items * (p.col_tiles_a + p.col_tiles_b) * rank_tiles));
-    if (rg == 1)
+    if (p.R <= 16)
         hipLaunchKernelGGL((grad_kernel<DT, 1>), grid, dim3(256), 0, stream, p);
     else
         hipLaunchKernelGGL((grad_kernel<DT, 2>), grid, dim3(256), 0, stream, p);

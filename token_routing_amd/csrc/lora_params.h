@@ -85,6 +85,13 @@ inline int lora_splits(int64_t T, int L, int R, int C)
     return (int)(n < 1 ? 1 : n > 16 ? 16 : n);
 }
 
+// Rank tiles of the gradients, 16 ranks (R <= 16) or 32 each.  64 leave one wave
+// a SIMD: at rank 128, 4096 rows, the kernel took 70 us instead of 60.
+inline int lora_rank_tiles(int R)
+{
+    return R <= 32 ? 1 : (R + 31) / 32;
+}
+
 // Rows of one chunk of the gradients' reduction, a multiple of 32: such that
 // chunks, column tiles and rank tiles make about 384 workgroups (two fit a
 // compute unit at a time, and segments that are no whole chunks add some), but
@@ -92,7 +99,7 @@ inline int lora_splits(int64_t T, int L, int R, int C)
 inline int lora_chunk(int64_t T, int R, int K, int N)
 {
     const int64_t tiles = (((int64_t)K + 127) / 128 + ((int64_t)N + 127) / 128) *
-                          (R <= 16 ? 1 : (R + 31) / 32);
+                          lora_rank_tiles(R);
     const int64_t c = (T * tiles / 384 + 31) / 32 * 32;
     return (int)(c < 128 ? 128 : c < T ? c : (T + 31) / 32 * 32 + 128);
 }
