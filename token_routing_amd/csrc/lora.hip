@@ -530,7 +530,7 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // instructions and its base as this one's is used, in the order in which they
 // are waited for.  SMALL: ranks up to 16, both parts of
 // h in one instruction.  EDGE: columns that are no whole passes (the last one
-// goes by single elements, a row at a time) or ranks that are no whole pieces
+// goes by single elements) or ranks that are no whole pieces
 // of 8.
 constexpr int expand_places(bool TR, int NS, int RT)
 {
@@ -822,13 +822,23 @@ __global__ __launch_bounds__(256, expand_places(TR, NS, RT)) void expand_kernel(
                 if constexpr (MORE)
                     load_base(t, c0 + 4 * kCols);
             } else {
-                for (int r = 0; r < min(16, tile.rows - t * 16); ++r) {
-                    const int64_t x = s_src[t * 16 + r];
-                    const int c = c0 + lane;
-                    if (x >= 0 && c < a.C) {
-                        const float y = Elem<DT>::widen(a.base[x * a.ld_base + c]) +
+                // A column a lane, 8 rows at once.
+                const int c = c0 + lane;
+                for (int r0 = 0; r0 < 16; r0 += 8) {
+                    int64_t row[8];
+                    uint16_t was[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        row[u] = s_src[t * 16 + r0 + u];
+                        was[u] = a.base[max(row[u], (int64_t)0) * a.ld_base + min(c, a.C - 1)];
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int r = r0 + u;
+                        const float y = Elem<DT>::widen(was[u]) +
                                         s_factor[t * 16 + r] * s_out[wave][r][lane];
-                        a.out[x * a.ld_out + c] = Elem<DT>::narrow(y);
+                        if (row[u] >= 0 && c < a.C)
+                            a.out[row[u] * a.ld_out + c] = Elem<DT>::narrow(y);
                     }
                 }
             }
