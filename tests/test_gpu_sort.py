@@ -212,8 +212,11 @@ def test_bad_rows_are_flagged_and_skipped(mg):
     sc[5] = T * k + 9
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     Xs = torch.full((T * k, K), 7.0, dtype=torch.bfloat16, device="cuda")
-    _, m = mg.permute(X, sc, k, w.cuda(), Xs=Xs, error_flags=err)
+    m = torch.empty_like(sc)
+    mg.permute(X, sc, k, w.cuda(), Xs=Xs, row_map=m, error_flags=err)
     assert int(err.item()) == mg.DERR_GATHER and m[5].item() == -1
+    assert torch.equal(torch.cat([m[:5], m[6:]]), torch.cat([sc[:5], sc[6:]]))
+    assert mg.permute(X, sc, k, w.cuda(), Xs=Xs)[1] is sc
     assert torch.all(Xs[want[5]] == 7.0)
     for call in (lambda e: mg.permute_bwd(Xs, X, k, sc, w.cuda(), error_flags=e),
                  lambda e: mg.unpermute_bwd(X, Xs, k, sc, w.cuda(), error_flags=e)):

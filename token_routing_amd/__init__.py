@@ -578,7 +578,8 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
     (moe_route) the block-padded layout, pad rows cleared; a new Xs then needs
     `rows` or the block_m that was routed with.  Returns (Xs [rows, K],
     row_map int32 [T*topk]); rows past the last expert's are left as they were
-    (a new Xs leaves them uninitialised).
+    (a new Xs leaves them uninitialised).  Without padding the map is
+    scatter_idx itself unless a row_map is given to write it to.
     """
     lib = load_library()
     dev = X.device
@@ -596,7 +597,10 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
 
     def call(stream_ptr):
         out, out_ptr = _out(Xs, "Xs", X.dtype, (rows, K), dev)
-        m, m_ptr = _out(row_map, "row_map", torch.int32, (S,), dev)
+        if row_map is None and padded_offsets is None:
+            m, m_ptr = scatter_idx, None
+        else:
+            m, m_ptr = _out(row_map, "row_map", torch.int32, (S,), dev)
         _check(lib.moegg_permute(
             _arg(X, "X", X.dtype, (T, K), index), code,
             _slots_arg(scatter_idx, "scatter_idx", torch.int32, S, index),
