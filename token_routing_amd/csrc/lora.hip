@@ -543,7 +543,10 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // no whole pieces of 8.  expand_places: workgroups a compute unit, by registers.
 constexpr int expand_places(bool TR, int NS, int RT)
 {
-    return RT == 1 ? (NS <= 2 ? 4 : 3) : NS == 1 || (NS == 2 && !TR) ? 3 : 2;
+    return RT == 1 ? (NS <= 2 ? 4 : NS == 8 && TR ? 2 : 3)
+           : NS == 8                          ? 1
+           : NS == 1 || (NS == 2 && !TR)      ? 3
+                                              : 2;
 }
 
 template <int DT, bool TR, int NS, bool SMALL, int RT, bool EDGE>
