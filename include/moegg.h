@@ -610,7 +610,10 @@ size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_
  *              adapters without rows and past an adapter's rank.  Both NULL
  *              skips them (X and H are then not read and may be NULL).
  *   workspace  moegg_lora_bwd_workspace_bytes(...) bytes.
- * Arguments, precision, determinism and errors otherwise as in the forward;
+ * dh enters the product of dX as h does in the forward; dh and H enter dA and
+ * dB with all 24 bits of an fp32 value (bf16) or 22 (fp16), so that
+ * LORA_FP32_GRAD gets gradients of fp32 precision.
+ * Arguments, determinism and errors otherwise as in the forward;
  * EINVAL for one of dA and dB without the other.  T = 0 writes zeros to dA
  * and dB.
  */

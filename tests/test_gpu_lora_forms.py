@@ -218,3 +218,33 @@ def test_gradients_against_differences_of_the_forward(mg, which, R):
     bound = bound + one * (grad * v.double()).abs().sum() + (2.0 ** -17 + (T + N + R + K) * U) * mag
     assert diff > 20 * bound                   # the comparison says something
     assert abs(diff - along) <= bound, (float(diff), float(along), float(bound))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("R", [9, 16, 40])
+def test_fp32_gradients_hold_fp32_values(mg, R, dtype):
+    """One row an adapter, so that dB is scale * dY * H and dA is dh * X, one
+    product an element: dY has a single column that is not zero, so dh is
+    fp32(scale * dY * B) with a full mantissa, and H is any fp32 value.  bf16
+    parts hold all 24 bits and fp16 parts leave 2^-22 at most; adding up to
+    three parts' products and the scale round once each (2^-23)."""
+    T, K, N = 37, 72, 40
+    g = torch.Generator().manual_seed(R)
+    dt = DT[dtype]
+    X = (torch.randn(T, K, generator=g) + 3).to(dt)
+    dY = torch.zeros(T, N, dtype=dt)
+    dY[torch.arange(T), torch.randint(0, N, (T,), generator=g)] = 1.5
+    A, B = torch.randn(T, R, K, generator=g).to(dt), torch.randn(T, N, R, generator=g).to(dt)
+    H = torch.rand(T, R, generator=g) + 0.5
+    s = torch.rand(T, generator=g) + 0.5
+    sizes = torch.ones(T, dtype=torch.int32).cuda()
+    _, dA, dB = mg.lora_bwd(X.cuda(), dY.cuda(), A.cuda(), B.cuda(), H.cuda(), sizes, None,
+                            scales=s.cuda(), want_dx=False, fp32_grads=True)
+    part = 0.0 if dtype == "bf16" else 2.0 ** -22
+    dB_ref = s.double()[:, None, None] * dY.double()[:, :, None] * H.double()[:, None, :]
+    dh = s.double()[:, None] * torch.einsum("tn,tnr->tr", dY.double(), B.double())
+    dA_ref = dh[:, :, None] * X.double()[:, None, :]
+    for got, ref in ((dA, dA_ref), (dB, dB_ref)):
+        rel = (got.cpu().double() - ref).abs() / ref.abs().clamp(min=1e-30)
+        assert float(rel[ref != 0].max()) <= part + 5 * U
+        assert torch.all(got.cpu()[ref == 0] == 0)

@@ -20,11 +20,15 @@
 // agree, and so is the assignment of output columns to lanes.
 //
 // h and dh stay in fp32 between the kernels.  Where one enters a matrix
-// instruction it goes as the sum of two 16-bit values (high part and rounded
-// rest), which keeps 16 bits of mantissa in bf16 and 22 in fp16, at twice the
-// matrix instructions, of which there are few.  With ranks up to 16 both parts
-// share one instruction: its 32 reduction elements hold 16 high and 16 low
-// ones.  fp16 parts are scaled by a power of two first, so that values past
+// instruction it goes as the sum of 16-bit values, each the rounded rest of the
+// ones before, at as many matrix instructions, of which there are few.  Two in
+// fp16 keep 22 bits of mantissa.  In bf16 expand takes two, 16 bits, since its
+// output is rounded to 8; the gradients, which may be fp32, take three, which
+// hold an fp32 value whole (with two the gradients of one adapter's rows were
+// off by 2.5e-6 instead of 3e-7; the third is not measurable in the call's
+// time: 54.3 us with two, 53.3 with three).  With ranks up to 16 expand's two
+// parts share one instruction: its 32 reduction elements hold 16 high and 16
+// low ones.  fp16 parts are scaled by a power of two first, so that values past
 // the type's range survive.
 //
 // Rows go by tiles inside one adapter's segment; each wave finds its tile by
@@ -243,30 +247,33 @@ __device__ __forceinline__ float inverse_scale(float s)
     return __builtin_bit_cast(float, (uint32_t)(254 - (__builtin_bit_cast(uint32_t, s) >> 23)) << 23);
 }
 
-// v as high + low 16-bit parts.  A value that is not finite has no rest.
-template <int DT>
-__device__ __forceinline__ void split8(const float (&v)[8], u32x4_t &hi, u32x4_t &lo)
+// v as the sum of PARTS 16-bit values, each the rounded rest of the ones before.
+// A value that is not finite has no rest.  Two parts hold 16 bits of mantissa in
+// bf16 and 22 in fp16, three all 24 of an fp32 value in bf16.
+template <int DT, int PARTS>
+__device__ __forceinline__ void split8(const float (&v)[8], u32x4_t (&part)[PARTS])
 {
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-        float h[2], r[2];
-        if constexpr (DT == kBf16) {
-            hi[d] = pack_bf16x2(v[2 * d], v[2 * d + 1]);
-            h[0] = __builtin_bit_cast(float, hi[d] << 16);
-            h[1] = __builtin_bit_cast(float, hi[d] & 0xffff0000u);
-        } else {
-            const uint32_t a = Elem<kFp16>::narrow(v[2 * d]), b = Elem<kFp16>::narrow(v[2 * d + 1]);
-            hi[d] = a | b << 16;
-            h[0] = Elem<kFp16>::widen((uint16_t)a);
-            h[1] = Elem<kFp16>::widen((uint16_t)b);
-        }
+        float r[2] = {v[2 * d], v[2 * d + 1]};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            r[i] = fabsf(h[i]) < __builtin_huge_valf() ? v[2 * d + i] - h[i] : 0.0f;
-        if constexpr (DT == kBf16)
-            lo[d] = pack_bf16x2(r[0], r[1]);
-        else
-            lo[d] = (uint32_t)Elem<kFp16>::narrow(r[0]) | (uint32_t)Elem<kFp16>::narrow(r[1]) << 16;
+        for (int p = 0; p < PARTS; ++p) {
+            float h[2];
+            if constexpr (DT == kBf16) {
+                const uint32_t both = pack_bf16x2(r[0], r[1]);
+                part[p][d] = both;
+                h[0] = __builtin_bit_cast(float, both << 16);
+                h[1] = __builtin_bit_cast(float, both & 0xffff0000u);
+            } else {
+                const uint32_t a = Elem<kFp16>::narrow(r[0]), b = Elem<kFp16>::narrow(r[1]);
+                part[p][d] = a | b << 16;
+                h[0] = Elem<kFp16>::widen((uint16_t)a);
+                h[1] = Elem<kFp16>::widen((uint16_t)b);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                r[i] = p > 0 || fabsf(h[i]) < __builtin_huge_valf() ? r[i] - h[i] : 0.0f;
+        }
     }
 }
 
@@ -690,13 +697,13 @@ expand_kernel(LoraParams a, int groups, int group_cols)
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            u32x4_t hi, lo;
-            split8<DT>(v[s], hi, lo);
+            u32x4_t part[2];
+            split8<DT>(v[s], part);
             if constexpr (SMALL) {
-                s_h[s][wave][0][lane] = g < 2 ? hi : lo;
+                s_h[s][wave][0][lane] = g < 2 ? part[0] : part[1];
             } else {
-                s_h[s][wave][0][lane] = hi;
-                s_h[s][wave][SMALL ? 0 : 1][lane] = lo;
+                s_h[s][wave][0][lane] = part[0];
+                s_h[s][wave][SMALL ? 0 : 1][lane] = part[1];
             }
         }
         if (g == 0)
@@ -885,6 +892,7 @@ template <int DT, int RG>
 __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
 {
     constexpr int kRanks = RG * 16;
+    constexpr int kParts = DT == kBf16 ? 3 : 2;
     constexpr int kPad = 128 + 4;
     __shared__ __attribute__((aligned(16))) float s_sum[2][kRanks][kPad];
     const int rank_tiles = (a.R + kRanks - 1) / kRanks;
@@ -1011,7 +1019,7 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
                     for (int q = 0; q < RG; ++q)
                         h[q][e] = ok[e] ? h[q][e] : 0.0f;
                 }
-            u32x4_t hi[RG], lo[RG];
+            u32x4_t part[RG][kParts];
 #pragma unroll
             for (int q = 0; q < RG; ++q) {
                 // Columns of sums past the rank come from a clamped rank and are
@@ -1020,16 +1028,16 @@ __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         h[q][e] *= fit[q];
-                split8<DT>(h[q], hi[q], lo[q]);
+                split8<DT>(h[q], part[q]);
             }
 #pragma unroll
             for (int f = 0; f < 8; ++f) {
                 const u32x4_t bf = column<8>(rows, f);
 #pragma unroll
-                for (int q = 0; q < RG; ++q) {
-                    acc[f][q] = mfma<DT>(bf, hi[q], acc[f][q]);
-                    acc[f][q] = mfma<DT>(bf, lo[q], acc[f][q]);
-                }
+                for (int q = 0; q < RG; ++q)
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i)
+                        acc[f][q] = mfma<DT>(bf, part[q][i], acc[f][q]);
             }
         }
     }
