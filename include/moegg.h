@@ -541,8 +541,9 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
                                  int64_t rows, void *dY, float *dw, int32_t *error_flags,
                                  void *stream);
 
-/* Adapter flag: write dA and dB in fp32 instead of `dtype`. */
-#define MOEGG_LORA_FP32_GRAD 1u
+/* Adapter flags. */
+#define MOEGG_LORA_FP32_GRAD 1u /* write dA and dB in fp32 instead of `dtype`          */
+#define MOEGG_LORA_ALL_ROWS 4u  /* rows of dX without an adapter get their base row    */
 
 /*
  * moegg_lora_fwd -- low-rank adapters of many requests at once, added to a
@@ -573,8 +574,8 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
  *   workspace  device, 16-byte aligned, moegg_lora_workspace_bytes(...) bytes,
  *              no initialisation.
  * Rows at no sorted position below the sum of m_sizes (moegg_route's dropped
- * ids) keep what Y holds: with a separate base give rows without an adapter
- * one of rank 0.  h is kept in fp32 and enters the second product with 16
+ * ids) keep what Y holds; moegg_lora_fwd_all_rows gives them their base row.
+ * H's rows at positions from that sum on are left as they were.  h is kept in fp32 and enters the second product with 16
  * (bf16) or 22 (fp16) bits of mantissa; sums in fp32; Y is rounded once.
  * Bit-for-bit deterministic.  Any K and N from 8 on and any strides; rows need
  * the alignment of one element.  T = 0 is a no-op.
@@ -591,6 +592,19 @@ moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const voi
                             float *H, void *workspace, size_t workspace_bytes,
                             int32_t *error_flags, void *stream);
 
+/*
+ * moegg_lora_fwd that writes every row of Y: a row without an adapter gets its
+ * base row, Y[i] = base[i].  For a Y apart from base that holds nothing yet;
+ * with base NULL or Y itself the two calls are the same.
+ */
+moegg_status moegg_lora_fwd_all_rows(const void *X, int64_t ldx, const void *A, const void *B, const
+                                     int32_t *m_sizes, const int32_t *gather_idx, const int32_t
+                                     *ranks, const float *scales, int32_t dtype, int64_t num_rows,
+                                     int32_t num_adapters, int32_t R, int32_t K, int32_t N, const
+                                     void *base, int64_t ld_base, void *Y, int64_t ldy, float *H,
+                                     void *workspace, size_t workspace_bytes, int32_t *error_flags,
+                                     void *stream);
+
 /* Workspace of moegg_lora_fwd; 0 for sizes it refuses. */
 size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
                                   int32_t N);
@@ -603,7 +617,8 @@ size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_
  *   dB[a, n, r] = scales[a] * sum_{p of a} dY[i, n] * H[p, r]
  *   H          the forward's H.
  *   base, dX   as base and Y in the forward (base: the shared projection's
- *              input gradient); dX NULL skips it.  dX may not be X when dA is
+ *              input gradient; rows without an adapter keep what dX holds, or
+ *              get their base row with LORA_ALL_ROWS); dX NULL skips it.  dX may not be X when dA is
  *              asked for: X is read after dX is written.
  *   dA, dB     out [L, R, K] and [L, N, R] of `dtype`, fp32 with
  *              MOEGG_LORA_FP32_GRAD; every element is written, zeros for

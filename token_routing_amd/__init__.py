@@ -38,6 +38,7 @@ GATE_SIGMOID = 1
 GATE_RENORM = 2
 
 LORA_FP32_GRAD = 1
+LORA_ALL_ROWS = 4
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -125,6 +126,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moegg_lora_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32,
                                    vp, i64, vp, i64, vp, vp, sz, vp, vp]
     lib.moegg_lora_fwd.restype = ctypes.c_int
+    lib.moegg_lora_fwd_all_rows.argtypes = lib.moegg_lora_fwd.argtypes
+    lib.moegg_lora_fwd_all_rows.restype = ctypes.c_int
     lib.moegg_lora_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i64, i32,
                                    i32, i32, i32, vp, i64, vp, i64, vp, vp, u32, vp, sz, vp, vp]
     lib.moegg_lora_bwd.restype = ctypes.c_int
@@ -732,8 +735,11 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
     gather_idx int32 [T] from moe_route over the rows' adapter ids (None: rows
     are in adapter order already); ranks int32 [L] or None (R); scales fp32 [L]
     or None (1).  base [T, N]: the projection's output; None adds to Y in
-    place.  X, base and Y may have any row stride.  Returns (Y, H): H is fp32
-    [T, R] in adapter order for lora_bwd, None unless given or want_h.
+    place.  X, base and Y may have any row stride.  A row without an adapter
+    (an id that moe_route dropped) gets its base row in a new Y, and keeps what
+    a given Y holds.  Returns (Y, H): H is fp32 [T, R] in adapter order for
+    lora_bwd, None unless given or want_h (rows at positions past the last
+    adapter's are left as they were).
     """
     lib = load_library()
     dev = X.device
@@ -755,7 +761,8 @@ def lora_fwd(X, A, B, m_sizes, gather_idx=None, *, ranks=None, scales=None, base
         x_ptr, ldx = _rows_arg(X, "X", dt, (T, K), index)
         y_ptr, ldy = _rows_arg(y, "Y", dt, (T, N), index)
         b_ptr, ldb = (None, ldy) if base is None else _rows_arg(base, "base", dt, (T, N), index)
-        _check(lib.moegg_lora_fwd(
+        forward = lib.moegg_lora_fwd_all_rows if Y is None else lib.moegg_lora_fwd
+        _check(forward(
             x_ptr, ldx, _arg(A, "A", dt, (L, R, K), index), _arg(B, "B", dt, (L, N, R), index),
             _arg(m_sizes, "m_sizes", torch.int32, (L,), index),
             _arg(gather_idx, "gather_idx", torch.int32, (T,), index),
@@ -774,7 +781,8 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
     """Gradients of lora_fwd (moegg_lora_bwd): (dX [T, K], dA [L, R, K], dB [L, N, R]).
 
     base [T, K]: the shared projection's input gradient, which dX adds to; None
-    adds to the dX given.  want_dx=False or want_weights=False leave dX or dA
+    adds to the dX given.  Rows without an adapter get their base row in a new
+    dX, and keep what a given dX holds.  want_dx=False or want_weights=False leave dX or dA
     and dB out (None in their place).  fp32_grads writes dA and dB in fp32.
     """
     lib = load_library()
@@ -812,8 +820,8 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
             _arg(ranks, "ranks", torch.int32, (L,), index),
             _arg(scales, "scales", torch.float32, (L,), index), code, T, L, R, K, N, b_ptr, ldb,
             dx_ptr, lddx, da_ptr, db_ptr,
-            LORA_FP32_GRAD if fp32_grads else 0, ws_ptr, ws.numel(), _flag_arg(error_flags, index),
-            stream_ptr), "moegg_lora_bwd")
+            (LORA_FP32_GRAD if fp32_grads else 0) | (LORA_ALL_ROWS if dX is None else 0),
+            ws_ptr, ws.numel(), _flag_arg(error_flags, index), stream_ptr), "moegg_lora_bwd")
         return dx, da, db
 
     return _run(dev, stream, call)

@@ -124,7 +124,7 @@ const char *moegg_status_string(moegg_status s)
 
 int32_t moegg_version(void)
 {
-    return 101;
+    return 102;
 }
 
 size_t moegg_route_workspace_bytes(int64_t num_slots, int32_t num_experts)
@@ -815,13 +815,13 @@ static moegg_status check_lora_dtype(int32_t dtype)
     return !known_dtype(dtype) ? MOEGG_EINVAL : dtype == MOEGG_FP32 ? MOEGG_EUNSUPPORTED : MOEGG_OK;
 }
 
-moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const void *B,
-                            const int32_t *m_sizes, const int32_t *gather_idx,
-                            const int32_t *ranks, const float *scales, int32_t dtype,
-                            int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
-                            int32_t N, const void *base, int64_t ld_base, void *Y, int64_t ldy,
-                            float *H, void *workspace, size_t workspace_bytes,
-                            int32_t *error_flags, void *stream)
+// all_rows: rows of no adapter get base's row; otherwise they keep what Y holds.
+static moegg_status lora_fwd(const void *X, int64_t ldx, const void *A, const void *B, const int32_t
+                             *m_sizes, const int32_t *gather_idx, const int32_t *ranks, const float
+                             *scales, int32_t dtype, int64_t num_rows, int32_t num_adapters, int32_t
+                             R, int32_t K, int32_t N, const void *base, int64_t ld_base, void *Y,
+                             int64_t ldy, float *H, void *workspace, size_t workspace_bytes, int32_t
+                             *error_flags, void *stream, bool all_rows)
 {
     moegg_status st = check_lora_sizes(num_rows, num_adapters, R, K, N);
     if (st == MOEGG_OK)
@@ -870,9 +870,36 @@ moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const voi
     p.ld_base = ld_base;
     p.ld_out = ldy;
     p.stream_base = moegg::lora_streams(num_rows, N);
+    p.copy_unrouted = all_rows && base != Y;
     p.h_out = H;
     return from_hip(
         moegg::lora_expand_launch(p, dtype, false, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_lora_fwd(const void *X, int64_t ldx, const void *A, const void *B,
+                            const int32_t *m_sizes, const int32_t *gather_idx,
+                            const int32_t *ranks, const float *scales, int32_t dtype,
+                            int64_t num_rows, int32_t num_adapters, int32_t R, int32_t K,
+                            int32_t N, const void *base, int64_t ld_base, void *Y, int64_t ldy,
+                            float *H, void *workspace, size_t workspace_bytes,
+                            int32_t *error_flags, void *stream)
+{
+    return lora_fwd(X, ldx, A, B, m_sizes, gather_idx, ranks, scales, dtype, num_rows, num_adapters,
+                    R, K, N, base, ld_base, Y, ldy, H, workspace, workspace_bytes, error_flags,
+                    stream, false);
+}
+
+moegg_status moegg_lora_fwd_all_rows(const void *X, int64_t ldx, const void *A, const void *B, const
+                                     int32_t *m_sizes, const int32_t *gather_idx, const int32_t
+                                     *ranks, const float *scales, int32_t dtype, int64_t num_rows,
+                                     int32_t num_adapters, int32_t R, int32_t K, int32_t N, const
+                                     void *base, int64_t ld_base, void *Y, int64_t ldy, float *H,
+                                     void *workspace, size_t workspace_bytes, int32_t *error_flags,
+                                     void *stream)
+{
+    return lora_fwd(X, ldx, A, B, m_sizes, gather_idx, ranks, scales, dtype, num_rows, num_adapters,
+                    R, K, N, base, ld_base, Y, ldy, H, workspace, workspace_bytes, error_flags,
+                    stream, true);
 }
 
 moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t lddy,
@@ -888,7 +915,7 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
         st = check_lora_dtype(dtype);
     if (st != MOEGG_OK)
         return st;
-    if (!dA != !dB || (flags & ~(uint32_t)MOEGG_LORA_FP32_GRAD))
+    if (!dA != !dB || (flags & ~(uint32_t)(MOEGG_LORA_FP32_GRAD | MOEGG_LORA_ALL_ROWS)))
         return MOEGG_EINVAL;
     if (!dX)
         lddx = K;
@@ -950,6 +977,7 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
         p.ld_base = ld_base;
         p.ld_out = lddx;
         p.stream_base = moegg::lora_streams(num_rows, K);
+        p.copy_unrouted = (flags & MOEGG_LORA_ALL_ROWS) && base != dX;
         p.h_out = dA && split ? dh : nullptr;
         e = moegg::lora_expand_launch(p, dtype, true, hs);
     } else if (e == hipSuccess && split) {

@@ -82,7 +82,8 @@ __device__ __forceinline__ int lane_of(uint32_t v, int lane)
 }
 
 // The tile `want` of all segments' tiles of `per` rows (empty segments have
-// `empty` tiles); false past the last one.  By adapter with by_adapter: the
+// `empty` tiles); false past the last one, with its distance from it in t.index
+// and the segments' rows together in t.p0.  By adapter with by_adapter: the
 // segment of adapter `want`.  All lanes of the wave call it.  Row sums
 // saturate at S, so that bad sizes cannot wrap around.
 __device__ __forceinline__ bool find_tile(const int32_t *m_sizes, int L, uint32_t S, int want,
@@ -120,6 +121,8 @@ __device__ __forceinline__ bool find_tile(const int32_t *m_sizes, int L, uint32_
         tile0 += lane_of(tiles, kWave - 1);
         slot0 += lane_of(slots, kWave - 1);
     }
+    t.index = want - tile0;
+    t.p0 = (int)row0;
     return false;
 }
 
@@ -556,6 +559,50 @@ constexpr int expand_places(bool TR, int NS, int RT)
                                               : 2;
 }
 
+// Rows at no sorted position below `sum` get base's row in columns [c0, c1):
+// workgroup `index` of `workgroups` takes an even share of the rows (without a
+// gather index those behind the sum), marks in `mark` which of them are routed,
+// and copies the others.
+__device__ __forceinline__ void copy_unrouted(const LoraParams &a, int sum, int index,
+                                              int workgroups, int c0, int c1, uint32_t *mark,
+                                              int words)
+{
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
+    const int first = a.gather ? 0 : sum;
+    const int per = ((int)a.T - first + workgroups - 1) / workgroups;
+    const int lo = first + index * per, hi = min((int)a.T, lo + per);
+    for (int r0 = lo; r0 < hi; r0 += words * 32) {
+        const int n = min(words * 32, hi - r0);
+        if (a.gather) {
+            for (int i = threadIdx.x; i < (n + 31) / 32; i += 256)
+                mark[i] = 0;
+            __syncthreads();
+            for (int p = threadIdx.x; p < sum; p += 256) {
+                const uint32_t d = (uint32_t)a.gather[p] - (uint32_t)r0;
+                if (d < (uint32_t)n)
+                    atomicOr(&mark[d / 32], 1u << d % 32);
+            }
+            __syncthreads();
+        }
+        for (int i = wave; i < n; i += 4) {
+            if (a.gather && (mark[i / 32] >> i % 32 & 1))
+                continue;
+            const uint16_t *const from = a.base + (int64_t)(r0 + i) * a.ld_base;
+            uint16_t *const to = a.out + (int64_t)(r0 + i) * a.ld_out;
+            for (int c = c0 + lane * 8; c < c1; c += kWave * 8) {
+                if (c + 8 <= c1) {
+                    *reinterpret_cast<Pack16<kBf16>::vec_t *>(to + c) =
+                        *reinterpret_cast<const Pack16<kBf16>::vec_t *>(from + c);
+                } else {
+                    for (int e = c; e < c1; ++e)
+                        to[e] = from[e];
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
 template <int DT, bool TR, int NS, bool SMALL, int RT, bool EDGE>
 __global__ __launch_bounds__(256, expand_places(TR, NS, RT)) void
 expand_kernel(LoraParams a, int groups, int group_cols)
@@ -569,13 +616,26 @@ expand_kernel(LoraParams a, int groups, int group_cols)
     __shared__ __attribute__((aligned(16))) float s_out[4][16][kPad];
     __shared__ int s_src[kRows];
     __shared__ float s_factor[kRows];
+    const int group = blockIdx.x % groups;
     Tile tile;
-    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / groups, kRows, 0, false, tile))
+    if (!find_tile(a.m_sizes, a.L, (uint32_t)a.T, blockIdx.x / groups, kRows, 0, false, tile)) {
+        // The grid holds ceil(T / kRows) + min(T, L) tiles, more than the sum of
+        // the adapters' when that is below T: at least one workgroup a column
+        // group gets here.  Each reads all of the gather index, so 512 at most.
+        if (a.copy_unrouted && tile.p0 < a.T) {
+            const int tiles = blockIdx.x / groups - tile.index;
+            const int most = groups < 512 ? 512 / groups : 1;
+            const int workgroups = min((int)(gridDim.x / groups) - tiles, most);
+            if (tile.index < workgroups)
+                copy_unrouted(a, tile.p0, tile.index, workgroups, group * group_cols,
+                              min(a.C, (group + 1) * group_cols),
+                              reinterpret_cast<uint32_t *>(s_out), sizeof(s_out) / 4);
+        }
         return;
+    }
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x & (kWave - 1);
     const int m = lane & 15, g = lane >> 4;
-    const int group = blockIdx.x % groups;
     const int rank = rank_of(a.ranks, tile.a, a.R);
     const int rg = SMALL ? (g & 1) * 8 : g * 8;  // this lane's ranks of a step
 

@@ -25,6 +25,7 @@ struct LoraParams {
     int L, R, C, splits;
     bool scale_shrink;  // the adapter's scale belongs to h (backward), not to out
     bool stream_base;   // base is too large to be worth a place in the caches
+    bool copy_unrouted;  // rows of no adapter get base's row, not what out holds
 };
 
 struct GradParams {
