@@ -502,8 +502,8 @@ moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_
  * moegg_permute_bwd -- gradient of moegg_permute:
  *   dX[t] = sum_{j<topk} w[s] * dXs[row_map[s]]   (fp32, j ascending, rounded once)
  *   dw[s] = sum_n X[t, n] * dXs[row_map[s], n]    (fp32), when dw is not NULL
- * X is read only for dw (and may be NULL without it).  A dropped slot adds
- * nothing and gets dw = 0.  Arguments and errors as moegg_permute.
+ * X is read only for dw (and may be NULL without it); dX may be X.  A dropped
+ * slot adds nothing and gets dw = 0.  Arguments and errors as moegg_permute.
  */
 moegg_status moegg_permute_bwd(const void *dXs, int32_t dtype, const void *X,
                                const int32_t *row_map, const float *topk_weights,
@@ -532,7 +532,7 @@ moegg_status moegg_unpermute(const void *Y, int32_t dtype, const int32_t *row_ma
  *   dw[s] = sum_n dOut[t, n] * Y[row_map[s], n]    (fp32), when dw is not NULL
  * With offsets and padded_offsets the pad rows of dY are set to zero, so that
  * products over the padded rows read no stale values; other rows no slot maps
- * to are left as they were.  Y is read only for dw.
+ * to are left as they were.  Y is read only for dw; dY may be Y.
  */
 moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
                                  const int32_t *row_map, const float *topk_weights,

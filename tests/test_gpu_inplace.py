@@ -1,0 +1,63 @@
+"""Outputs that take the place of an input: the results of a call with buffers
+of its own, bit for bit."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def mg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import token_routing_amd as m
+    m.load_library()
+    return m
+
+
+# T, k, K: one, two and four waves a row, up to eight picks and more
+SORT = [(5, 1, 7), (40, 8, 515), (40, 9, 515), (33, 11, 2048), (20, 17, 129), (70, 64, 1003)]
+
+
+def sorted_inputs(T, k, K, dtype):
+    g = torch.Generator().manual_seed(T * k + K)
+    dt = DT[dtype]
+    scatter = torch.randperm(T * k, generator=g).int()
+    scatter[::7] = -1                              # dropped slots
+    return dict(X=torch.randn(T, K, generator=g).to(dt).cuda(), scatter=scatter.cuda(),
+                rows=torch.randn(T * k, K, generator=g).to(dt).cuda(),
+                w=torch.rand(T * k, generator=g).cuda())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,k,K", SORT)
+def test_permute_gradient_over_its_input(mg, T, k, K, dtype):
+    c = sorted_inputs(T, k, K, dtype)
+    dX, dw = mg.permute_bwd(c["rows"], c["X"], k, c["scatter"], c["w"])
+    X = c["X"].clone()
+    got, dw2 = mg.permute_bwd(c["rows"], X, k, c["scatter"], c["w"], dX=X)
+    assert got is X and torch.equal(X, dX) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,k,K", SORT)
+def test_unpermute_gradient_over_its_input(mg, T, k, K, dtype):
+    c = sorted_inputs(T, k, K, dtype)
+    want = c["rows"].clone()                       # rows no slot maps to stay
+    _, dw = mg.unpermute_bwd(c["X"], c["rows"], k, c["scatter"], c["w"], dY=want)
+    Y = c["rows"].clone()
+    _, dw2 = mg.unpermute_bwd(c["X"], Y, k, c["scatter"], c["w"], dY=Y)
+    assert torch.equal(Y, want) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,k,K", SORT)
+def test_unpermute_onto_its_base(mg, T, k, K, dtype):
+    c = sorted_inputs(T, k, K, dtype)
+    want = mg.unpermute(c["rows"], k, c["scatter"], c["w"], base=c["X"])
+    X = c["X"].clone()
+    mg.unpermute(c["rows"], k, c["scatter"], c["w"], base=X, out=X)
+    assert torch.equal(X, want)

@@ -619,7 +619,7 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
 def permute_bwd(dXs, X, topk: int, row_map, topk_weights=None, *, want_dw: bool = True, dX=None,
                 dw=None, error_flags=None, stream=None):
     """Gradient of permute (moegg_permute_bwd): (dX [T, K], dw fp32 [T*topk] or None).
-    X (the forward's input) is read only for dw."""
+    X (the forward's input) is read only for dw; dX may be X."""
     lib = load_library()
     dev = dXs.device
     index = dev.index
@@ -673,7 +673,7 @@ def unpermute_bwd(dOut, Y, topk: int, row_map, topk_weights=None, *, offsets=Non
     """Gradient of unpermute (moegg_unpermute_bwd): (dY [rows, K], dw fp32 [T*topk] or None).
 
     Y (the forward's input) is read only for dw and may be None without it
-    (`rows` or dY then say how many rows dY has).  With offsets and
+    (`rows` or dY then say how many rows dY has); dY may be Y.  With offsets and
     padded_offsets the pad rows of dY are cleared; rows no slot maps to are
     left as they were.
     """

@@ -244,6 +244,20 @@ __global__ __launch_bounds__(kSortThreads) void collect_kernel(CollectParams a)
             }
     };
 
+    // More slots than the registers hold at once: their dots in a pass of their
+    // own, ahead of the stores, since out may be `other`.
+    if constexpr (DOTS)
+        if (a.topk > kGroup)
+            for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
+                fetch(j0);
+                if (live)
+                    for (int c0 = first; c0 < a.K; c0 += WPR * kWave * P) {
+                        vec_t raw[kGroup];
+                        load_rows(raw, c0 + lane * P);
+                        add_dots(raw, c0 + lane * P);
+                    }
+                store_dots<WPR>(dot, a.dw, t * a.topk + j0, min(kGroup, a.topk - j0), live, s_dot);
+            }
     fetch(0);
     if (live)
         for (int c0 = first; c0 < a.K; c0 += WPR * kWave * P) {
@@ -276,23 +290,9 @@ __global__ __launch_bounds__(kSortThreads) void collect_kernel(CollectParams a)
             }
             store16<DT>(out, col, a.K, acc);
         }
-    if constexpr (DOTS) {
-        if (a.topk <= kGroup) {
+    if constexpr (DOTS)
+        if (a.topk <= kGroup)
             store_dots<WPR>(dot, a.dw, t * a.topk, a.topk, live, s_dot);
-            return;
-        }
-        // More slots than the registers hold at once: their dots in a second pass.
-        for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
-            fetch(j0);
-            if (live)
-                for (int c0 = first; c0 < a.K; c0 += WPR * kWave * P) {
-                    vec_t raw[kGroup];
-                    load_rows(raw, c0 + lane * P);
-                    add_dots(raw, c0 + lane * P);
-                }
-            store_dots<WPR>(dot, a.dw, t * a.topk + j0, min(kGroup, a.topk - j0), live, s_dot);
-        }
-    }
 }
 
 // Waves that share a token's row: as many (1, 2 or 4) as it fills with 16
