@@ -618,8 +618,9 @@ size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_
  *   H          the forward's H.
  *   base, dX   as base and Y in the forward (base: the shared projection's
  *              input gradient; rows without an adapter keep what dX holds, or
- *              get their base row with LORA_ALL_ROWS); dX NULL skips it.  dX may not be X when dA is
- *              asked for: X is read after dX is written.
+ *              get their base row with LORA_ALL_ROWS); dX NULL skips it.  dX
+ *              may not overlap X or dY when dA and dB are asked for (EINVAL):
+ *              both are read after dX is written.
  *   dA, dB     out [L, R, K] and [L, N, R] of `dtype`, fp32 with
  *              MOEGG_LORA_FP32_GRAD; every element is written, zeros for
  *              adapters without rows and past an adapter's rank.  Both NULL

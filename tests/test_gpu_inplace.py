@@ -61,3 +61,31 @@ def test_unpermute_onto_its_base(mg, T, k, K, dtype):
     X = c["X"].clone()
     mg.unpermute(c["rows"], k, c["scatter"], c["w"], base=X, out=X)
     assert torch.equal(X, want)
+
+
+def test_adapter_gradients_beside_their_inputs(mg):
+    """X, dY and dX as column slices of one matrix; dX over dY where no weight
+    gradients are asked for; and the refusals."""
+    T, L, R, K = 70, 3, 16, 72
+    g = torch.Generator().manual_seed(1)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g).bfloat16().cuda()
+
+    sizes = torch.tensor([30, 0, 40], dtype=torch.int32).cuda()
+    X, dY, base, A, B = rnd(T, K), rnd(T, K), rnd(T, K), rnd(L, R, K), rnd(L, K, R)
+    H = torch.randn(T, R, generator=g).cuda()
+    want = mg.lora_bwd(X, dY, A, B, H, sizes, base=base)
+    wide = torch.zeros(T, 3 * K + 5, dtype=torch.bfloat16, device="cuda")
+    x, d, o = (wide[:, i * K + 2:(i + 1) * K + 2] for i in (0, 2, 1))
+    x.copy_(X)
+    d.copy_(dY)
+    got = mg.lora_bwd(x, d, A, B, H, sizes, base=base, dX=o)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    over = dY.clone()
+    mg.lora_bwd(None, over, A, B, None, sizes, base=base, dX=over, want_weights=False)
+    assert torch.equal(over, want[0])
+    for dX in (X, dY):
+        with pytest.raises(Exception, match="moegg_lora_bwd"):
+            mg.lora_bwd(X, dY, A, B, H, sizes, base=base, dX=dX)

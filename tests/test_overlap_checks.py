@@ -1,0 +1,60 @@
+"""Refusals of outputs that overlap an input which is read after they are
+written.  Every call here fails on the host, before anything is enqueued."""
+
+import ctypes
+import os
+
+import pytest
+
+EINVAL = 1
+BF16 = 0
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import token_routing_amd as mg
+    if not os.path.exists(mg.LIB_PATH):
+        from token_routing_amd import build
+        build.build()
+    return mg.load_library()
+
+
+T, L, R, K, N = 10, 4, 16, 64, 64
+AT = 1 << 20                                       # never dereferenced
+FAR = ctypes.c_void_p(1 << 24)
+
+
+def bwd(lib, X, ldx, dY, lddy, dX, lddx):
+    # no workspace: a call that passes the other checks is refused for that
+    # (EWORKSPACE) and enqueues nothing either
+    p = ctypes.c_void_p
+    return lib.moegg_lora_bwd(p(X), ldx, p(dY), lddy, FAR, FAR, FAR, FAR, FAR, None, None, BF16, T,
+                              L, R, K, N, p(dX), lddx, p(dX), lddx, FAR, FAR, 0, None, 0, None, None)
+
+
+@pytest.mark.parametrize("dX,lddx", [
+    (AT, K),                                       # the same matrix
+    (AT + 2 * 8, K),                               # begins inside it
+    (AT - 2 * K * (T - 1), K),                     # ends in its first row
+    (AT + 2 * K * (T - 1), K),                     # begins in its last
+    (AT + 6, 100),                                 # another stride across it
+])
+@pytest.mark.parametrize("over", ["X", "dY"])
+def test_adapter_gradient_over_its_input(lib, over, dX, lddx):
+    other = AT + (1 << 20)
+    args = (AT, K, other, N) if over == "X" else (other, K, AT, N)
+    assert bwd(lib, *args, dX, lddx) == EINVAL
+
+
+@pytest.mark.parametrize("dX,lddx,ld", [
+    (AT + 2 * K * T, K, K),                        # right behind
+    (AT - 2 * K * T, K, K),                        # right in front
+    (AT + 2 * K, 200, 200),                        # column slices of one matrix
+    (AT - 2 * K, 200, 200),
+    (AT + 2 * 200 * 3 + 2 * K, 200, 200),          # some rows further down, beside
+])
+@pytest.mark.parametrize("over", ["X", "dY"])
+def test_adapter_gradient_beside_its_input(lib, over, dX, lddx, ld):
+    other = AT + (1 << 20)
+    args = (AT, ld, other, N) if over == "X" else (other, K, AT, ld)
+    assert bwd(lib, *args, dX, lddx) == 4          # EWORKSPACE: past the overlap check

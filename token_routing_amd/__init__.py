@@ -782,7 +782,8 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
 
     base [T, K]: the shared projection's input gradient, which dX adds to; None
     adds to the dX given.  Rows without an adapter get their base row in a new
-    dX, and keep what a given dX holds.  want_dx=False or want_weights=False leave dX or dA
+    dX, and keep what a given dX holds.  A given dX may not overlap X or dY
+    unless want_weights=False.  want_dx=False or want_weights=False leave dX or dA
     and dB out (None in their place).  fp32_grads writes dA and dB in fp32.
     """
     lib = load_library()

@@ -774,6 +774,26 @@ static bool stride_ok(int64_t ld, int64_t n, int64_t T)
     return ld >= n && ld <= INT32_MAX && (T == 0 || ld <= ((int64_t)1 << 39) / T);
 }
 
+// Whether two matrices of T rows of 16-bit elements share any.  With one row
+// stride (column slices of one matrix, say) columns and rows decide; with two
+// any common stretch of memory counts.
+static bool rows_overlap(const void *a, int64_t ld_a, int64_t cols_a, const void *b, int64_t ld_b,
+                         int64_t cols_b, int64_t T)
+{
+    if (!a || !b || T == 0)
+        return false;
+    const int64_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
+    const int64_t end_a = pa + 2 * ((T - 1) * ld_a + cols_a);
+    const int64_t end_b = pb + 2 * ((T - 1) * ld_b + cols_b);
+    if (pa >= end_b || pb >= end_a)
+        return false;
+    if (ld_a != ld_b)
+        return true;
+    const int64_t row = 2 * ld_a;
+    const int64_t shift = ((pb - pa) % row + row) % row;  // b's first column in a's rows
+    return shift < 2 * cols_a || shift + 2 * cols_b > row;
+}
+
 static size_t lora_h_bytes(int64_t T, int32_t L, int32_t R, int32_t C)
 {
     // 32 bytes behind the last row: it is read in pieces of 8 values
@@ -936,8 +956,12 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     if (num_rows > 0 && (!dY || !A || !B || !aligned2(dY) || !aligned2(A) || !aligned2(B)))
         return MOEGG_EINVAL;
     if (dA) {
-        if (num_rows > 0 && (!X || !H || !aligned2(X) || !aligned4(H) || X == dX))
-            return MOEGG_EINVAL;  // dX is written before X is read for dA
+        if (num_rows > 0 && (!X || !H || !aligned2(X) || !aligned4(H)))
+            return MOEGG_EINVAL;
+        // dX is written before X is read for dA and dY for dB
+        if (rows_overlap(dX, lddx, K, X, ldx, K, num_rows) ||
+            rows_overlap(dX, lddx, K, dY, lddy, N, num_rows))
+            return MOEGG_EINVAL;
         if ((flags & MOEGG_LORA_FP32_GRAD) ? !aligned4(dA) || !aligned4(dB)
                                            : !aligned2(dA) || !aligned2(dB))
             return MOEGG_EINVAL;
