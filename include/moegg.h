@@ -433,6 +433,8 @@ moegg_status moegg_combine_bwd(const void *dOut, const void *Y, const int32_t *s
  *   bias         [E] fp32 device, or NULL.
  *   topk_ids     out [T, topk] int32.    topk_weights  out [T, topk] fp32.
  *   scores       out [T, E] fp32, or NULL (a load-balancing loss reads them).
+ *                Without bias and groups they may take the logits' place
+ *                (fp32, ld_logits = E); any other overlap is EINVAL.
  * T = 0 is a no-op.  Errors: ESHAPE for sizes outside 1 <= E <=
  * MOEGG_MAX_EXPERTS, 1 <= topk <= min(E, MOEGG_MAX_TOPK), 1 <= topk_groups <=
  * n_groups <= MOEGG_MAX_GATE_GROUPS, n_groups dividing E, topk <=
@@ -453,7 +455,9 @@ moegg_status moegg_gate(const void *logits, int32_t dtype, int64_t ld_logits, co
  *   topk_ids     [T, topk] int32 as moegg_gate wrote them; a negative id has
  *                no gradient, an id >= E none either (MOEGG_DERR_EXPERT_ID).
  *   dweights     [T, topk] fp32.   dscores  [T, E] fp32, or NULL for zero.
- *   dlogits      out [T, E] of `dtype`, contiguous; masked experts get 0.
+ *   dlogits      out [T, E] of `dtype`, contiguous; masked experts get 0.  May
+ *                take the logits' place (ld_logits = E; any other overlap is
+ *                EINVAL) or that of dscores in fp32.
  * scale and flags as in the forward; the scores are computed again from the
  * logits.  Sums in fp32, one rounding to `dtype`.  Errors as moegg_gate.
  */

@@ -89,3 +89,50 @@ def test_adapter_gradients_beside_their_inputs(mg):
     for dX in (X, dY):
         with pytest.raises(Exception, match="moegg_lora_bwd"):
             mg.lora_bwd(X, dY, A, B, H, sizes, base=base, dX=dX)
+
+
+# E, k, bias, groups, sigmoid, renorm
+GATE = [(8, 2, False, 1, False, True), (60, 6, True, 1, False, False), (64, 8, True, 8, True, True),
+        (128, 8, False, 1, True, False), (256, 8, True, 8, False, False),
+        (511, 10, True, 1, True, False), (1024, 64, False, 8, False, True)]
+
+
+@pytest.mark.parametrize("E,k,has_bias,groups,sigmoid,renorm", GATE)
+def test_gate_scores_over_the_logits(mg, E, k, has_bias, groups, sigmoid, renorm):
+    g = torch.Generator().manual_seed(E + k)
+    T = 77
+    l = torch.randn(T, E, generator=g) * 3
+    l[torch.rand(T, E, generator=g) < 0.1] = -float("inf")
+    l[5] = -float("inf")
+    l = l.cuda()
+    kw = dict(bias=torch.randn(E, generator=g).cuda() if has_bias else None, n_groups=groups,
+              topk_groups=max(1, groups // 2), sigmoid=sigmoid, renorm=renorm)
+    ids, w, s = mg.moe_gate(l, k, want_scores=True, **kw)
+    over = l.clone()
+    if has_bias or groups > 1:                     # the picks' logits are read behind the scores
+        with pytest.raises(mg.MoeggError):
+            mg.moe_gate(over, k, scores=over, **kw)
+        assert torch.equal(over, l)
+        return
+    ids2, w2, s2 = mg.moe_gate(over, k, scores=over, **kw)
+    assert s2 is over and torch.equal(over, s)
+    assert torch.equal(ids2, ids) and torch.equal(w2, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,k,has_bias,groups,sigmoid,renorm", GATE)
+def test_gate_gradient_over_an_input(mg, E, k, has_bias, groups, sigmoid, renorm, dtype):
+    g = torch.Generator().manual_seed(2 * E + k)
+    T = 77
+    l = (torch.randn(T, E, generator=g) * 3).to(DT[dtype]).cuda()
+    ids, w, s = mg.moe_gate(l, k, sigmoid=sigmoid, renorm=renorm, want_scores=True)
+    gw, gs = torch.randn(T, k, generator=g).cuda(), torch.randn(T, E, generator=g).cuda()
+    kw = dict(sigmoid=sigmoid, renorm=renorm)
+    want = mg.moe_gate_bwd(l, ids, gw, dscores=gs, **kw)
+    over = l.clone()
+    mg.moe_gate_bwd(over, ids, gw, dscores=gs, dlogits=over, **kw)
+    assert torch.equal(over, want)
+    if dtype == "fp32":
+        over = gs.clone()
+        mg.moe_gate_bwd(l, ids, gw, dscores=over, dlogits=over, **kw)
+        assert torch.equal(over, want)

@@ -58,3 +58,35 @@ def test_adapter_gradient_beside_its_input(lib, over, dX, lddx, ld):
     other = AT + (1 << 20)
     args = (AT, ld, other, N) if over == "X" else (other, K, AT, ld)
     assert bwd(lib, *args, dX, lddx) == 4          # EWORKSPACE: past the overlap check
+
+
+FP32 = 2
+
+
+def gate(lib, logits, dtype, ld, scores, T=10, E=64, bias=None, groups=1):
+    p = ctypes.c_void_p
+    return lib.moegg_gate(p(logits), dtype, ld, bias, T, E, 2, groups, 1, 1.0, 0, FAR, FAR,
+                          p(scores), None, None)
+
+
+@pytest.mark.parametrize("dtype,ld,scores,bias,groups", [
+    (FP32, 64, AT, FAR, 1),                        # in place, but the logits are read again
+    (FP32, 64, AT, None, 8),
+    (FP32, 80, AT, None, 1),                       # other rows
+    (FP32, 64, AT + 4, None, 1),
+    (FP32, 64, AT - 4, None, 1),
+    (FP32, 64, AT + 4 * 639, None, 1),             # the last logit
+    (BF16, 64, AT, None, 1),                       # another type
+    (BF16, 64, AT + 2 * 636, None, 1),
+])
+def test_gate_scores_across_the_logits(lib, dtype, ld, scores, bias, groups):
+    assert gate(lib, AT, dtype, ld, scores, bias=bias, groups=groups) == EINVAL
+
+
+@pytest.mark.parametrize("dtype,ld,out", [
+    (FP32, 80, AT), (FP32, 64, AT + 4), (BF16, 64, AT - 2), (BF16, 65, AT),
+])
+def test_gate_gradient_across_the_logits(lib, dtype, ld, out):
+    p = ctypes.c_void_p
+    assert lib.moegg_gate_bwd(p(AT), dtype, ld, FAR, FAR, None, 10, 64, 2, 1.0, 0, p(out), None,
+                              None) == EINVAL

@@ -504,6 +504,18 @@ moegg_status moegg_combine_bwd(const void *dOut, const void *Y, const int32_t *s
                           : moegg::combine_bwd_any_launch(p, static_cast<hipStream_t>(stream)));
 }
 
+// Whether a [T, E] output of the gate overlaps its logits other than element
+// for element (in place).
+static bool beside_logits(const void *out, int64_t out_size, const void *logits, int32_t dtype,
+                          int64_t ld, int64_t T, int64_t E)
+{
+    const int64_t size = dtype == MOEGG_FP32 ? 4 : 2;
+    const int64_t po = reinterpret_cast<intptr_t>(out), pl = reinterpret_cast<intptr_t>(logits);
+    if (!out || po >= pl + ((T - 1) * ld + E) * size || pl >= po + T * E * out_size)
+        return false;
+    return po != pl || out_size != size || (ld != E && T > 1);
+}
+
 // Shared checks of the gate entry points.
 static moegg_status check_gate(const void *logits, int32_t dtype, int64_t ld, int64_t num_tokens,
                                int32_t E, int32_t topk, float scale, uint32_t flags)
@@ -539,6 +551,10 @@ moegg_status moegg_gate(const void *logits, int32_t dtype, int64_t ld_logits, co
     if (!topk_ids || !topk_weights || !aligned4(topk_ids) || !aligned4(topk_weights) ||
         !aligned4(scores) || !aligned4(bias))
         return MOEGG_EINVAL;
+    // With a bias or groups the picks' logits are read again after scores are written.
+    if (beside_logits(scores, 4, logits, dtype, ld_logits, num_tokens, num_experts) ||
+        (scores == logits && (bias || n_groups > 1)))
+        return MOEGG_EINVAL;
     moegg::GateParams p;
     p.logits = logits;
     p.bias = bias;
@@ -572,6 +588,9 @@ moegg_status moegg_gate_bwd(const void *logits, int32_t dtype, int64_t ld_logits
         return MOEGG_OK;
     if (!topk_ids || !dweights || !dlogits || !aligned4(topk_ids) || !aligned4(dweights) ||
         !aligned4(dscores) || !aligned_elem(dlogits, dtype))
+        return MOEGG_EINVAL;
+    if (beside_logits(dlogits, dtype == MOEGG_FP32 ? 4 : 2, logits, dtype, ld_logits, num_tokens,
+                      num_experts))
         return MOEGG_EINVAL;
     moegg::GateBwdParams p;
     p.logits = logits;
