@@ -494,7 +494,9 @@ moegg_status moegg_gate_bwd(const void *logits, int32_t dtype, int64_t ld_logits
  * Errors: ESHAPE for T < 0 or past 16 million, topk < 1, K < 1, rows < 0,
  * sizes past 2^40 bytes, E outside [1, MOEGG_MAX_EXPERTS] in the padded layout; EINVAL for an unknown
  * dtype, one of offsets / padded_offsets without the other, NULL or
- * misaligned pointers (rows need the alignment of one element only).
+ * misaligned pointers (rows need the alignment of one element only), Xs over
+ * X (in these four calls an output overlaps an input's rows only where that is
+ * said, and then row for row).
  */
 moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_idx,
                            const float *topk_weights, const int32_t *offsets,

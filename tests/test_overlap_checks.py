@@ -90,3 +90,39 @@ def test_gate_gradient_across_the_logits(lib, dtype, ld, out):
     p = ctypes.c_void_p
     assert lib.moegg_gate_bwd(p(AT), dtype, ld, FAR, FAR, None, 10, 64, 2, 1.0, 0, p(out), None,
                               None) == EINVAL
+
+
+# 10 tokens of 64 bf16 columns (1280 bytes), two picks each (2560 bytes)
+SORTED = AT + (1 << 20)
+
+
+def sort_call(lib, name, tok, other, rows):
+    p, none = ctypes.c_void_p, None
+    if name == "permute":
+        return lib.moegg_permute(p(tok), BF16, FAR, none, none, none, 10, 2, 0, 64, 20, p(rows),
+                                 none, none, none)
+    if name == "permute_bwd":
+        return lib.moegg_permute_bwd(p(rows), BF16, p(other), FAR, none, 10, 2, 64, 20, p(tok), FAR,
+                                     none, none)
+    if name == "unpermute":
+        return lib.moegg_unpermute(p(rows), BF16, FAR, none, p(other), 10, 2, 64, 20, p(tok), none,
+                                   none)
+    return lib.moegg_unpermute_bwd(p(tok), BF16, p(other), FAR, none, none, none, 10, 2, 0, 64, 20,
+                                   p(rows), FAR, none, none)
+
+
+@pytest.mark.parametrize("shift", [0, 2, -2, 1278, -2558])
+@pytest.mark.parametrize("name", ["permute", "permute_bwd", "unpermute", "unpermute_bwd"])
+def test_token_rows_across_sorted_rows(lib, name, shift):
+    """tok at AT, the 20 sorted rows from `shift` bytes behind it."""
+    assert sort_call(lib, name, AT, SORTED + (1 << 18), AT + shift) == EINVAL
+
+
+@pytest.mark.parametrize("name,shift", [("permute_bwd", 128), ("permute_bwd", -2),
+                                        ("unpermute", 2), ("unpermute", -1278),
+                                        ("unpermute_bwd", 128), ("unpermute_bwd", -2558)])
+def test_output_beside_its_place(lib, name, shift):
+    """The input that the output may replace, but not row for row."""
+    out = SORTED if name == "unpermute_bwd" else AT
+    tok, rows = (AT, SORTED)
+    assert sort_call(lib, name, tok, out + shift, rows) == EINVAL

@@ -633,6 +633,17 @@ static moegg_status check_sort(const void *tok, const void *sorted, int32_t dtyp
     return MOEGG_OK;
 }
 
+// Whether two matrices of [rows, K] elements share memory; of one place and
+// size they may where that is said (the kernels then read an element before
+// they write it).
+static bool sort_overlap(const void *a, int64_t rows_a, const void *b, int64_t rows_b, int32_t K,
+                         int32_t dtype, bool in_place)
+{
+    const int64_t row = (int64_t)K * (dtype == MOEGG_FP32 ? 4 : 2);
+    const int64_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
+    return a && b && pa < pb + rows_b * row && pb < pa + rows_a * row && !(in_place && pa == pb);
+}
+
 // The padded layout's metadata: both offset arrays or neither.
 static moegg_status check_padded(const int32_t *offsets, const int32_t *padded, int32_t E,
                                  const void *sorted, int32_t dtype, int64_t rows)
@@ -665,6 +676,8 @@ moegg_status moegg_permute(const void *X, int32_t dtype, const int32_t *scatter_
     if (num_tokens > 0 &&
         ((padded_offsets && (!row_map || row_map == scatter_idx)) || !aligned4(row_map)))
         return MOEGG_EINVAL;
+    if (sort_overlap(Xs, rows, X, num_tokens, K, dtype, false))
+        return MOEGG_EINVAL;
     moegg::SpreadParams p = {};
     p.src = X;
     p.map = scatter_idx;
@@ -692,6 +705,9 @@ moegg_status moegg_permute_bwd(const void *dXs, int32_t dtype, const void *X,
         return st;
     if (dw && (!X || !aligned_elem(X, dtype) || !aligned4(dw)))
         return MOEGG_EINVAL;
+    if (sort_overlap(dX, num_tokens, dXs, rows, K, dtype, false) ||
+        (dw && sort_overlap(dX, num_tokens, X, num_tokens, K, dtype, true)))
+        return MOEGG_EINVAL;
     moegg::CollectParams p = {};
     p.rows_in = dXs;
     p.other = dw ? X : nullptr;
@@ -716,6 +732,9 @@ moegg_status moegg_unpermute(const void *Y, int32_t dtype, const int32_t *row_ma
     if (st != MOEGG_OK || num_tokens == 0)
         return st;
     if (base && !aligned_elem(base, dtype))
+        return MOEGG_EINVAL;
+    if (sort_overlap(out, num_tokens, Y, rows, K, dtype, false) ||
+        sort_overlap(out, num_tokens, base, num_tokens, K, dtype, true))
         return MOEGG_EINVAL;
     moegg::CollectParams p = {};
     p.rows_in = Y;
@@ -745,6 +764,9 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
     if (st != MOEGG_OK)
         return st;
     if (num_tokens > 0 && dw && ((rows > 0 && !Y) || !aligned_elem(Y, dtype) || !aligned4(dw)))
+        return MOEGG_EINVAL;
+    if (sort_overlap(dY, rows, dOut, num_tokens, K, dtype, false) ||
+        (dw && sort_overlap(dY, rows, Y, rows, K, dtype, true)))
         return MOEGG_EINVAL;
     moegg::SpreadParams p = {};
     p.src = dOut;
