@@ -148,3 +148,37 @@ def test_captured_with_changing_routing(mg):
         want = c["base"].clone()
         mg.lora_fwd(*args, Y=want)
         assert torch.equal(Y, want), drop
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 0.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [40, 300])
+def test_rank_zero_takes_nothing_from_its_adapter(mg, T, dtype, scale):
+    """An adapter of rank 0 leaves base as it is and has zero gradients, also
+    where its place holds NaN weights and a scale that is not a number."""
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(T)
+    L, R, K, N = 3, 16, 64, 192
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g).to(dt).cuda()
+
+    X, dY, base, dbase, A, B = rnd(T, K), rnd(T, N), rnd(T, N), rnd(T, K), rnd(L, R, K), rnd(L, N, R)
+    A[1], B[1] = float("nan"), float("nan")
+    ids = (torch.arange(T, dtype=torch.int32) % L).cuda()
+    r = mg.moe_route(ids.view(T, 1), L, 16)
+    ranks = torch.tensor([16, 0, 7], dtype=torch.int32).cuda()
+    good = torch.tensor([1.5, 1.0, 0.5]).cuda()
+    bad = torch.tensor([1.5, scale, 0.5]).cuda()
+    out = {}
+    for name, scales in (("good", good), ("bad", bad)):
+        Y, H = mg.lora_fwd(X, A, B, r["m_sizes"], r["gather"], ranks=ranks, scales=scales,
+                           base=base, want_h=True)
+        out[name] = (Y, H, *mg.lora_bwd(X, dY, A, B, H, r["m_sizes"], r["gather"], ranks=ranks,
+                                        scales=scales, base=dbase))
+    none = ids == 1
+    Y, _, dX, dA, dB = out["bad"]
+    assert torch.equal(Y[none], base[none]) and torch.equal(dX[none], dbase[none])
+    assert not dA[1].any() and not dB[1].any()
+    for a, b in zip(out["good"], out["bad"]):
+        assert torch.equal(a, b)

@@ -716,7 +716,8 @@ expand_kernel(LoraParams a, int groups, int group_cols)
     if (wave < RT) {
         const int t = wave * 16 + m;
         const int p = tile.p0 + min(t, tile.rows - 1);
-        float factor = !a.scale_shrink && a.scales ? a.scales[tile.a] : 1.0f;
+        // Rank 0 is no adapter, whatever its scale holds.
+        float factor = !a.scale_shrink && a.scales && rank > 0 ? a.scales[tile.a] : 1.0f;
         float v[NS][8];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
