@@ -582,7 +582,9 @@ def permute(X, scatter_idx, topk: int, topk_weights=None, *, offsets=None, padde
     `rows` or the block_m that was routed with.  Returns (Xs [rows, K],
     row_map int32 [T*topk]); rows past the last expert's are left as they were
     (a new Xs leaves them uninitialised).  Without padding the map is
-    scatter_idx itself unless a row_map is given to write it to.
+    scatter_idx itself, its buffer and its entries as they are, unless a
+    row_map is given to write it to: give one where scatter_idx is written again
+    before the backward, or may hold rows past Xs (a written map has -1 there).
     """
     lib = load_library()
     dev = X.device

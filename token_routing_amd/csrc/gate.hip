@@ -10,7 +10,7 @@
 // A token is held by G = 8 to 64 lanes of one wave, V logits a lane, all in
 // registers: the logits are read once, and maxima, sums and the k picks are
 // reductions over the G lanes, which bound the kernel (its bytes would take a
-// tenth of the time).  Both scores rise with the logit, so without
+// fifth of the time, a fifteenth with keys in 64 bits).  Both scores rise with the logit, so without
 // bias and groups the picks compare the logits themselves and need no exp;
 // with them the keys are computed and compared in 64 bits, because keys of
 // different experts come as close as a rounding of 32 bits and the pick must

@@ -6,12 +6,15 @@
 //             dx[src(p)] = base[src(p)] + dh[p] A_a       (expand, A transposed)
 //             dA_a = sum_p dh[p]^T x[src(p)], dB_a = s_a sum_p dy[src(p)]^T h[p]  (grad)
 //
-// for sorted position p of adapter a.  With ranks of 4 to 256 against rows of
+// for sorted position p of adapter a.  With ranks up to 64 against rows of
 // thousands of columns every one of these is bound by moving x, y and dy, not
 // by its matrix instructions (16 x 16 x 32, fp32 accumulators).  So no tile is
 // staged for reuse between waves: a wave loads what it multiplies, 8 reduction
 // elements (16 contiguous bytes) a lane, and LDS only moves values between the
 // lanes of a wave where the layout of a fragment would waste cache lookups.
+// Above rank 64 that costs: shrink's 16-row tiles read 8 (rank 128) to 16 times
+// (256) their rows' bytes in weights from the caches, and grad reads x and dy
+// once for every 32 ranks.
 //
 // Operands whose reduction runs along a strided index (B in dh, A in dx, x and
 // dy in the gradients) are loaded as 8 rows of up to 8 contiguous elements a
@@ -24,9 +27,8 @@
 // ones before, at as many matrix instructions, of which there are few.  Two in
 // fp16 keep 22 bits of mantissa.  In bf16 expand takes two, 16 bits, since its
 // output is rounded to 8; the gradients, which may be fp32, take three, which
-// hold an fp32 value whole (with two the gradients of one adapter's rows were
-// off by 2.5e-6 instead of 3e-7; the third is not measurable in the call's
-// time: 54.3 us with two, 53.3 with three).  With ranks up to 16 expand's two
+// hold an fp32 value whole (4096 rows, rank 32: fp32 gradients off by 2.5e-6 in
+// norm with two, 1.8e-7 with three; the call took 53.8 us with either).  With ranks up to 16 expand's two
 // parts share one instruction: its 32 reduction elements hold 16 high and 16
 // low ones.  fp16 parts are scaled by a power of two first, so that values past
 // the type's range survive.
@@ -550,7 +552,11 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 //
 // SMALL: ranks up to 16, both parts of h in one instruction.  EDGE: columns that
 // are no whole passes (the last one goes by single elements) or ranks that are
-// no whole pieces of 8.  expand_places: workgroups a compute unit, by registers.
+// no whole pieces of 8.  expand_places: workgroups a compute unit, by registers, and
+// above rank 128 with 64-row tiles by shared memory (83 KB a workgroup).
+// Registers spilled to scratch, of 256: 30 to 46 in the 64-row dX at ranks 65 to
+// 128 (37.6 us at rank 128, 4096 rows of 4096 columns, where the forward takes
+// 26.6); 15 at most in ten forms of other ranks and tiles.
 constexpr int expand_places(bool TR, int NS, int RT)
 {
     return RT == 1 ? (NS <= 2 ? 4 : NS == 8 && TR ? 2 : 3)
@@ -946,8 +952,9 @@ expand_kernel(LoraParams a, int groups, int group_cols)
 // A step is 8 rows of 16 bytes a lane, issued together; the rows' numbers are
 // loaded a step ahead.  Rows past the chunk's end repeat its last row and are
 // set to zero.  dh comes summed over shrink's splits.  4096 rows, 4 adapters of
-// rank 32, K = N = 4096: 19.7 us for 67 MB of x and dy (3.4 TB/s), two waves a
-// SIMD by registers.  Lanes past the last column load the row's last 8 elements and
+// rank 32, K = N = 4096: 19.6 us for 67 MB of x and dy (3.4 TB/s), two waves a
+// SIMD by registers and 1613 vector instructions a wave; every further 32 ranks
+// read x and dy again: 29.9 us at rank 64, 61 us at 128.  Lanes past the last column load the row's last 8 elements and
 // store only what is their own.
 template <int DT, int RG>
 __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
