@@ -126,3 +126,10 @@ def test_output_beside_its_place(lib, name, shift):
     out = SORTED if name == "unpermute_bwd" else AT
     tok, rows = (AT, SORTED)
     assert sort_call(lib, name, tok, out + shift, rows) == EINVAL
+
+
+def test_no_tokens_overlap_nothing(lib):
+    """An empty X that begins inside Xs (an empty slice of one buffer)."""
+    p, none = ctypes.c_void_p, None
+    assert lib.moegg_permute(p(AT + 128), BF16, FAR, none, none, none, 0, 2, 0, 64, 20, p(AT), none,
+                             none, none) == 0

@@ -641,7 +641,8 @@ static bool sort_overlap(const void *a, int64_t rows_a, const void *b, int64_t r
 {
     const int64_t row = (int64_t)K * (dtype == MOEGG_FP32 ? 4 : 2);
     const int64_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
-    return a && b && pa < pb + rows_b * row && pb < pa + rows_a * row && !(in_place && pa == pb);
+    return a && b && rows_a > 0 && rows_b > 0 && pa < pb + rows_b * row &&
+           pb < pa + rows_a * row && !(in_place && pa == pb);
 }
 
 // The padded layout's metadata: both offset arrays or neither.
