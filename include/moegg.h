@@ -581,8 +581,9 @@ moegg_status moegg_unpermute_bwd(const void *dOut, int32_t dtype, const void *Y,
  *              no initialisation.
  * Rows at no sorted position below the sum of m_sizes (moegg_route's dropped
  * ids) keep what Y holds; moegg_lora_fwd_all_rows gives them their base row.
- * H's rows at positions from that sum on are left as they were.  h is kept in fp32 and enters the second product with 16
- * (bf16) or 22 (fp16) bits of mantissa; sums in fp32; Y is rounded once.
+ * H's rows at positions from that sum on are left as they were.  h is kept in
+ * fp32 and enters the second product with all 24 bits of its mantissa in bf16
+ * and 22 in fp16; sums in fp32; Y is rounded once.
  * Bit-for-bit deterministic.  Any K and N from 8 on and any strides; rows need
  * the alignment of one element.  T = 0 is a no-op.
  * Errors: ESHAPE for T < 0, L outside [1, MOEGG_MAX_EXPERTS], R outside
@@ -632,9 +633,7 @@ size_t moegg_lora_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_
  *              adapters without rows and past an adapter's rank.  Both NULL
  *              skips them (X and H are then not read and may be NULL).
  *   workspace  moegg_lora_bwd_workspace_bytes(...) bytes.
- * dh enters the product of dX as h does in the forward; dh and H enter dA and
- * dB with all 24 bits of an fp32 value (bf16) or 22 (fp16), so that
- * LORA_FP32_GRAD gets gradients of fp32 precision.
+ * dh and H enter the products as h does in the forward.
  * Arguments, determinism and errors otherwise as in the forward;
  * EINVAL for one of dA and dB without the other.  T = 0 writes zeros to dA
  * and dB.

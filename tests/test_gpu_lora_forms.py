@@ -248,3 +248,60 @@ def test_fp32_gradients_hold_fp32_values(mg, R, dtype):
         rel = (got.cpu().double() - ref).abs() / ref.abs().clamp(min=1e-30)
         assert float(rel[ref != 0].max()) <= part + 5 * U
         assert torch.all(got.cpu()[ref == 0] == 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 40], ids=["one-row", "many-rows"])
+@pytest.mark.parametrize("R", [9, 16, 24, 64, 128, 256])
+def test_outputs_where_base_and_adapter_cancel(mg, R, rows, dtype):
+    """base is minus the adapter's product, rounded, so the output is what that
+    rounding left: it shows every bit that h or dh loses on its way into the
+    product.  Each output column takes one rank (the others' weights are zero),
+    so there is one product an element.  bf16 parts hold all 24 bits of h and
+    fp16 parts leave 2^-22 at most; adding up to three parts, the scale and base
+    round five times (2^-23 each, of the product), dh once more."""
+    L, K, N = 7, 72, 136
+    T = L * rows
+    g = torch.Generator().manual_seed(R + rows)
+    dt = DT[dtype]
+    half, part = torch.finfo(dt).eps / 2, 0.0 if dtype == "bf16" else 2.0 ** -22
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    one = torch.arange(L).repeat_interleave(rows)
+    sizes = torch.full((L,), rows, dtype=torch.int32).cuda()
+    s = torch.rand(L, generator=g) + 0.5
+    X = torch.randn(T, K, generator=g).to(dt)
+    A = torch.randn(L, R, K, generator=g).to(dt)
+    B = torch.zeros(L, N, R)
+    pick = torch.randint(0, R, (L, N), generator=g)
+    B.scatter_(2, pick[:, :, None], torch.rand(L, N, 1, generator=g) + 0.5)
+    B = B.to(dt)
+
+    def check(got, base, prod, bound):
+        ref = base.double() + prod
+        err = (got.cpu().double() - ref).abs()
+        assert torch.all(err <= half * ref.abs() * (1 + half) + bound + tiny), float(err.max())
+
+    zero = torch.zeros(T, N, dtype=dt).cuda()
+    H = mg.lora_fwd(X.cuda(), A.cuda(), B.cuda(), sizes, scales=s.cuda(), base=zero,
+                    want_h=True)[1]
+    prod = s.double()[one][:, None] * torch.stack(
+        [B[a].double() @ H[t].cpu().double() for t, a in enumerate(one.tolist())])
+    base = (-prod).to(dt)
+    Y, _ = mg.lora_fwd(X.cuda(), A.cuda(), B.cuda(), sizes, scales=s.cuda(), base=base.cuda())
+    check(Y, base, prod, (part + 5 * U) * prod.abs())
+
+    # dX: dY has one column that is not zero, so dh is one product; A one rank a column
+    dY = torch.zeros(T, N, dtype=dt)
+    dY[torch.arange(T), torch.randint(0, N, (T,), generator=g)] = 1.5
+    B2 = torch.randn(L, N, R, generator=g).to(dt)
+    A2 = torch.zeros(L, R, K)
+    pick = torch.randint(0, R, (L, K), generator=g)
+    A2.scatter_(1, pick[:, None, :], torch.rand(L, 1, K, generator=g) + 0.5)
+    A2 = A2.to(dt)
+    dh = torch.stack([s.double()[a] * (dY[t].double() @ B2[a].double())
+                      for t, a in enumerate(one.tolist())])
+    prod = torch.stack([dh[t] @ A2[a].double() for t, a in enumerate(one.tolist())])
+    base = (-prod).to(dt)
+    dX, _, _ = mg.lora_bwd(None, dY.cuda(), A2.cuda(), B2.cuda(), None, sizes, scales=s.cuda(),
+                           base=base.cuda(), want_weights=False)
+    check(dX, base, prod, (part + 6 * U) * prod.abs())

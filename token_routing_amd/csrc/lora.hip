@@ -25,13 +25,15 @@
 // h and dh stay in fp32 between the kernels.  Where one enters a matrix
 // instruction it goes as the sum of 16-bit values, each the rounded rest of the
 // ones before, at as many matrix instructions, of which there are few.  Two in
-// fp16 keep 22 bits of mantissa.  In bf16 expand takes two, 16 bits, since its
-// output is rounded to 8; the gradients, which may be fp32, take three, which
-// hold an fp32 value whole (4096 rows, rank 32: fp32 gradients off by 2.5e-6 in
-// norm with two, 1.8e-7 with three; the call took 53.8 us with either).  With ranks up to 16 expand's two
-// parts share one instruction: its 32 reduction elements hold 16 high and 16
-// low ones.  fp16 parts are scaled by a power of two first, so that values past
-// the type's range survive.
+// fp16 keep 22 bits of mantissa, three in bf16 hold an fp32 value whole.  Two in
+// bf16 kept 16 bits, which showed in fp32 gradients (4096 rows, rank 32: off by
+// 2.5e-6 in norm, 1.8e-7 with three) and in outputs where base and the adapter
+// cancel; the third part costs nothing in the gradients (53.8 us the call with
+// either), 1 us of 139 in expand at rank 64 into 28672 columns, 2 of 59 at rank
+// 128 and 4 of 71 at rank 256.  With ranks up to 16 two parts share one
+// instruction of expand: its 32 reduction elements hold 16 of each.  fp16 parts
+// are scaled by a power of two first, so that values past the type's range
+// survive.
 //
 // Rows go by tiles inside one adapter's segment; each wave finds its tile by
 // a scan of m_sizes in registers (64 segments a step), so no launch depends
@@ -536,7 +538,7 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 //
 // A workgroup takes up to RT * 16 rows of one adapter and a run of columns, its
 // waves 64 columns each at a time; rows past the tile's repeat its last one and
-// are not stored.  h is split into its two parts once and kept in LDS as
+// are not stored.  h is split into its parts once and kept in LDS as
 // fragments (NS steps of 32 ranks).  A wave's pass: the weights' fragments (each
 // used for all rows), the matrix instructions, and the sums through a strip of
 // LDS into row order, so that base is read and out written in whole 128-byte
@@ -550,13 +552,13 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // inside the passes.  64 rows over 32 adapters of rank 16, 4096 columns: 5.8 us,
 // four dependent loads long.
 //
-// SMALL: ranks up to 16, both parts of h in one instruction.  EDGE: columns that
+// SMALL: ranks up to 16, two parts of h in one instruction.  EDGE: columns that
 // are no whole passes (the last one goes by single elements) or ranks that are
 // no whole pieces of 8.  expand_places: workgroups a compute unit, by registers, and
-// above rank 128 with 64-row tiles by shared memory (83 KB a workgroup).
+// above rank 128 with 64-row tiles by shared memory (116 KB a workgroup).
 // Registers spilled to scratch, of 256: 30 to 46 in the 64-row dX at ranks 65 to
 // 128 (37.6 us at rank 128, 4096 rows of 4096 columns, where the forward takes
-// 26.6); 15 at most in ten forms of other ranks and tiles.
+// 26.6); 15 at most in sixteen forms of other ranks and tiles.
 constexpr int expand_places(bool TR, int NS, int RT)
 {
     return RT == 1 ? (NS <= 2 ? 4 : NS == 8 && TR ? 2 : 3)
@@ -618,7 +620,9 @@ expand_kernel(LoraParams a, int groups, int group_cols)
     constexpr int kRows = RT * 16;
     constexpr int kPad = kCols + 4;
     constexpr bool STEPWISE = NS > 2;
-    __shared__ u32x4_t s_h[NS][RT][SMALL ? 1 : 2][kWave];
+    constexpr int kParts = DT == kBf16 ? 3 : 2;
+    constexpr int kFragments = SMALL ? (kParts + 1) / 2 : kParts;  // of h, a step and block
+    __shared__ u32x4_t s_h[NS][RT][kFragments][kWave];
     __shared__ __attribute__((aligned(16))) float s_out[4][16][kPad];
     __shared__ int s_src[kRows];
     __shared__ float s_factor[kRows];
@@ -764,13 +768,15 @@ expand_kernel(LoraParams a, int groups, int group_cols)
         }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-            u32x4_t part[2];
+            u32x4_t part[kParts];
             split8<DT>(v[s], part);
-            if constexpr (SMALL) {
-                s_h[s][wave][0][lane] = g < 2 ? part[0] : part[1];
-            } else {
-                s_h[s][wave][0][lane] = part[0];
-                s_h[s][wave][SMALL ? 0 : 1][lane] = part[1];
+#pragma unroll
+            for (int i = 0; i < kFragments; ++i) {
+                u32x4_t f = part[SMALL ? 2 * i : i];
+                if constexpr (SMALL)
+                    if (g >= 2)
+                        f = 2 * i + 1 < kParts ? part[min(2 * i + 1, kParts - 1)] : u32x4_t{};
+                s_h[s][wave][i][lane] = f;
             }
         }
         if (g == 0)
@@ -808,7 +814,7 @@ expand_kernel(LoraParams a, int groups, int group_cols)
         };
         auto multiply = [&](f32x4_t (&acc)[F], const u32x4_t (&wf)[F], int s, int t) {
 #pragma unroll
-            for (int part = 0; part < (SMALL ? 1 : 2); ++part) {
+            for (int part = 0; part < kFragments; ++part) {
                 const u32x4_t h = s_h[s][t][part][lane];
 #pragma unroll
                 for (int f = 0; f < F; ++f)
