@@ -547,7 +547,7 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // are issued after this one's matrix instructions and its base as this one's is
 // used, in the order in which they are waited for.
 //
-// 4096 rows, 8 adapters of rank up to 64, 28672 columns: 121 us, 3.9 TB/s of
+// 4096 rows, 8 adapters of rank up to 64, 28672 columns: 120 us, 3.9 TB/s of
 // base and out, of which 9 us pass before the first pass; HBM is the bound
 // inside the passes.  64 rows over 32 adapters of rank 16, 4096 columns: 5.8 us,
 // four dependent loads long.
@@ -557,8 +557,8 @@ __global__ __launch_bounds__(kShrinkWaves *kWave, RF <= 8 ? 4 : 2) void shrink_k
 // no whole pieces of 8.  expand_places: workgroups a compute unit, by registers, and
 // above rank 128 with 64-row tiles by shared memory (116 KB a workgroup).
 // Registers spilled to scratch, of 256: 30 to 46 in the 64-row dX at ranks 65 to
-// 128 (37.6 us at rank 128, 4096 rows of 4096 columns, where the forward takes
-// 26.6); 15 at most in sixteen forms of other ranks and tiles.
+// 128 (35.3 us at rank 128, 4096 rows of 4096 columns, where the forward takes
+// 29.7); 15 at most in sixteen forms of other ranks and tiles.
 constexpr int expand_places(bool TR, int NS, int RT)
 {
     return RT == 1 ? (NS <= 2 ? 4 : NS == 8 && TR ? 2 : 3)
@@ -960,7 +960,7 @@ expand_kernel(LoraParams a, int groups, int group_cols)
 // set to zero.  dh comes summed over shrink's splits.  4096 rows, 4 adapters of
 // rank 32, K = N = 4096: 19.6 us for 67 MB of x and dy (3.4 TB/s), two waves a
 // SIMD by registers and 1613 vector instructions a wave; every further 32 ranks
-// read x and dy again: 29.9 us at rank 64, 61 us at 128.  Lanes past the last column load the row's last 8 elements and
+// read x and dy again: 29.7 us at rank 64, 61 us at 128.  Lanes past the last column load the row's last 8 elements and
 // store only what is their own.
 template <int DT, int RG>
 __global__ __launch_bounds__(256) void grad_kernel(GradParams a)
