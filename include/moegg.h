@@ -64,6 +64,8 @@ typedef enum {
 #define MOEGG_FUSE_MUL_POST 4u /* multiply each output row by its gate weight     */
 #define MOEGG_DW_FP32_OUT 8u   /* dW only: write fp32 instead of bf16             */
 #define MOEGG_GATED_SILU 32u   /* forward only: gated SiLU on (gate, linear) pairs */
+#define MOEGG_GATED_GELU 64u   /* i8 and gated entry points: gated GELU (tanh form)  */
+#define MOEGG_GATED_HALVES 128u /* the same: gate rows, then linear rows, no pairs  */
 
 /* Device error bits ORed into *error_flags. */
 #define MOEGG_DERR_EXPERT_ID 1 /* a top-k expert id outside [0, E): slot dropped  */
@@ -77,6 +79,7 @@ typedef enum {
 #define MOEGG_MAX_TOPK 64       /* moegg_gate: picks a token                       */
 #define MOEGG_MAX_GATE_GROUPS 64
 #define MOEGG_MAX_LORA_RANK 256
+#define MOEGG_MAX_I8_K 131056   /* moegg_grouped_gemm_i8: 128 * 128 * K stays in int32 */
 
 /* Element types of the entry points that take a dtype. */
 #define MOEGG_BF16 0
@@ -649,6 +652,172 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
 /* Workspace of moegg_lora_bwd; 0 for sizes it refuses. */
 size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, int32_t R,
                                       int32_t K, int32_t N);
+
+/*
+ * moegg_quant_rows -- rows in 8-bit integers with a scale for each row: what
+ * moegg_grouped_gemm_i8 takes for its tokens and, laid out once, its weights
+ * ([E * N] rows of K).
+ *
+ *   scales[i] = m / 127, m = max_k |X[i, k]|            (fp32)
+ *   Q[i, k]   = round(127 X[i, k] / m)                  (real quotient, ties to even)
+ *
+ * so |Q| <= 127, and scales[i] * Q[i, k] is X[i, k] to half a scale.  A row of
+ * zeros gets scale 0 and codes 0; a row that holds an infinity or NaN scale
+ * NaN and codes 0.
+ *   X       [rows, K] of `dtype`, rows ldx >= K elements apart.
+ *   Q       out [rows, Kq], Kq = K rounded up to a multiple of 16, 16-byte
+ *           aligned; columns from K on are zeros.
+ *   scales  out [rows] fp32.
+ * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  Errors:
+ * ESHAPE for rows < 0 or past 2^24 - 1, K < 1, ldx < K, sizes past 2^40
+ * bytes; EINVAL for an unknown dtype, NULL or misaligned pointers.
+ */
+moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t K,
+                              int8_t *Q, float *scales, void *stream);
+
+/*
+ * moegg_grouped_gemm_i8 -- moegg_grouped_gemm_fwd on 8-bit integers: for
+ * sorted position p of expert e and row i = src(p) of Xq,
+ *   y[n] = x_scales[i] * w_scales[e, n] * sum_k Xq[i, k] * Wq[e, n, k]
+ * The sum is exact (int32), the scales are applied in fp32.  src, the
+ * permute flags and FUSE_MUL_POST as in the forward, Y bf16 rounded once.
+ *   MOEGG_GATED_SILU or MOEGG_GATED_GELU: Y [S, N/2] = act(gate) * linear with
+ *   act(g) = g / (1 + e^-g), or g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
+ *   W rows in (gate, linear) pairs, or with MOEGG_GATED_HALVES the N/2 gate
+ *   rows first.  Not with PERMUTE_Y or FUSE_MUL_POST.
+ *
+ *   Xq        [T or S, K] int8, x_scales [T or S] fp32; Wq [E, N, K] int8,
+ *             w_scales [E, N] fp32: as moegg_quant_rows writes them.  K is
+ *             the padded row length Kq, a multiple of 16.  Any int8 value.
+ *   others    as in the forward; 2 GiB at most for Xq and for one expert's Wq.
+ * Rows at positions past the sum of m_sizes are left as they were.  T = 0 is a
+ * no-op.  Errors: as the forward, and ESHAPE for K not a multiple of 16 or past
+ * MOEGG_MAX_I8_K, Xq or Wq not 16-byte aligned; EINVAL for both activations, or
+ * HALVES without one.
+ */
+moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, const int8_t *Wq,
+                                   const float *w_scales, const int32_t *m_sizes,
+                                   const int32_t *gather_idx, const float *topk_weights,
+                                   int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                   int32_t N, int32_t K, uint32_t flags, void *Y,
+                                   int32_t *error_flags, void *stream);
+
+/*
+ * moegg_pack8 -- an activation kept in 8 bits until the backward pass: 8.25
+ * bits a value.  Blocks of 32 neighbours of a row share a power of two,
+ *   step = 2^(b - 127), the smallest with round(max |x| / step) <= 127, b >= 1
+ *   code = round(x / step)                               (ties to even)
+ * code * step is exact in bf16 (and fp32), so that reading it back loses
+ * nothing more.  A block that holds an infinity or NaN gets b = 255 and reads
+ * back as NaN.
+ *   X       [rows, cols] of `dtype`, rows ldx >= cols elements apart.
+ *   Q       out [rows, Cp] int8, Cp = cols rounded up to a multiple of 32,
+ *           16-byte aligned; codes from cols on are 0.
+ *   scales  out [rows, Cp / 32], the bytes b.
+ * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  Errors:
+ * ESHAPE for rows < 0, cols < 1, ldx < cols, sizes past 2^40 bytes; EINVAL for
+ * an unknown dtype, NULL or misaligned pointers.
+ */
+moegg_status moegg_pack8(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t cols,
+                         int8_t *Q, uint8_t *scales, void *stream);
+
+/*
+ * moegg_unpack8 -- X[i, c] = Q[i, c] * 2^(scales[i, c / 32] - 127), rounded to
+ * `dtype` (fp16: held at +-65504).  Arguments and errors as moegg_pack8.
+ */
+moegg_status moegg_unpack8(const int8_t *Q, const uint8_t *scales, int64_t rows, int32_t cols,
+                           void *X, int32_t dtype, int64_t ldx, void *stream);
+
+/*
+ * moegg_gated_fwd -- the gated feed-forward block's first half in one kernel,
+ * for training: both projections, the activation and the product, and what
+ * the backward needs of them.  For sorted position p of expert e
+ *   A[p, :] = X[src(p), :] W_e^T       W [E, 2 I, K]: gate and linear rows
+ *   H[p, c] = act(g) * u               g, u: columns c of A's gate and linear part
+ * from the fp32 sums, rounded once.  Flags: PERMUTE_X as in the forward;
+ * GATED_SILU or GATED_GELU (one of them), with GATED_HALVES W's and A's gate
+ * part first instead of pairs.
+ *
+ *   X      bf16 [T, K] (PERMUTE_X) or [S, K].
+ *   H      out bf16 [S, I].
+ *   A      out bf16 [S, 2 I], in W's order of rows, or NULL.
+ *   Aq, As out: g and u packed as by moegg_pack8 from their fp32 sums, or both
+ *          NULL: Aq [S, 2 Ip] int8, the gate codes and then the linear ones,
+ *          Ip = I rounded up to a multiple of 32; As [S, 2 Ip / 32].  Aq 16-byte
+ *          aligned.  Not together with A.
+ *   workspace  device, 16-byte aligned, moegg_gated_fwd_workspace_bytes(...)
+ *          bytes: X and the used experts' W in rows of whole 16-byte chunks,
+ *          needed when K is not a multiple of 8 or X or W is not 16-byte
+ *          aligned; else may be NULL.  No initialisation.
+ * Rows at positions past the sum of m_sizes are left as they were.  T = 0 is a
+ * no-op.  Errors: EINVAL for flags other than these, none or both activations,
+ * Aq without As (or As without Aq, or A beside them), NULL or misaligned
+ * pointers; ESHAPE for sizes as in the forward, I < 1; EWORKSPACE.
+ */
+moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_sizes,
+                             const int32_t *gather_idx, int32_t num_tokens, int32_t topk,
+                             int32_t num_experts, int32_t I, int32_t K, uint32_t flags, void *H,
+                             void *A, int8_t *Aq, uint8_t *As, void *workspace,
+                             size_t workspace_bytes, int32_t *error_flags, void *stream);
+
+/* Workspace of moegg_gated_fwd for rows that are not whole 16-byte chunks (K not
+ * a multiple of 8, or operands not 16-byte aligned); 0 for sizes it refuses. */
+size_t moegg_gated_fwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                       int32_t I, int32_t K, uint32_t flags);
+
+/*
+ * moegg_gated_bwd -- from the down projection's output gradient to the gradient
+ * of moegg_gated_fwd's A, in one kernel: for sorted position p of expert e
+ *   dH[p, c] = sum_n dY[q(p), n] * W[e, n, c]            (fp32, not rounded)
+ *   dg = dH * u * act'(g),  du = dH * act(g)             rounded once to dA
+ *   H[p, c] = act(g) * u                                 when H is not NULL
+ * with g and u as the forward kept them (A, or Aq and As).  H, from the kept
+ * values, is the X of the down projection's dW; dA is the dY of the first
+ * projections' dX and dW (moegg_grouped_gemm_dX / _dW with N = 2 I).
+ *
+ *   dY    bf16 [S, N]; q(p) = gather_idx[p] with PERMUTE_Y (the flag of the
+ *         down projection's forward), else p.
+ *   W     bf16 [E, N, I], the down projection's weight.
+ *   dA    out bf16 [S, 2 I] in A's order; may be A itself.
+ *   flags PERMUTE_Y, GATED_SILU or GATED_GELU, GATED_HALVES.
+ *   workspace  as moegg_gated_fwd's, moegg_gated_bwd_workspace_bytes(...)
+ *         bytes: needed when N or I is not a multiple of 8 or dY or W is not
+ *         16-byte aligned.
+ * Rows of dA and H at positions past the sum of m_sizes, and rows whose gather
+ * entry is bad, are left as they were.  T = 0 is a no-op.  Errors as
+ * moegg_gated_fwd; exactly one of A and (Aq, As) is given (EINVAL).
+ */
+moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_sizes,
+                             const int32_t *gather_idx, const void *A, const int8_t *Aq,
+                             const uint8_t *As, int32_t num_tokens, int32_t topk,
+                             int32_t num_experts, int32_t N, int32_t I, uint32_t flags, void *dA,
+                             void *H, void *workspace, size_t workspace_bytes,
+                             int32_t *error_flags, void *stream);
+
+/* Workspace of moegg_gated_bwd for rows that are not whole 16-byte chunks; 0 for
+ * sizes it refuses. */
+size_t moegg_gated_bwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                       int32_t N, int32_t I);
+
+/*
+ * moegg_grouped_gemm_dW_packed -- moegg_grouped_gemm_dW with X as moegg_pack8
+ * keeps it: Xq [T or S, Cp] int8 and x_scales [T or S, Cp / 32], Cp = K rounded up to
+ * a multiple of 32.  The rows are expanded to bf16 (without loss) in the
+ * workspace, in expert order, and reduced there; everything else, the split
+ * of hot experts among it, as moegg_grouped_gemm_dW.
+ *   workspace  device, 16-byte aligned, required:
+ *              moegg_grouped_gemm_dW_packed_workspace_bytes(...) bytes.
+ */
+moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_scales,
+                                          const void *dY, const int32_t *m_sizes,
+                                          const int32_t *gather_idx, int32_t num_tokens,
+                                          int32_t topk, int32_t num_experts, int32_t N, int32_t K,
+                                          uint32_t flags, void *dW, void *workspace,
+                                          size_t workspace_bytes, int32_t *error_flags,
+                                          void *stream);
+
+size_t moegg_grouped_gemm_dW_packed_workspace_bytes(int32_t num_tokens, int32_t topk,
+                                                    int32_t num_experts, int32_t N, int32_t K);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,8 @@ PERMUTE_Y = 2
 FUSE_MUL_POST = 4
 DW_FP32_OUT = 8
 GATED_SILU = 32
+GATED_GELU = 64
+GATED_HALVES = 128
 
 DERR_EXPERT_ID = 1
 DERR_M_SIZES = 2
@@ -131,6 +133,30 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moegg_lora_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i64, i32,
                                    i32, i32, i32, vp, i64, vp, i64, vp, vp, u32, vp, sz, vp, vp]
     lib.moegg_lora_bwd.restype = ctypes.c_int
+    lib.moegg_quant_rows.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+    lib.moegg_quant_rows.restype = ctypes.c_int
+    lib.moegg_grouped_gemm_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32,
+                                          vp, vp, vp]
+    lib.moegg_grouped_gemm_i8.restype = ctypes.c_int
+    lib.moegg_pack8.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+    lib.moegg_pack8.restype = ctypes.c_int
+    lib.moegg_unpack8.argtypes = [vp, vp, i64, i32, vp, i32, i64, vp]
+    lib.moegg_unpack8.restype = ctypes.c_int
+    lib.moegg_gated_fwd.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, u32, vp, vp, vp, vp,
+                                    vp, sz, vp, vp]
+    lib.moegg_gated_fwd.restype = ctypes.c_int
+    lib.moegg_gated_fwd_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, u32]
+    lib.moegg_gated_fwd_workspace_bytes.restype = sz
+    lib.moegg_gated_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32, vp,
+                                    vp, vp, sz, vp, vp]
+    lib.moegg_gated_bwd.restype = ctypes.c_int
+    lib.moegg_gated_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.moegg_gated_bwd_workspace_bytes.restype = sz
+    lib.moegg_grouped_gemm_dW_packed.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32,
+                                                 vp, vp, sz, vp, vp]
+    lib.moegg_grouped_gemm_dW_packed.restype = ctypes.c_int
+    lib.moegg_grouped_gemm_dW_packed_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.moegg_grouped_gemm_dW_packed_workspace_bytes.restype = sz
     _lib = lib
     return lib
 
@@ -826,5 +852,278 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
             (LORA_FP32_GRAD if fp32_grads else 0) | (LORA_ALL_ROWS if dX is None else 0),
             ws_ptr, ws.numel(), _flag_arg(error_flags, index), stream_ptr), "moegg_lora_bwd")
         return dx, da, db
+
+    return _run(dev, stream, call)
+
+
+PACK_BLOCK = 32
+
+
+def quant_rows(X, *, Q=None, scales=None, stream=None):
+    """Rows in 8-bit integers with a scale each (moegg_quant_rows).
+
+    X: [..., K] bf16, fp16 or fp32; a matrix may have any row stride, more
+    dimensions (weights [E, N, K]) are contiguous.  Returns (Q int8 [..., Kq],
+    scales fp32 [...]) with Kq = K rounded up to a multiple of 16, the columns
+    from K on zero: what grouped_gemm_i8 takes for tokens and for weights.
+    """
+    lib = load_library()
+    dev = X.device
+    index = dev.index
+    lead, K = X.shape[:-1], X.shape[-1]
+    rows = lead.numel()
+    code = _dtype_code(X, "X")
+    if X.dim() == 2:
+        x_ptr, ldx = _rows_arg(X, "X", X.dtype, (rows, K), index)
+    else:
+        x_ptr, ldx = _arg(X, "X", X.dtype, X.shape, index), K
+
+    def call(stream_ptr):
+        q, q_ptr = _out(Q, "Q", torch.int8, lead + ((K + 15) // 16 * 16,), dev)
+        s, s_ptr = _out(scales, "scales", torch.float32, lead, dev)
+        _check(lib.moegg_quant_rows(x_ptr, code, ldx, rows, K, q_ptr, s_ptr, stream_ptr),
+               "moegg_quant_rows")
+        return q, s
+
+    return _run(dev, stream, call)
+
+
+def grouped_gemm_i8(Xq, x_scales, Wq, w_scales, m_sizes, gather_idx, topk_weights, topk: int,
+                    flags: int, *, Y=None, error_flags=None, stream=None):
+    """grouped_gemm_fwd on 8-bit integers with a scale for each token and output channel
+    (moegg_grouped_gemm_i8).
+
+    Xq int8 [T, Kq] (PERMUTE_X) or [T*topk, Kq] and x_scales fp32, Wq int8 [E, N, Kq]
+    and w_scales fp32 [E, N], as quant_rows gives them; the others as in
+    grouped_gemm_fwd.  flags: also GATED_SILU or GATED_GELU, with GATED_HALVES
+    for W's gate rows first instead of (gate, linear) pairs.  Returns Y bf16
+    [T*topk, N], [T*topk, N/2] when gated.
+    """
+    lib = load_library()
+    dev = Xq.device
+    index = dev.index
+    E, N, K = Wq.shape
+    S = gather_idx.numel() if gather_idx is not None else Xq.shape[0]
+    T = S // topk
+    x_rows = T if flags & PERMUTE_X else T * topk
+    cols = N // 2 if flags & (GATED_SILU | GATED_GELU) else N
+
+    def call(stream_ptr):
+        y, y_ptr = _out(Y, "Y", torch.bfloat16, (T * topk, cols), dev)
+        _check(lib.moegg_grouped_gemm_i8(
+            _arg(Xq, "Xq", torch.int8, (x_rows, K), index),
+            _slots_arg(x_scales, "x_scales", torch.float32, x_rows, index),
+            _arg(Wq, "Wq", torch.int8, (E, N, K), index),
+            _arg(w_scales, "w_scales", torch.float32, (E, N), index),
+            _arg(m_sizes, "m_sizes", torch.int32, (E,), index),
+            _slots_arg(gather_idx, "gather_idx", torch.int32, T * topk, index),
+            _slots_arg(topk_weights, "topk_weights", torch.float32, T * topk, index), T, topk, E, N,
+            K, int(flags), y_ptr, _flag_arg(error_flags, index), stream_ptr),
+            "moegg_grouped_gemm_i8")
+        return y
+
+    return _run(dev, stream, call)
+
+
+def _packed_shapes(rows, cols):
+    padded = (cols + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+    return (rows, padded), (rows, padded // PACK_BLOCK)
+
+
+def pack8(X, *, Q=None, scales=None, stream=None):
+    """An activation in 8.25 bits a value (moegg_pack8): blocks of 32 neighbours
+    of a row share a power of two.
+
+    X: [rows, cols] bf16, fp16 or fp32, any row stride.  Returns (Q int8 [rows,
+    Cp], scales uint8 [rows, Cp / 32]), Cp = cols rounded up to a multiple of 32.
+    """
+    lib = load_library()
+    dev = X.device
+    index = dev.index
+    rows, cols = X.shape
+    code = _dtype_code(X, "X")
+    x_ptr, ldx = _rows_arg(X, "X", X.dtype, (rows, cols), index)
+    q_shape, s_shape = _packed_shapes(rows, cols)
+
+    def call(stream_ptr):
+        q, q_ptr = _out(Q, "Q", torch.int8, q_shape, dev)
+        s, s_ptr = _out(scales, "scales", torch.uint8, s_shape, dev)
+        _check(lib.moegg_pack8(x_ptr, code, ldx, rows, cols, q_ptr, s_ptr, stream_ptr),
+               "moegg_pack8")
+        return q, s
+
+    return _run(dev, stream, call)
+
+
+def unpack8(Q, scales, cols: int, dtype=torch.bfloat16, *, X=None, stream=None):
+    """The values of pack8's (Q, scales) (moegg_unpack8): [rows, cols] of `dtype`,
+    exact in bf16 and fp32.  A given X may have any row stride."""
+    lib = load_library()
+    dev = Q.device
+    index = dev.index
+    rows, cols = Q.shape[0], int(cols)
+    dtype = dtype if X is None else X.dtype
+    q_shape, s_shape = _packed_shapes(rows, cols)
+
+    def call(stream_ptr):
+        x = torch.empty(rows, cols, dtype=dtype, device=dev) if X is None else X
+        x_ptr, ldx = _rows_arg(x, "X", dtype, (rows, cols), index)
+        _check(lib.moegg_unpack8(
+            _arg(Q, "Q", torch.int8, q_shape, index),
+            _arg(scales, "scales", torch.uint8, s_shape, index), rows, cols, x_ptr,
+            _dtype_code(x, "X"), ldx, stream_ptr), "moegg_unpack8")
+        return x
+
+    return _run(dev, stream, call)
+
+
+def _chunked(cols, *tensors):
+    """Whether rows of `cols` elements of 16 bits are whole, aligned 16-byte chunks."""
+    return cols % 8 == 0 and all(t.data_ptr() % 16 == 0 for t in tensors)
+
+
+def _optional_workspace(workspace, need, device):
+    """(workspace, address, bytes): allocated when needed and not given."""
+    if workspace is None and need == 0:
+        return None, None, 0
+    workspace, ptr = _workspace_arg(workspace, need, device)
+    return workspace, ptr, workspace.numel()
+
+
+def gated_fwd(X, W, m_sizes, gather_idx, topk: int, flags: int, *, keep=None, H=None, kept=None,
+              workspace=None, error_flags=None, stream=None):
+    """The gated block's first half with what its backward needs (moegg_gated_fwd):
+    H = act(g) * u of the grouped product X W_e^T, gate columns g and linear u.
+
+    X: bf16 [T, K] (PERMUTE_X) or [T*topk, K]; W: bf16 [E, 2 I, K], its rows in
+    (gate, linear) pairs or with GATED_HALVES the I gate rows first; flags:
+    PERMUTE_X, GATED_SILU or GATED_GELU, GATED_HALVES.  keep: None, "bf16" (A =
+    X W_e^T, [T*topk, 2 I]) or "packed" (g and u in 8.25 bits a value: codes int8
+    [T*topk, 2 Ip] and scales uint8 [T*topk, 2 Ip / 32], the gate's and then the
+    linear part's, Ip = I rounded up to a multiple of 32).  Returns (H bf16
+    [T*topk, I], kept): the A, the pair, or None; `kept` may give its buffers.
+    """
+    lib = load_library()
+    dev = X.device
+    index = dev.index
+    E, N, K = W.shape
+    S = gather_idx.numel() if gather_idx is not None else X.shape[0]
+    T = S // topk
+    S, I = T * topk, N // 2
+    if N % 2:
+        raise ValueError(f"W must have an even number of rows per expert, not {N}")
+    if keep not in (None, "bf16", "packed"):
+        raise ValueError(f"keep must be None, 'bf16' or 'packed', not {keep!r}")
+    padded = (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+
+    def call(stream_ptr):
+        h, h_ptr = _out(H, "H", torch.bfloat16, (S, I), dev)
+        out = a_ptr = q_ptr = s_ptr = None
+        if keep == "bf16":
+            out, a_ptr = _out(kept, "kept", torch.bfloat16, (S, N), dev)
+        elif keep == "packed":
+            q, s = (None, None) if kept is None else kept
+            q, q_ptr = _out(q, "kept[0]", torch.int8, (S, 2 * padded), dev)
+            s, s_ptr = _out(s, "kept[1]", torch.uint8, (S, 2 * padded // PACK_BLOCK), dev)
+            out = (q, s)
+        need = 0 if _chunked(K, X, W) else lib.moegg_gated_fwd_workspace_bytes(T, topk, E, I, K,
+                                                                               int(flags))
+        ws, ws_ptr, ws_bytes = _optional_workspace(workspace, need, dev)
+        _check(lib.moegg_gated_fwd(
+            _arg(X, "X", torch.bfloat16, (T if flags & PERMUTE_X else S, K), index),
+            _arg(W, "W", torch.bfloat16, (E, N, K), index),
+            _arg(m_sizes, "m_sizes", torch.int32, (E,), index),
+            _slots_arg(gather_idx, "gather_idx", torch.int32, S, index), T, topk, E, I, K,
+            int(flags), h_ptr, a_ptr, q_ptr, s_ptr, ws_ptr, ws_bytes,
+            _flag_arg(error_flags, index), stream_ptr), "moegg_gated_fwd")
+        return h, out
+
+    return _run(dev, stream, call)
+
+
+def gated_bwd(dY, W, kept, m_sizes, gather_idx, topk: int, flags: int, *, want_h: bool = True,
+              dA=None, H=None, workspace=None, error_flags=None, stream=None):
+    """From the down projection's output gradient to that of gated_fwd's A (moegg_gated_bwd).
+
+    dY: bf16 [T*topk, N] (slot order with PERMUTE_Y, the flag of the down
+    projection's forward); W: bf16 [E, N, I], the down projection's weight;
+    kept: what gated_fwd returned, A or the packed pair; the other flags as
+    there.  Returns (dA bf16 [T*topk, 2 I], the dY of the first projections'
+    grouped_gemm_dX and grouped_gemm_dW; H bf16 [T*topk, I] from the kept values,
+    the X of the down projection's grouped_gemm_dW, or None).  dA may be A.
+    """
+    lib = load_library()
+    dev = dY.device
+    index = dev.index
+    E, N, I = W.shape
+    T = dY.shape[0] // topk
+    S = T * topk
+    padded = (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+
+    def call(stream_ptr):
+        a_ptr = q_ptr = s_ptr = None
+        if isinstance(kept, torch.Tensor):
+            a_ptr = _arg(kept, "kept", torch.bfloat16, (S, 2 * I), index)
+        else:
+            q_ptr = _arg(kept[0], "kept[0]", torch.int8, (S, 2 * padded), index)
+            s_ptr = _arg(kept[1], "kept[1]", torch.uint8, (S, 2 * padded // PACK_BLOCK), index)
+        da, da_ptr = _out(dA, "dA", torch.bfloat16, (S, 2 * I), dev)
+        h = h_ptr = None
+        if want_h or H is not None:
+            h, h_ptr = _out(H, "H", torch.bfloat16, (S, I), dev)
+        need = 0
+        if not (_chunked(N, dY) and _chunked(I, W)):
+            need = lib.moegg_gated_bwd_workspace_bytes(T, topk, E, N, I)
+        ws, ws_ptr, ws_bytes = _optional_workspace(workspace, need, dev)
+        _check(lib.moegg_gated_bwd(
+            _arg(dY, "dY", torch.bfloat16, (S, N), index),
+            _arg(W, "W", torch.bfloat16, (E, N, I), index),
+            _arg(m_sizes, "m_sizes", torch.int32, (E,), index),
+            _slots_arg(gather_idx, "gather_idx", torch.int32, S, index), a_ptr, q_ptr, s_ptr, T,
+            topk, E, N, I, int(flags), da_ptr, h_ptr, ws_ptr, ws_bytes,
+            _flag_arg(error_flags, index), stream_ptr), "moegg_gated_bwd")
+        return da, h
+
+    return _run(dev, stream, call)
+
+
+def dw_packed_workspace_bytes(num_tokens: int, topk: int, num_experts: int, N: int,
+                              K: int) -> int:
+    """Workspace bytes of grouped_gemm_dW_packed."""
+    return int(load_library().moegg_grouped_gemm_dW_packed_workspace_bytes(
+        num_tokens, topk, num_experts, N, K))
+
+
+def grouped_gemm_dW_packed(Xq, x_scales, dY, m_sizes, gather_idx, topk: int, flags: int, *, K: int,
+                           dW=None, workspace=None, error_flags=None, stream=None):
+    """grouped_gemm_dW with X as pack8 keeps it (moegg_grouped_gemm_dW_packed).
+
+    Xq int8 [T or T*topk, Cp] and x_scales uint8: a packed X of K columns; the
+    others as in grouped_gemm_dW.  The rows are expanded in `workspace` (a uint8
+    CUDA tensor of dw_packed_workspace_bytes(...) bytes, allocated here when not
+    given).  Returns [E, N, K] bf16 (fp32 with DW_FP32_OUT).
+    """
+    lib = load_library()
+    dev = dY.device
+    index = dev.index
+    N, E, K = dY.shape[1], m_sizes.numel(), int(K)
+    T = dY.shape[0] // topk
+    S = T * topk
+    q_shape, s_shape = _packed_shapes(T if flags & PERMUTE_X else S, K)
+
+    def call(stream_ptr):
+        w, w_ptr = _out(dW, "dW", torch.float32 if flags & DW_FP32_OUT else torch.bfloat16,
+                        (E, N, K), dev)
+        need = lib.moegg_grouped_gemm_dW_packed_workspace_bytes(T, topk, E, N, K)
+        ws, ws_ptr = _workspace_arg(workspace, need, dev)
+        _check(lib.moegg_grouped_gemm_dW_packed(
+            _arg(Xq, "Xq", torch.int8, q_shape, index),
+            _arg(x_scales, "x_scales", torch.uint8, s_shape, index),
+            _arg(dY, "dY", torch.bfloat16, (S, N), index),
+            _arg(m_sizes, "m_sizes", torch.int32, (E,), index),
+            _slots_arg(gather_idx, "gather_idx", torch.int32, S, index), T, topk, E, N, K,
+            int(flags), w_ptr, ws_ptr, ws.numel(), _flag_arg(error_flags, index), stream_ptr),
+            "moegg_grouped_gemm_dW_packed")
+        return w
 
     return _run(dev, stream, call)

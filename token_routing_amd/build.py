@@ -33,7 +33,7 @@ FLAGS = [
 ]
 
 SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "gate.hip", "sort.hip",
-           "lora.hip", "api.hip"]
+           "lora.hip", "block.hip", "pack.hip", "api.hip"]
 
 
 def _compile(src: str, report: bool, defines=(), build_dir=BUILD) -> str:

@@ -11,6 +11,7 @@
 #include "../../include/moegg.h"
 
 #include "gemm_params.h"
+#include "block_params.h"
 #include "layer_params.h"
 #include "lora_params.h"
 
@@ -105,6 +106,31 @@ moegg_status from_hip(hipError_t e)
     return e == hipSuccess ? MOEGG_OK : MOEGG_EHIP;
 }
 
+// Bytes [p, p + bytes) of an operand; none where p is NULL.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+bool meet(const Span &a, const Span &b)
+{
+    const int64_t pa = reinterpret_cast<intptr_t>(a.p), pb = reinterpret_cast<intptr_t>(b.p);
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && pa < pb + b.bytes && pb < pa + a.bytes;
+}
+// Whether an output meets an input or another output.
+template <int NO, int NI>
+bool outputs_meet(const Span (&outs)[NO], const Span (&ins)[NI])
+{
+    for (int i = 0; i < NO; ++i) {
+        for (int j = i + 1; j < NO; ++j)
+            if (meet(outs[i], outs[j]))
+                return true;
+        for (int j = 0; j < NI; ++j)
+            if (meet(outs[i], ins[j]))
+                return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -124,7 +150,7 @@ const char *moegg_status_string(moegg_status s)
 
 int32_t moegg_version(void)
 {
-    return 102;
+    return 103;
 }
 
 size_t moegg_route_workspace_bytes(int64_t num_slots, int32_t num_experts)
@@ -1070,6 +1096,467 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
     g.col_tiles_b = (N + 127) / 128;
     g.fp32_out = flags & MOEGG_LORA_FP32_GRAD;
     return from_hip(moegg::lora_grad_launch(g, dtype, hs));
+}
+
+// ---------------------------------------------------------------------------
+// The feed-forward block: 8-bit products, packed activations, the gated block
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxBytes = (int64_t)1 << 40;
+
+// Rows of K values of `dtype`, ld apart.
+static moegg_status check_values(const void *X, int32_t dtype, int64_t ld, int64_t rows, int32_t K)
+{
+    if (rows < 0 || rows > INT32_MAX || K < 1 || ld < K || ld > kMaxBytes / 4 / (rows + 1))
+        return MOEGG_ESHAPE;
+    if (!known_dtype(dtype))
+        return MOEGG_EINVAL;
+    if (rows > 0 && (!X || !aligned_elem(X, dtype)))
+        return MOEGG_EINVAL;
+    return MOEGG_OK;
+}
+static Span values_span(const void *X, int32_t dtype, int64_t ld, int64_t rows, int32_t K)
+{
+    return {X, rows > 0 ? ((rows - 1) * ld + K) * (dtype == MOEGG_FP32 ? 4 : 2) : 0};
+}
+
+moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t K,
+                              int8_t *Q, float *scales, void *stream)
+{
+    moegg_status st = check_values(X, dtype, ldx, rows, K);
+    if (st != MOEGG_OK)
+        return st;
+    if (rows >= kMaxThreads / 256)
+        return MOEGG_ESHAPE;
+    if (rows == 0)
+        return MOEGG_OK;
+    if (!Q || !scales || !aligned16(Q) || !aligned4(scales))
+        return MOEGG_EINVAL;
+    moegg::QuantParams p;
+    p.X = X;
+    p.ldx = ldx;
+    p.Q = reinterpret_cast<char *>(Q);
+    p.scales = scales;
+    p.rows = rows;
+    p.K = K;
+    p.Kq = (int)(((int64_t)K + 15) / 16 * 16);
+    if (p.Kq < K)
+        return MOEGG_ESHAPE;
+    const Span outs[] = {{Q, rows * p.Kq}, {scales, rows * 4}};
+    const Span ins[] = {values_span(X, dtype, ldx, rows, K)};
+    if (outputs_meet(outs, ins))
+        return MOEGG_EINVAL;
+    return from_hip(moegg::quant_rows_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+static moegg_status pack_params(const void *X, int32_t dtype, int64_t ldx, int64_t rows,
+                                int32_t cols, const int8_t *Q, const uint8_t *scales, bool pack,
+                                moegg::PackParams *p)
+{
+    moegg_status st = check_values(X, dtype, ldx, rows, cols);
+    if (st != MOEGG_OK || rows == 0)
+        return st;
+    if (!Q || !scales || !aligned16(Q))
+        return MOEGG_EINVAL;
+    const int64_t Cp = moegg::packed_cols(cols);
+    if (Cp > INT32_MAX)
+        return MOEGG_ESHAPE;
+    const Span x = values_span(X, dtype, ldx, rows, cols);
+    const Span q = {Q, rows * Cp}, s = {scales, rows * (Cp / moegg::kPackBlock)};
+    if (meet(x, q) || meet(x, s) || (pack && meet(q, s)))
+        return MOEGG_EINVAL;
+    p->X = X;
+    p->out = const_cast<void *>(X);
+    p->ldx = ldx;
+    p->Q = const_cast<char *>(reinterpret_cast<const char *>(Q));
+    p->S = const_cast<uint8_t *>(scales);
+    p->rows = rows;
+    p->cols = cols;
+    return MOEGG_OK;
+}
+
+moegg_status moegg_pack8(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t cols,
+                         int8_t *Q, uint8_t *scales, void *stream)
+{
+    moegg::PackParams p;
+    moegg_status st = pack_params(X, dtype, ldx, rows, cols, Q, scales, true, &p);
+    if (st != MOEGG_OK || rows == 0)
+        return st;
+    return from_hip(moegg::pack8_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+moegg_status moegg_unpack8(const int8_t *Q, const uint8_t *scales, int64_t rows, int32_t cols,
+                           void *X, int32_t dtype, int64_t ldx, void *stream)
+{
+    moegg::PackParams p;
+    moegg_status st = pack_params(X, dtype, ldx, rows, cols, Q, scales, false, &p);
+    if (st != MOEGG_OK || rows == 0)
+        return st;
+    return from_hip(moegg::unpack8_launch(p, dtype, static_cast<hipStream_t>(stream)));
+}
+
+// At most one activation, and halves only with one.
+static moegg_status check_activation(uint32_t flags, bool required)
+{
+    const uint32_t act = flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU);
+    if (act == (MOEGG_GATED_SILU | MOEGG_GATED_GELU) ||
+        (act == 0 && (required || (flags & MOEGG_GATED_HALVES))))
+        return MOEGG_EINVAL;
+    return MOEGG_OK;
+}
+
+moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, const int8_t *Wq,
+                                   const float *w_scales, const int32_t *m_sizes,
+                                   const int32_t *gather_idx, const float *topk_weights,
+                                   int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                   int32_t N, int32_t K, uint32_t flags, void *Y,
+                                   int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_gemm_common(num_tokens, topk, num_experts, N, K);
+    if (st != MOEGG_OK)
+        return st;
+    if (flags & ~(MOEGG_PERMUTE_X | MOEGG_PERMUTE_Y | MOEGG_FUSE_MUL_POST | MOEGG_GATED_SILU |
+                  MOEGG_GATED_GELU | MOEGG_GATED_HALVES))
+        return MOEGG_EINVAL;
+    const int64_t S = (int64_t)num_tokens * topk;
+    const bool gated = flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU);
+    if ((st = check_activation(flags, false)) != MOEGG_OK ||
+        (st = check_permute_flags(flags, gather_idx, S)) != MOEGG_OK)
+        return st;
+    if ((flags & MOEGG_FUSE_MUL_POST) && !(flags & MOEGG_PERMUTE_Y))
+        return MOEGG_EINVAL;
+    if (gated && (flags & (MOEGG_PERMUTE_Y | MOEGG_FUSE_MUL_POST)))
+        return MOEGG_EINVAL;
+    if (gated && N % 2 != 0)
+        return MOEGG_ESHAPE;
+    if (K % 16 != 0 || K > MOEGG_MAX_I8_K)
+        return MOEGG_ESHAPE;
+    if ((flags & MOEGG_FUSE_MUL_POST) && num_tokens > 0 && !topk_weights)
+        return MOEGG_EINVAL;
+    if (num_tokens == 0)
+        return MOEGG_OK;
+    if (!Xq || !x_scales || !Wq || !w_scales || !m_sizes || !Y || !aligned4(x_scales) ||
+        !aligned4(w_scales) || !aligned4(topk_weights))
+        return MOEGG_EINVAL;
+    if (!aligned16(Xq) || !aligned16(Wq) || !aligned2(Y))
+        return MOEGG_ESHAPE;
+    const int64_t x_rows = (flags & MOEGG_PERMUTE_X) ? num_tokens : S;
+    if (!fits(x_rows, K, 1) || !fits(N, K, 1))
+        return MOEGG_ESHAPE;
+    const Span outs[] = {{Y, S * (gated ? N / 2 : N) * 2}};
+    const Span ins[] = {{Xq, x_rows * K}, {x_scales, x_rows * 4},
+                        {Wq, (int64_t)num_experts * N * K},
+                        {w_scales, (int64_t)num_experts * N * 4}};
+    if (outputs_meet(outs, ins))
+        return MOEGG_EINVAL;
+    int cus = 0;
+    if (device_cus(&cus) != 0)
+        return MOEGG_EHIP;
+    moegg::BlockFwdParams p = {};
+    p.X = reinterpret_cast<const char *>(Xq);
+    p.W = reinterpret_cast<const char *>(Wq);
+    p.x_scales = x_scales;
+    p.w_scales = w_scales;
+    p.m_sizes = m_sizes;
+    p.gather = gather_idx;
+    p.topk_w = topk_weights;
+    p.Y = static_cast<char *>(Y);
+    p.err = error_flags;
+    p.S = S;
+    p.ldx = p.ldw = K;
+    p.topk = topk;
+    p.E = num_experts;
+    p.N = N;
+    p.K = K / 2;
+    p.flags = flags;
+    return from_hip(moegg::i8_launch(p, cus, static_cast<hipStream_t>(stream)));
+}
+
+// What the gated entry points keep of the pre-activations: A, or Aq and As.
+static moegg_status check_kept(const void *A, const int8_t *Aq, const uint8_t *As, bool required)
+{
+    if (!Aq != !As || (A && Aq) || (required && !A && !Aq))
+        return MOEGG_EINVAL;
+    return aligned2(A) && aligned16(Aq) ? MOEGG_OK : MOEGG_EINVAL;
+}
+
+// Copies of `rows` rows and of `groups` weights of w_rows rows in whole 16-byte chunks:
+// the second one's offset, and the bytes of both.
+static int64_t padded_second(int64_t rows, int64_t cols)
+{
+    return (rows * moegg::padded_row_bytes(cols) + 255) / 256 * 256;
+}
+static int64_t padded_bytes(int64_t rows, int64_t cols, int64_t groups, int64_t w_rows,
+                            int64_t w_cols)
+{
+    return padded_second(rows, cols) + groups * w_rows * moegg::padded_row_bytes(w_cols);
+}
+
+size_t moegg_gated_fwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                       int32_t I, int32_t K, uint32_t flags)
+{
+    if (I > INT32_MAX / 2 ||
+        check_gemm_common(num_tokens, topk, num_experts, 2 * I, K) != MOEGG_OK)
+        return 0;
+    const int64_t rows = (int64_t)num_tokens * ((flags & MOEGG_PERMUTE_X) ? 1 : topk);
+    return (size_t)padded_bytes(rows, K, num_experts, 2 * (int64_t)I, K);
+}
+
+size_t moegg_gated_bwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts,
+                                       int32_t N, int32_t I)
+{
+    if (check_gemm_common(num_tokens, topk, num_experts, N, I) != MOEGG_OK)
+        return 0;
+    return (size_t)padded_bytes((int64_t)num_tokens * topk, N, num_experts, N, I);
+}
+
+// Copies a bf16 operand whose rows are not whole aligned 16-byte chunks.
+static hipError_t pad_operand(const char **src, int64_t *ld, char *dst, const int32_t *m_sizes,
+                              int64_t groups, int64_t rows, int cols, int cus, hipStream_t stream)
+{
+    moegg::PadParams p;
+    p.src = *src;
+    p.dst = dst;
+    p.m_sizes = m_sizes;
+    p.groups = groups;
+    p.rows = rows;
+    p.cols = cols;
+    *src = dst;
+    *ld = moegg::padded_row_bytes(cols);
+    return moegg::pad_rows_launch(p, cus, stream);
+}
+
+moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_sizes,
+                             const int32_t *gather_idx, int32_t num_tokens, int32_t topk,
+                             int32_t num_experts, int32_t I, int32_t K, uint32_t flags, void *H,
+                             void *A, int8_t *Aq, uint8_t *As, void *workspace,
+                             size_t workspace_bytes, int32_t *error_flags, void *stream)
+{
+    if (I < 1 || I > INT32_MAX / 2)
+        return MOEGG_ESHAPE;
+    const int32_t N = 2 * I;
+    moegg_status st = check_gemm_common(num_tokens, topk, num_experts, N, K);
+    if (st != MOEGG_OK)
+        return st;
+    const int64_t S = (int64_t)num_tokens * topk;
+    if (flags & ~(MOEGG_PERMUTE_X | MOEGG_GATED_SILU | MOEGG_GATED_GELU | MOEGG_GATED_HALVES))
+        return MOEGG_EINVAL;
+    if ((st = check_activation(flags, true)) != MOEGG_OK ||
+        (st = check_permute_flags(flags, gather_idx, S)) != MOEGG_OK ||
+        (st = check_kept(A, Aq, As, false)) != MOEGG_OK)
+        return st;
+    const int64_t x_rows = (flags & MOEGG_PERMUTE_X) ? num_tokens : S;
+    const int64_t pad = moegg::padded_row_bytes(K);
+    if (!fits(x_rows, pad, 1) || !fits(N, pad, 1))
+        return MOEGG_ESHAPE;
+    if (num_tokens == 0)
+        return MOEGG_OK;
+    if (!X || !W || !m_sizes || !H || !aligned2(X) || !aligned2(W) || !aligned2(H))
+        return MOEGG_EINVAL;
+    const bool pad_x = K % 8 != 0 || !aligned16(X), pad_w = K % 8 != 0 || !aligned16(W);
+    const int64_t need = padded_bytes(x_rows, K, num_experts, N, K);
+    if (pad_x || pad_w) {
+        if (!aligned16(workspace))
+            return MOEGG_EINVAL;
+        if (!workspace || (int64_t)workspace_bytes < need)
+            return MOEGG_EWORKSPACE;
+    }
+    const int64_t Ip = moegg::packed_cols(I);
+    const Span outs[] = {{H, S * I * 2}, {A, S * N * 2}, {Aq, S * 2 * Ip},
+                         {As, S * 2 * Ip / moegg::kPackBlock},
+                         {workspace, pad_x || pad_w ? need : 0}};
+    const Span ins[] = {{X, x_rows * K * 2}, {W, (int64_t)num_experts * N * K * 2}};
+    if (outputs_meet(outs, ins))
+        return MOEGG_EINVAL;
+    int cus = 0;
+    if (device_cus(&cus) != 0)
+        return MOEGG_EHIP;
+    moegg::BlockFwdParams p = {};
+    p.X = static_cast<const char *>(X);
+    p.W = static_cast<const char *>(W);
+    p.m_sizes = m_sizes;
+    p.gather = gather_idx;
+    p.Y = static_cast<char *>(H);
+    p.A = static_cast<char *>(A);
+    p.Aq = reinterpret_cast<char *>(Aq);
+    p.As = As;
+    p.err = error_flags;
+    p.S = S;
+    p.ldx = p.ldw = (int64_t)K * 2;
+    p.topk = topk;
+    p.E = num_experts;
+    p.N = N;
+    p.K = (K + 7) / 8 * 8;
+    p.flags = flags;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    hipError_t e = hipSuccess;
+    if (pad_x)
+        e = pad_operand(&p.X, &p.ldx, ws, nullptr, 1, x_rows, K, cus, hs);
+    if (e == hipSuccess && pad_w)
+        e = pad_operand(&p.W, &p.ldw, ws + padded_second(x_rows, K), m_sizes, num_experts, N, K,
+                        cus, hs);
+    if (e != hipSuccess)
+        return MOEGG_EHIP;
+    return from_hip(moegg::gated_fwd_launch(p, cus, hs));
+}
+
+moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_sizes,
+                             const int32_t *gather_idx, const void *A, const int8_t *Aq,
+                             const uint8_t *As, int32_t num_tokens, int32_t topk,
+                             int32_t num_experts, int32_t N, int32_t I, uint32_t flags, void *dA,
+                             void *H, void *workspace, size_t workspace_bytes,
+                             int32_t *error_flags, void *stream)
+{
+    moegg_status st = check_gemm_common(num_tokens, topk, num_experts, N, I);
+    if (st != MOEGG_OK)
+        return st;
+    const int64_t S = (int64_t)num_tokens * topk;
+    if (flags & ~(MOEGG_PERMUTE_Y | MOEGG_GATED_SILU | MOEGG_GATED_GELU | MOEGG_GATED_HALVES))
+        return MOEGG_EINVAL;
+    if ((st = check_activation(flags, true)) != MOEGG_OK ||
+        (st = check_permute_flags(flags, gather_idx, S)) != MOEGG_OK)
+        return st;
+    const int64_t ldy = moegg::padded_row_bytes(N), ldw = moegg::padded_row_bytes(I);
+    if (I > INT32_MAX / 2 || !fits(S, ldy, 1) || !fits(N, ldw, 1))
+        return MOEGG_ESHAPE;
+    if (num_tokens == 0)
+        return MOEGG_OK;
+    if ((st = check_kept(A, Aq, As, true)) != MOEGG_OK)
+        return st;
+    if (!dY || !W || !m_sizes || !dA || !aligned2(dY) || !aligned2(W) || !aligned2(dA) ||
+        !aligned2(H))
+        return MOEGG_EINVAL;
+    const bool pad_y = N % 8 != 0 || !aligned16(dY), pad_w = I % 8 != 0 || !aligned16(W);
+    const int64_t need = padded_bytes(S, N, num_experts, N, I);
+    if (pad_y || pad_w) {
+        if (!aligned16(workspace))
+            return MOEGG_EINVAL;
+        if (!workspace || (int64_t)workspace_bytes < need)
+            return MOEGG_EWORKSPACE;
+    }
+    const int64_t Ip = moegg::packed_cols(I);
+    const Span outs[] = {{dA, S * I * 4}, {H, S * I * 2},
+                         {workspace, pad_y || pad_w ? need : 0}};
+    const Span ins[] = {{dY, S * N * 2}, {W, (int64_t)num_experts * N * I * 2},
+                        {A == dA ? nullptr : A, S * I * 4}, {Aq, S * 2 * Ip},
+                        {As, S * 2 * Ip / moegg::kPackBlock}};
+    if (outputs_meet(outs, ins))
+        return MOEGG_EINVAL;
+    int cus = 0;
+    if (device_cus(&cus) != 0)
+        return MOEGG_EHIP;
+    moegg::GatedBwdParams p = {};
+    p.dY = static_cast<const char *>(dY);
+    p.W = static_cast<const char *>(W);
+    p.m_sizes = m_sizes;
+    p.gather = gather_idx;
+    p.A = static_cast<const char *>(A);
+    p.Aq = reinterpret_cast<const char *>(Aq);
+    p.As = As;
+    p.dA = static_cast<char *>(dA);
+    p.H = static_cast<char *>(H);
+    p.err = error_flags;
+    p.S = S;
+    p.ldy = (int64_t)N * 2;
+    p.ldw = (int64_t)I * 2;
+    p.topk = topk;
+    p.E = num_experts;
+    p.N = N;
+    p.I = I;
+    p.flags = flags;
+    const hipStream_t hs = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    hipError_t e = hipSuccess;
+    if (pad_y)
+        e = pad_operand(&p.dY, &p.ldy, ws, nullptr, 1, S, N, cus, hs);
+    if (e == hipSuccess && pad_w)
+        e = pad_operand(&p.W, &p.ldw, ws + padded_second(S, N), m_sizes, num_experts, N, I, cus,
+                        hs);
+    if (e != hipSuccess)
+        return MOEGG_EHIP;
+    return from_hip(moegg::gated_bwd_launch(p, cus, hs));
+}
+
+// Where dW's workspace holds X's rows again, and whether in expert order.
+static int64_t packed_rows_offset(int64_t S, int32_t E, int32_t N, int32_t K)
+{
+    return tiled_rows(N, K) ? moegg::dw_gather_offset(S, E, N, K) : 0;
+}
+
+size_t moegg_grouped_gemm_dW_packed_workspace_bytes(int32_t num_tokens, int32_t topk,
+                                                    int32_t num_experts, int32_t N, int32_t K)
+{
+    if (check_gemm_common(num_tokens, topk, num_experts, N, K) != MOEGG_OK)
+        return 0;
+    const int64_t S = (int64_t)num_tokens * topk;
+    return (size_t)(packed_rows_offset(S, num_experts, N, K) +
+                    (fits(S, K) ? S : num_tokens) * (int64_t)K * 2);
+}
+
+moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_scales,
+                                          const void *dY, const int32_t *m_sizes,
+                                          const int32_t *gather_idx, int32_t num_tokens,
+                                          int32_t topk, int32_t num_experts, int32_t N, int32_t K,
+                                          uint32_t flags, void *dW, void *workspace,
+                                          size_t workspace_bytes, int32_t *error_flags,
+                                          void *stream)
+{
+    moegg_status st = check_gemm_common(num_tokens, topk, num_experts, N, K);
+    if (st != MOEGG_OK)
+        return st;
+    if (flags & MOEGG_FUSE_MUL_POST)
+        return MOEGG_EUNSUPPORTED;
+    if (flags & ~(MOEGG_PERMUTE_X | MOEGG_PERMUTE_Y | MOEGG_DW_FP32_OUT))
+        return MOEGG_EINVAL;
+    const int64_t S = (int64_t)num_tokens * topk;
+    if ((st = check_permute_flags(flags, gather_idx, S)) != MOEGG_OK)
+        return st;
+    const bool px = flags & MOEGG_PERMUTE_X;
+    const int64_t x_rows = px ? num_tokens : S;
+    if (!fits(x_rows, K) || !fits(S, N))
+        return MOEGG_ESHAPE;
+    const bool fp32 = flags & MOEGG_DW_FP32_OUT;
+    if (!dW || !m_sizes || !aligned2(dW) || (fp32 && !aligned4(dW)))
+        return MOEGG_EINVAL;
+    if (num_tokens == 0)
+        return moegg_grouped_gemm_dW(nullptr, nullptr, m_sizes, nullptr, 0, topk, num_experts, N, K,
+                                     fp32 ? MOEGG_DW_FP32_OUT : 0, dW, nullptr, 0, error_flags,
+                                     stream);
+    if (!Xq || !x_scales || !dY || !aligned16(Xq) || !aligned2(dY) || !aligned16(workspace))
+        return MOEGG_EINVAL;
+    const int64_t need = (int64_t)moegg_grouped_gemm_dW_packed_workspace_bytes(
+        num_tokens, topk, num_experts, N, K);
+    if (!workspace || (int64_t)workspace_bytes < need)
+        return MOEGG_EWORKSPACE;
+    const int64_t Cp = moegg::packed_cols(K);
+    const Span outs[] = {{dW, (int64_t)num_experts * N * K * (fp32 ? 4 : 2)}, {workspace, need}};
+    const Span ins[] = {{Xq, x_rows * Cp}, {x_scales, x_rows * Cp / moegg::kPackBlock},
+                        {dY, S * N * 2}};
+    if (outputs_meet(outs, ins))
+        return MOEGG_EINVAL;
+    int cus = 0;
+    if (device_cus(&cus) != 0)
+        return MOEGG_EHIP;
+    // In expert order, or in token order where that copy would be 2 GiB or more.
+    const bool sorted = px && fits(S, K);
+    const int64_t off = packed_rows_offset(S, num_experts, N, K);
+    moegg::UnpackRowsParams x;
+    x.Q = reinterpret_cast<const char *>(Xq);
+    x.S = x_scales;
+    x.m_sizes = sorted ? m_sizes : nullptr;
+    x.gather = sorted ? gather_idx : nullptr;
+    x.out = static_cast<char *>(workspace) + off;
+    x.err = error_flags;
+    x.rows = sorted ? S : x_rows;
+    x.topk = topk;
+    x.E = num_experts;
+    x.cols = K;
+    if (moegg::unpack_rows_launch(x, cus, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return MOEGG_EHIP;
+    return moegg_grouped_gemm_dW(x.out, dY, m_sizes, gather_idx, num_tokens, topk, num_experts, N,
+                                 K, sorted ? flags & ~MOEGG_PERMUTE_X : flags, dW,
+                                 off > 0 ? workspace : nullptr, (size_t)off, error_flags, stream);
 }
 
 }  // extern "C"

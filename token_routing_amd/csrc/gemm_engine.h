@@ -56,9 +56,16 @@ __device__ __forceinline__ int lds_swz(int row, int chunk)
     return row * (BK * 2) + (swz_chunk(row, chunk) << 4);
 }
 
-template <int BM_, int BN_, int WM_, int WN_>
+// I8: operands are 8-bit integers with int32 accumulators.  A row of 2 k int8
+// has the bytes of a row of k bf16, and v_mfma_i32_32x32x32_i8 takes fragments
+// of the same 16 bytes a lane, twice as deep: only the MFMA differs (the
+// accumulators' bits are kept in the same registers).
+// SWAP: the MFMA's operands are exchanged, so that a lane's accumulators are 16
+// columns of one tile row instead of 16 rows of one column.
+template <int BM_, int BN_, int WM_, int WN_, bool SWAP_ = false, bool I8_ = false>
 struct Cfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+    static constexpr bool SWAP = SWAP_, I8 = I8_;
     static constexpr int NT = kWave * WM * WN;
     static constexpr int TM = BM / WM, TN = BN / WN;
     static constexpr int FM = TM / 32, FN = TN / 32;
@@ -337,6 +344,18 @@ __device__ __forceinline__ void read_step(const char *As, const char *Bs, int kk
     }
 }
 
+template <bool I8>
+__device__ __forceinline__ f32x16_t mfma_32(const bf16x8_t &a, const bf16x8_t &b, const f32x16_t &c)
+{
+    if constexpr (I8)
+        return __builtin_bit_cast(
+            f32x16_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                          __builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b),
+                          __builtin_bit_cast(i32x16_t, c), 0, 0, 0));
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
 template <class C, bool PART = false>
 __device__ __forceinline__ void mma_step(const bf16x8_t (&a)[C::FM], const bf16x8_t (&b)[C::FN],
                                          f32x16_t (&acc)[C::FM][C::FN], int ib = 0)
@@ -347,7 +366,8 @@ __device__ __forceinline__ void mma_step(const bf16x8_t (&a)[C::FM], const bf16x
             continue;
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = C::SWAP ? mfma_32<C::I8>(b[j], a[i], acc[i][j])
+                                : mfma_32<C::I8>(a[i], b[j], acc[i][j]);
     }
 }
 
