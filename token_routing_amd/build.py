@@ -33,7 +33,8 @@ FLAGS = [
 ]
 
 SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "gate.hip", "sort.hip",
-           "lora.hip", "block.hip", "pack.hip", "api.hip"]
+           "lora.hip", "block_i8.hip", "block_gated.hip", "block_bwd.hip",
+           "pack.hip", "api.hip"]
 
 
 def _compile(src: str, report: bool, defines=(), build_dir=BUILD) -> str:

@@ -1,6 +1,6 @@
 // The grouped-GEMM engine for gfx950: operand copies, MFMA stages, main loops,
 // epilogues and the tile schedule shared by the kernels of gemm.hip and
-// block.hip.
+// the block_* files.
 //
 // One engine serves all of them.  A workgroup owns an output tile of BM x BN
 // and walks the reduction in stages of BK = 64 elements:
