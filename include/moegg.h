@@ -708,7 +708,8 @@ moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, cons
  *   step = 2^(b - 127), the smallest with round(max |x| / step) <= 127, b >= 1
  *   code = round(x / step)                               (ties to even)
  * code * step is exact in bf16 (and fp32), so that reading it back loses
- * nothing more.  A block that holds an infinity or NaN gets b = 255 and reads
+ * nothing more.  b is at most 248, where codes are held at +-127 (magnitudes past
+ * 127.5 * 2^121).  A block that holds an infinity or NaN gets b = 255 and reads
  * back as NaN.
  *   X       [rows, cols] of `dtype`, rows ldx >= cols elements apart.
  *   Q       out [rows, Cp] int8, Cp = cols rounded up to a multiple of 32,

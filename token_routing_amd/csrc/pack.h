@@ -9,6 +9,10 @@
 // (half to even, at most half a step), and code * step has 7 bits, exact in bf16,
 // and in fp16 and fp32 inside their ranges.
 //
+// The largest step is 2^121 (b = 248), whose codes are held at +-127, so that no
+// value reads back as an infinity: magnitudes from 127.5 * 2^121 on (the largest
+// bf16, and the last 2^-8 of fp32's range) come back as 127 * 2^121.
+//
 // b = 255 marks a block that holds an infinity or NaN: its codes are 0, and
 // 0 * 2^128 (infinity's bits) reads back as NaN.
 #pragma once
@@ -19,35 +23,62 @@ namespace moegg {
 
 constexpr uint32_t kAbsBits = 0x7fffffffu, kInfBits = 0x7f800000u;
 
-// The byte of a block whose largest |x| has the bits m.
+constexpr uint32_t kLostBlock = 255, kLargestStep = 248;
+
+// The byte of a block whose largest |x| has the bits m: kLargestStep + 1 where
+// codes have to be held.
 __device__ __forceinline__ uint32_t pack_exp(uint32_t m)
 {
     const int b = max((int)((m + 0x10000u) >> 23) - 6, 1);
-    return m >= kInfBits ? 255u : (uint32_t)b;
-}
-// 1 / step (0 for a block that is not finite).
-__device__ __forceinline__ float pack_inverse(uint32_t b)
-{
-    return __builtin_bit_cast(float, b == 255u ? 0u : (254u - b) << 23);
+    return m >= kInfBits ? kLostBlock : (uint32_t)b;
 }
 __device__ __forceinline__ float pack_step(uint32_t b)
 {
-    return __builtin_bit_cast(float, b << 23);
+    return __uint_as_float(b << 23);
+}
+// 1 / step, a normal number for every b up to kLargestStep.
+__device__ __forceinline__ float pack_inverse(uint32_t b)
+{
+    return __uint_as_float((254u - b) << 23);
 }
 
 // Four codes.  x * inv + 1.5 * 2^23 is rounded to a whole number by the one
 // rounding of the fma, and its low byte is the code.
-__device__ __forceinline__ uint32_t pack_codes4(float x0, float x1, float x2, float x3, float inv,
-                                                bool finite)
+template <bool HOLD>
+__device__ __forceinline__ uint32_t pack_code(float x, float inv)
 {
     constexpr float kRound = 12582912.0f;
-    const uint32_t a = __builtin_bit_cast(uint32_t, __builtin_fmaf(x0, inv, kRound));
-    const uint32_t b = __builtin_bit_cast(uint32_t, __builtin_fmaf(x1, inv, kRound));
-    const uint32_t c = __builtin_bit_cast(uint32_t, __builtin_fmaf(x2, inv, kRound));
-    const uint32_t d = __builtin_bit_cast(uint32_t, __builtin_fmaf(x3, inv, kRound));
-    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
-    const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
-    return finite ? lo | hi : 0u;
+    float r = __builtin_fmaf(x, inv, kRound);
+    if constexpr (HOLD)
+        r = __builtin_amdgcn_fmed3f(r, kRound - 127.0f, kRound + 127.0f);
+    return __float_as_uint(r);
+}
+template <bool HOLD>
+__device__ __forceinline__ uint32_t pack_codes4(float x0, float x1, float x2, float x3, float inv)
+{
+    const uint32_t lo = __builtin_amdgcn_perm(pack_code<HOLD>(x1, inv), pack_code<HOLD>(x0, inv),
+                                              0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(pack_code<HOLD>(x3, inv), pack_code<HOLD>(x2, inv),
+                                              0x04000c0cu);
+    return lo | hi;
+}
+// N codes of a block of byte b (pack_exp's), four to a word; b becomes the byte to store.
+template <int N>
+__device__ __forceinline__ void pack_codes(const float (&f)[N], uint32_t &b, uint32_t (&w)[N / 4])
+{
+    const float inv = pack_inverse(b);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+        w[i] = pack_codes4<false>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], inv);
+    if (b > kLargestStep) {
+        const float most = pack_inverse(kLargestStep);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            w[i] = b == kLostBlock ? 0u
+                                   : pack_codes4<true>(f[4 * i], f[4 * i + 1], f[4 * i + 2],
+                                                       f[4 * i + 3], most);
+        b = b == kLostBlock ? kLostBlock : kLargestStep;
+    }
 }
 
 template <int N>
@@ -56,7 +87,7 @@ __device__ __forceinline__ uint32_t abs_max_bits(const float (&f)[N])
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        m = max(m, __builtin_bit_cast(uint32_t, f[i]) & kAbsBits);
+        m = max(m, __float_as_uint(f[i]) & kAbsBits);
     return m;
 }
 
@@ -66,13 +97,9 @@ __device__ __forceinline__ uint32_t pack_cols(const float (&f)[16], uint4 &codes
 {
     const uint32_t m = abs_max_bits(f);
     const auto o = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    const uint32_t b = pack_exp(max(o[0], o[1]));
-    const float inv = pack_inverse(b);
-    const bool fin = b != 255u;
-    codes.x = pack_codes4(f[0], f[1], f[2], f[3], inv, fin);
-    codes.y = pack_codes4(f[4], f[5], f[6], f[7], inv, fin);
-    codes.z = pack_codes4(f[8], f[9], f[10], f[11], inv, fin);
-    codes.w = pack_codes4(f[12], f[13], f[14], f[15], inv, fin);
+    uint32_t b = pack_exp(max(o[0], o[1])), w[4];
+    pack_codes(f, b, w);
+    codes = uint4{w[0], w[1], w[2], w[3]};
     return b;
 }
 

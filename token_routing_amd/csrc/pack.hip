@@ -158,12 +158,9 @@ __global__ __launch_bounds__(kPackThreads) void pack8_kernel(PackParams a)
             continue;
         float f[8];
         load8f<DT>(static_cast<const T *>(a.X) + row * a.ldx, col, a.cols, f);
-        const uint32_t b = pack_exp(quad_max(abs_max_bits(f)));
-        const float inv = pack_inverse(b);
-        const bool fin = b != 255u;
-        *reinterpret_cast<uint2 *>(a.Q + row * Cp + col) =
-            uint2{pack_codes4(f[0], f[1], f[2], f[3], inv, fin),
-                  pack_codes4(f[4], f[5], f[6], f[7], inv, fin)};
+        uint32_t b = pack_exp(quad_max(abs_max_bits(f))), w[2];
+        pack_codes(f, b, w);
+        *reinterpret_cast<uint2 *>(a.Q + row * Cp + col) = uint2{w[0], w[1]};
         if ((threadIdx.x & 3) == 0)
             a.S[(row * Cp + col) / kPackBlock] = (uint8_t)b;
     }
