@@ -2,14 +2,24 @@
 // with the MFMA's operands exchanged (Cfg::SWAP), on a ring of NST LDS stages of
 // DEPTH reduction elements (16-bit units: 64 or 32).
 //
-// LDS is addressed by 32-bit offsets throughout.  Stage s waits for its own
-// copies, passes one barrier, starts the copies of stage s + NST - 1 into the
-// buffer that every wave has left at that barrier, and runs its MFMAs.
+// LDS is addressed by 32-bit offsets throughout.  A stage's one wait and barrier
+// stand before its last 16-deep step (ring_loop_body), whose MFMAs then cover
+// the barrier, the reads of the next stage's first fragments and the start of
+// the copies that replace this stage.  Against the barrier at a stage's begin:
+// 8192 rows by 28672 columns of 4096 int8 0.985 -> 0.954 ms, the gated step of the
+// same sizes in bf16 3.13 -> 3.01 ms.  Tried and slower: 32-deep stages in a ring of
+// four (1.06 ms for the integers), copies spread over the MFMAs of the last step
+// (0.99) or of the whole stage (1.05), reads spread over the MFMAs (0.99), lines
+// touched two stages ahead (1.04).
+//
+// The epilogues leave LDS alone, so that a persistent kernel starts the next
+// tile's first stages (ring_start) before this tile's epilogue.
 #pragma once
 
 #include "gemm_engine.h"
 
 namespace moegg {
+
 
 // A 32-bit LDS offset as a pointer: no cast of a generic pointer, whose null
 // check costs instructions in the loop (and which the compiler rejects in some
@@ -96,107 +106,139 @@ struct RingTileLoader {
     }
 };
 
-template <class C, int DEPTH, int NST>
-struct Ring {
-    static constexpr int A = C::BM * DEPTH * 2, B = C::BN * DEPTH * 2, STAGE = A + B;
+// A tile shape (Cfg) with its ring: NST stages of DEPTH.
+template <int BM, int BN, int WM, int WN, bool I8, int DEPTH_, int NST_>
+struct RingCfg : Cfg<BM, BN, WM, WN, true, I8> {
+    static constexpr int DEPTH = DEPTH_, NST = NST_;
+    static constexpr int A = BM * DEPTH * 2, B = BN * DEPTH * 2, STAGE = A + B;
     static constexpr int BYTES = NST * STAGE;
+    static_assert((NST & (NST - 1)) == 0 && NST >= 2 && NST <= 4, "2 or 4 stages");
 };
 
-// Fragments of 16-deep step kk of the stage at LDS offset `st`.
-template <class C, int DEPTH, bool B_TR, bool PART>
-__device__ __forceinline__ void ring_read(uint32_t st, int kk, int wm, int wn,
-                                          bf16x8_t (&a)[C::FM], bf16x8_t (&b)[C::FN], int ib)
+// Fragment r (A blocks, then B blocks) of 16-deep step kk of the stage at LDS offset `st`.
+template <class C, bool B_TR, bool PART>
+__device__ __forceinline__ void ring_read_one(uint32_t st, int kk, int r, int wm, int wn,
+                                              bf16x8_t (&a)[C::FM], bf16x8_t (&b)[C::FN], int ib)
 {
+    constexpr int DEPTH = C::DEPTH;
     const int lane = threadIdx.x & (kWave - 1);
-    const int r = lane & 31, chunk = kk * 2 + (lane >> 5);
-    const uint32_t in = (uint32_t)(r * DEPTH * 2 + (ring_chunk<DEPTH>(r, chunk) << 4));
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-        if (!PART || i < ib)
-            a[i] = *lds_ptr<const bf16x8_t>(st + in + (wm * C::TM + i * 32) * DEPTH * 2);
-    const uint32_t bs = st + C::BM * DEPTH * 2;
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-        if constexpr (B_TR) {
-            const int q = lane & 15;
-            const int row = kk * 16 + 8 * (lane >> 5) + (q >> 2);
-            const int col = wn * C::TN + j * 32 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
-            const uint32_t at = bs + tr_off<C::BN>(row, col >> 3) + (col & 7) * 2;
-            const v4i16_t both[2] = {
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<v4i16_t>(at)),
-                __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<v4i16_t>(at + 4 * C::BN * 2))};
-            b[j] = __builtin_bit_cast(bf16x8_t, both);
-        } else {
-            b[j] = *lds_ptr<const bf16x8_t>(bs + in + (wn * C::TN + j * 32) * DEPTH * 2);
-        }
+    const int row = lane & 31, chunk = kk * 2 + (lane >> 5);
+    const uint32_t in = (uint32_t)(row * DEPTH * 2 + (ring_chunk<DEPTH>(row, chunk) << 4));
+    if (r < C::FM) {
+        if (!PART || r < ib)
+            a[r] = *lds_ptr<const bf16x8_t>(st + in + (wm * C::TM + r * 32) * DEPTH * 2);
+        return;
+    }
+    const int j = r - C::FM;
+    const uint32_t bs = st + C::A;
+    if constexpr (B_TR) {
+        const int q = lane & 15;
+        const int k = kk * 16 + 8 * (lane >> 5) + (q >> 2);
+        const int col = wn * C::TN + j * 32 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
+        const uint32_t at = bs + tr_off<C::BN>(k, col >> 3) + (col & 7) * 2;
+        const v4i16_t both[2] = {
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<v4i16_t>(at)),
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_ptr<v4i16_t>(at + 4 * C::BN * 2))};
+        b[j] = __builtin_bit_cast(bf16x8_t, both);
+    } else {
+        b[j] = *lds_ptr<const bf16x8_t>(bs + in + (wn * C::TN + j * 32) * DEPTH * 2);
     }
 }
 
-// copy(s, n, lds): this wave's copy n (0 .. CPS - 1) of stage s to the LDS offset of
-// its buffer.
-template <class C, int DEPTH, int NST, bool B_TR, int CPS, bool PART, class Copy>
-__device__ __forceinline__ void ring_loop_body(uint32_t lds, int nsteps,
-                                               f32x16_t (&acc)[C::FM][C::FN], Copy &copy, int wm,
-                                               int wn, int ib)
+// Waits until at most the copies of the last `newer` stages are in flight.
+template <int CPS>
+__device__ __forceinline__ void wait_stages(int newer)
 {
-    typedef Ring<C, DEPTH, NST> R;
-    constexpr int KK = DEPTH / 16;
-    // None of the compiler's own loads is pending from here on: a wait for one
-    // inside the loop would wait for the copies too.
-    __builtin_amdgcn_s_waitcnt(0);
-    for (int s = 0; s < NST - 1 && s < nsteps; ++s)
+    if (newer >= 3)
+        wait_vmcnt<3 * CPS>();
+    else if (newer == 2)
+        wait_vmcnt<2 * CPS>();
+    else if (newer == 1)
+        wait_vmcnt<CPS>();
+    else
+        wait_vmcnt<0>();
+}
+
+// Starts the copies of the first NST stages of a tile.  copy(s, n, lds): this
+// wave's copy n (0 .. CPS - 1) of stage s to the LDS offset of its buffer.
+template <class C, int CPS, class Copy>
+__device__ __forceinline__ void ring_start(uint32_t lds, int nsteps, const Copy &copy)
+{
+    for (int s = 0; s < C::NST && s < nsteps; ++s)
 #pragma unroll
         for (int n = 0; n < CPS; ++n)
-            copy(s, n, lds + s * R::STAGE);
+            copy(s, n, lds + s * C::STAGE);
+}
+
+// A stage's last step holds the wait and the barrier: behind it every wave has
+// read the stage's last fragments, so that its buffer takes the copies of stage
+// s + NST, and stage s + 1 has landed, so that its first fragments are read while
+// the last step's MFMAs run.
+template <class C, bool B_TR, int CPS, bool PART, class Copy>
+__device__ __forceinline__ void ring_loop_body(uint32_t lds, int nsteps,
+                                               f32x16_t (&acc)[C::FM][C::FN], const Copy &copy,
+                                               int wm, int wn, int ib)
+{
+    constexpr int KK = C::DEPTH / 16, NST = C::NST, NR = C::FM + C::FN;
+    static_assert(KK % 2 == 0, "two sets of fragments");
+    bf16x8_t a[2][C::FM], b[2][C::FN];
+    // Stage 0 has landed: loads complete in order among themselves, so that with one
+    // of its copies outstanding those of the other stages started are as well, and
+    // more operations (stores behind them or not) than are allowed here.
+    wait_stages<CPS>(min(NST, nsteps) - 1);
+    wait_lds();
+    wg_barrier();
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+        ring_read_one<C, B_TR, PART>(lds, 0, r, wm, wn, a[0], b[0], ib);
     for (int s = 0; s < nsteps; ++s) {
-        const int pending = min(NST - 2, nsteps - 1 - s);
-        if (pending >= 2)
-            wait_vmcnt<2 * CPS>();
-        else if (pending == 1)
-            wait_vmcnt<CPS>();
-        else
-            wait_vmcnt<0>();
-        wait_lds();
-        wg_barrier();
-        if (s + NST - 1 < nsteps) {
-            const uint32_t to = lds + ((s + NST - 1) & (NST - 1)) * R::STAGE;
+        const uint32_t st = lds + (s & (NST - 1)) * C::STAGE;
+        const uint32_t next = lds + ((s + 1) & (NST - 1)) * C::STAGE;
 #pragma unroll
-            for (int n = 0; n < CPS; ++n)
-                copy(s + NST - 1, n, to);
-        }
-        const uint32_t st = lds + (s & (NST - 1)) * R::STAGE;
-        // Fragment reads a step ahead of the MFMAs.
-        bf16x8_t a[2][C::FM], b[2][C::FN];
-        ring_read<C, DEPTH, B_TR, PART>(st, 0, wm, wn, a[0], b[0], ib);
+        for (int kk = 0; kk < KK - 1; ++kk) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-            if (kk + 1 < KK)
-                ring_read<C, DEPTH, B_TR, PART>(st, kk + 1, wm, wn, a[(kk + 1) & 1],
-                                                b[(kk + 1) & 1], ib);
+            for (int r = 0; r < NR; ++r)
+                ring_read_one<C, B_TR, PART>(st, kk + 1, r, wm, wn, a[(kk + 1) & 1], b[(kk + 1) & 1],
+                                             ib);
             __builtin_amdgcn_sched_barrier(0);
             mma_step<C, PART>(a[kk & 1], b[kk & 1], acc, ib);
             __builtin_amdgcn_sched_barrier(0);
         }
+        wait_stages<CPS>(min(NST - 2, nsteps - 2 - s));  // those started after s + 1
+        wait_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        wg_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < nsteps) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                ring_read_one<C, B_TR, PART>(next, 0, r, wm, wn, a[0], b[0], ib);
+        }
+        if (s + NST < nsteps) {
+#pragma unroll
+            for (int n = 0; n < CPS; ++n)
+                copy(s + NST, n, st);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mma_step<C, PART>(a[(KK - 1) & 1], b[(KK - 1) & 1], acc, ib);
+        __builtin_amdgcn_sched_barrier(0);
     }
-    wait_lds();
-    wg_barrier();
 }
 
-// rows: real rows of the tile; a wave of a ragged tail skips its padding blocks'
-// reads and MFMAs and keeps every barrier.
-template <class C, int DEPTH, int NST, bool B_TR, int CPS, class Copy>
+// The tile whose copies ring_start began.  rows: real rows of the tile; a wave of a
+// ragged tail skips its padding blocks' reads and MFMAs and keeps every barrier.
+template <class C, bool B_TR, int CPS, class Copy>
 __device__ __forceinline__ void ring_loop(uint32_t lds, int nsteps, f32x16_t (&acc)[C::FM][C::FN],
-                                          Copy copy, int rows)
+                                          const Copy &copy, int rows)
 {
-    static_assert((NST & (NST - 1)) == 0 && NST >= 2 && NST <= 4, "2 or 4 stages");
     const int wave = threadIdx.x / kWave;
     const int wm = wave / C::WN, wn = wave % C::WN;
     const int ib = __builtin_amdgcn_readfirstlane(
         min(C::FM, max(0, (rows - wm * C::TM + 31) / 32)));
     if (ib == C::FM)
-        ring_loop_body<C, DEPTH, NST, B_TR, CPS, false>(lds, nsteps, acc, copy, wm, wn, ib);
+        ring_loop_body<C, B_TR, CPS, false>(lds, nsteps, acc, copy, wm, wn, ib);
     else
-        ring_loop_body<C, DEPTH, NST, B_TR, CPS, true>(lds, nsteps, acc, copy, wm, wn, ib);
+        ring_loop_body<C, B_TR, CPS, true>(lds, nsteps, acc, copy, wm, wn, ib);
 }
 
 }  // namespace moegg

@@ -1,0 +1,37 @@
+// The gated feed-forward block's forward in bf16, gfx950 (moegg_gated_fwd): gelu.
+#include "block_fwd.h"
+
+namespace moegg {
+
+using GatedBigCfg = RingCfg<256, 256, 4, 2, false, 64, 2>;
+using GatedSmallCfg = RingCfg<32, 256, 1, 4, false, 64, 2>;
+
+template <int ACT, int KEEP, bool TAIL>
+static void gated_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
+{
+    if (p.S / p.E < kBlockSmallRows)
+        block_fwd_cfg<GatedSmallCfg, ACT, KEEP, TAIL>(p, cus, stream);
+    else
+        block_fwd_cfg<GatedBigCfg, ACT, KEEP, TAIL>(p, cus, stream);
+}
+
+template <int ACT, bool TAIL>
+static void gated_keep(const BlockFwdParams &p, int cus, hipStream_t stream)
+{
+    if (p.Aq)
+        gated_rows<ACT, kKeepPacked, TAIL>(p, cus, stream);
+    else if (p.A)
+        gated_rows<ACT, kKeepBf16, TAIL>(p, cus, stream);
+    else
+        gated_rows<ACT, kKeepNone, TAIL>(p, cus, stream);
+}
+
+void gated_fwd_gelu(const BlockFwdParams &p, int cus, hipStream_t stream)
+{
+    if (p.N / 2 % 8)
+        gated_keep<kGelu, true>(p, cus, stream);
+    else
+        gated_keep<kGelu, false>(p, cus, stream);
+}
+
+}  // namespace moegg

@@ -5,25 +5,29 @@ namespace moegg {
 
 // Tile shapes: many rows per expert, and few (the weights are then streamed
 // once per 32-row tile).
-using I8BigCfg = Cfg<256, 256, 2, 4, true, true>;
-using I8SmallCfg = Cfg<32, 128, 1, 4, true, true>;
-using I8SmallGatedCfg = Cfg<32, 256, 1, 4, true, true>;
+using I8BigCfg = RingCfg<256, 256, 2, 4, true, 64, 2>;
+using I8SmallCfg = RingCfg<32, 128, 1, 4, true, 64, 2>;
+using I8SmallGatedCfg = RingCfg<32, 256, 1, 4, true, 64, 2>;
+
+template <int ACT, bool TAIL>
+static void i8_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
+{
+    using Small = std::conditional_t<ACT == kPlain, I8SmallCfg, I8SmallGatedCfg>;
+    if (p.S / p.E < kBlockSmallRows)
+        block_fwd_cfg<Small, ACT, kKeepNone, TAIL>(p, cus, stream);
+    else
+        block_fwd_cfg<I8BigCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
+}
 
 template <bool TAIL>
 static void i8_tail(const BlockFwdParams &p, int cus, hipStream_t stream)
 {
-    const bool small = p.S / p.E < kBlockSmallRows;
-    if (p.flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU)) {
-        if (small)
-            block_fwd_cfg<I8SmallGatedCfg, true, kKeepNone, TAIL>(p, cus, stream);
-        else
-            block_fwd_cfg<I8BigCfg, true, kKeepNone, TAIL>(p, cus, stream);
-    } else {
-        if (small)
-            block_fwd_cfg<I8SmallCfg, false, kKeepNone, TAIL>(p, cus, stream);
-        else
-            block_fwd_cfg<I8BigCfg, false, kKeepNone, TAIL>(p, cus, stream);
-    }
+    if (p.flags & MOEGG_GATED_SILU)
+        i8_rows<kSilu, TAIL>(p, cus, stream);
+    else if (p.flags & MOEGG_GATED_GELU)
+        i8_rows<kGelu, TAIL>(p, cus, stream);
+    else
+        i8_rows<kPlain, TAIL>(p, cus, stream);
 }
 
 hipError_t i8_launch(const BlockFwdParams &p, int cus, hipStream_t stream)

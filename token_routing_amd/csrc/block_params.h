@@ -103,7 +103,17 @@ inline int64_t padded_row_bytes(int64_t cols)
 }
 
 hipError_t i8_launch(const BlockFwdParams &p, int cus, hipStream_t stream);
-hipError_t gated_fwd_launch(const BlockFwdParams &p, int cus, hipStream_t stream);
+// The two activations, compiled apart.
+void gated_fwd_silu(const BlockFwdParams &p, int cus, hipStream_t stream);
+void gated_fwd_gelu(const BlockFwdParams &p, int cus, hipStream_t stream);
+inline hipError_t gated_fwd_launch(const BlockFwdParams &p, int cus, hipStream_t stream)
+{
+    if (p.flags & MOEGG_GATED_GELU)
+        gated_fwd_gelu(p, cus, stream);
+    else
+        gated_fwd_silu(p, cus, stream);
+    return hipGetLastError();
+}
 hipError_t gated_bwd_launch(const GatedBwdParams &p, int cus, hipStream_t stream);
 hipError_t quant_rows_launch(const QuantParams &p, int dtype, hipStream_t stream);
 hipError_t pack8_launch(const PackParams &p, int dtype, hipStream_t stream);

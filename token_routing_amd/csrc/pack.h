@@ -93,14 +93,25 @@ __device__ __forceinline__ uint32_t abs_max_bits(const float (&f)[N])
 
 // 16 columns of a lane and the 16 of the lane 32 away form a block: both get
 // its byte, each the codes of its own columns.  All lanes take part.
-__device__ __forceinline__ uint32_t pack_cols(const float (&f)[16], uint4 &codes)
+__device__ __forceinline__ uint32_t pack_cols(const float (&f)[16], uint32_t (&codes)[4])
 {
     const uint32_t m = abs_max_bits(f);
     const auto o = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    uint32_t b = pack_exp(max(o[0], o[1])), w[4];
-    pack_codes(f, b, w);
-    codes = uint4{w[0], w[1], w[2], w[3]};
+    uint32_t b = pack_exp(max(o[0], o[1]));
+    pack_codes(f, b, codes);
     return b;
+}
+
+// Codes of columns 8 (l / 32) .. + 7 and 16 + 8 (l / 32) .. + 7 of a block, and of
+// columns 16 (l / 32) .. + 15: each is the other's by the same exchange.
+__device__ __forceinline__ void exchange_codes(uint32_t (&w)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const auto r = __builtin_amdgcn_permlane32_swap(w[i], w[2 + i], false, false);
+        w[i] = r[0];
+        w[2 + i] = r[1];
+    }
 }
 
 __device__ __forceinline__ void unpack4(uint32_t q, float step, float *f)
@@ -111,13 +122,12 @@ __device__ __forceinline__ void unpack4(uint32_t q, float step, float *f)
     f[3] = (float)(int8_t)(q >> 24) * step;
 }
 
-__device__ __forceinline__ void unpack_cols(const uint4 &q, uint32_t b, float (&f)[16])
+// The values of 8 codes.
+__device__ __forceinline__ void unpack_cols(uint32_t lo, uint32_t hi, uint32_t b, float (&f)[8])
 {
     const float step = pack_step(b);
-    unpack4(q.x, step, f);
-    unpack4(q.y, step, f + 4);
-    unpack4(q.z, step, f + 8);
-    unpack4(q.w, step, f + 12);
+    unpack4(lo, step, f);
+    unpack4(hi, step, f + 4);
 }
 
 }  // namespace moegg
