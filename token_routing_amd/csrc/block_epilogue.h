@@ -1,12 +1,17 @@
-// Epilogues of the feed-forward block's kernels on the main loop of
-// block_engine.h: a lane then holds 16 columns of
-// one output row in each 32 x 32 block, and one exchange with the lane 32 away
-// makes them two times 8 neighbours (row_cols).  Scales, activation, block maxima and codes
-// need no other lane but that one, and a row's 32 columns leave in whole 32- or
-// 64-byte pieces without shared memory.
+// Epilogues of the feed-forward block's kernels on the main loop of block_engine.h: a
+// lane holds 16 columns of one output row in each 32 x 32 block, and one exchange
+// with the lane 32 away makes them two times 8 neighbours (row_cols).  Scales,
+// activation, block maxima and codes need no other lane but that one, and a row's 32
+// columns leave in whole 32- or 64-byte pieces without shared memory.  Their stores
+// are at the memory's rate (8192 x 14336 bf16 of H and twice that of A in 110 us), but
+// a compute unit's MFMAs wait for them: with 256 accumulator columns a wave pair
+// fills the registers, so that no second tile runs beside.  Tried and slower:
+// nontemporal stores (the backward 1.19 -> 1.58 ms: a row's line leaves in pieces),
+// groups of workgroups started apart (no gain beyond their delay).
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <utility>
 
 #include "block_engine.h"
@@ -16,10 +21,8 @@
 
 namespace moegg {
 
-typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 // 16 bytes at the alignment of a bf16 (or a byte): global memory takes them so.
 typedef unsigned short u16x8_any_t __attribute__((ext_vector_type(8), aligned(2)));
-typedef unsigned u32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
 
 // x of the lanes below 32 with y of those from 32 on: afterwards x holds both
 // first halves (x's own, then y's), y both second halves.
@@ -166,8 +169,31 @@ inline int64_t row_tiles(int64_t rows, int E, int block)
     return rows <= E ? rows : (rows - E + 1 + block - 1) / block + E - 1;
 }
 
-// Average rows per expert below which the small tiles are used, as for the
-// bf16 products.
-constexpr int64_t kBlockSmallRows = 96;
+// Tile shapes: small (32 rows: for a few row tiles of streamed weights), middle (128 x
+// 128, two workgroups a compute unit) and large (256 x 256, one).
+enum Shape { kSmallTiles, kMidTiles, kBigTiles };
+
+// Which of them a launch takes.  Rows per expert are known on the device alone: an
+// expert's last row tile counts as half full (one expert's is known).
+//   small   where a launch is bound by latency: it has up to `most_small` rounds of
+//           small tiles.  8 experts of 64 rows, 2048 into 2048: int8 16.2 us (middle
+//           19.5, large 27.8), bf16 23.9 (29.5, 47.6).
+//   large   where their rounds over the compute units cost less than the middle
+//           tiles', 1.65 times as much a round, two tiles a unit in a middle one whose
+//           last round costs what it fills: 60 experts, 2048 into 2048 int8, of 1024
+//           rows 318 us (middle 362, small 690), of 128 rows 85 (66, 140).
+// Swept over 1, 8 and 60 experts of 16 to 1024 rows and 512 to 8192 columns.
+inline Shape tile_shape(int64_t S, int E, int cols, int small_cols, double most_small, int cus)
+{
+    auto rounds = [&](int64_t bm, int64_t bn, int a_round) {
+        const int64_t rows =
+            E == 1 ? (S + bm - 1) / bm : std::max(std::min<int64_t>(S, E), S / bm + E / 2);
+        return (double)(rows * ((cols + bn - 1) / bn)) / a_round;
+    };
+    if (rounds(32, small_cols, cus) <= most_small)
+        return kSmallTiles;
+    const double mid = std::max(0.6, rounds(128, 128, 2 * cus) + 0.2);
+    return 1.65 * std::ceil(rounds(256, 256, cus)) < mid ? kBigTiles : kMidTiles;
+}
 
 }  // namespace moegg

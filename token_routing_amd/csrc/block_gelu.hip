@@ -4,13 +4,17 @@
 namespace moegg {
 
 using GatedBigCfg = RingCfg<256, 256, 4, 2, false, 64, 2>;
-using GatedSmallCfg = RingCfg<32, 256, 1, 4, false, 64, 2>;
+using GatedMidCfg = RingCfg<128, 128, 2, 2, false, 64, 2>;
+using GatedSmallCfg = RingCfg<32, 256, 1, 4, false, 64, 4>;
 
 template <int ACT, int KEEP, bool TAIL>
 static void gated_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
 {
-    if (p.S / p.E < kBlockSmallRows)
+    const Shape shape = tile_shape(p.S, p.E, p.N, GatedSmallCfg::BN, 0.75, cus);
+    if (shape == kSmallTiles)
         block_fwd_cfg<GatedSmallCfg, ACT, KEEP, TAIL>(p, cus, stream);
+    else if (shape == kMidTiles)
+        block_fwd_cfg<GatedMidCfg, ACT, KEEP, TAIL>(p, cus, stream);
     else
         block_fwd_cfg<GatedBigCfg, ACT, KEEP, TAIL>(p, cus, stream);
 }

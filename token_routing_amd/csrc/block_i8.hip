@@ -3,18 +3,20 @@
 
 namespace moegg {
 
-// Tile shapes: many rows per expert, and few (the weights are then streamed
-// once per 32-row tile).
 using I8BigCfg = RingCfg<256, 256, 2, 4, true, 64, 2>;
-using I8SmallCfg = RingCfg<32, 128, 1, 4, true, 64, 2>;
-using I8SmallGatedCfg = RingCfg<32, 256, 1, 4, true, 64, 2>;
+using I8MidCfg = RingCfg<128, 128, 2, 2, true, 64, 2>;
+using I8SmallCfg = RingCfg<32, 128, 1, 4, true, 64, 4>;
+using I8SmallGatedCfg = RingCfg<32, 256, 1, 4, true, 64, 4>;
 
 template <int ACT, bool TAIL>
 static void i8_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
 {
     using Small = std::conditional_t<ACT == kPlain, I8SmallCfg, I8SmallGatedCfg>;
-    if (p.S / p.E < kBlockSmallRows)
+    const Shape shape = tile_shape(p.S, p.E, p.N, Small::BN, 0.75, cus);
+    if (shape == kSmallTiles)
         block_fwd_cfg<Small, ACT, kKeepNone, TAIL>(p, cus, stream);
+    else if (shape == kMidTiles)
+        block_fwd_cfg<I8MidCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
     else
         block_fwd_cfg<I8BigCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
 }
