@@ -804,8 +804,8 @@ size_t moegg_gated_bwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t
  * moegg_grouped_gemm_dW_packed -- moegg_grouped_gemm_dW with X as moegg_pack8
  * keeps it: Xq [T or S, Cp] int8 and x_scales [T or S, Cp / 32], Cp = K rounded up to
  * a multiple of 32.  The rows are expanded to bf16 (without loss) in the
- * workspace, in expert order, and reduced there; everything else, the split
- * of hot experts among it, as moegg_grouped_gemm_dW.
+ * workspace, in expert order where that pays, and reduced there; everything
+ * else, the split of hot experts among it, as moegg_grouped_gemm_dW.
  *   workspace  device, 16-byte aligned, required:
  *              moegg_grouped_gemm_dW_packed_workspace_bytes(...) bytes.
  */
@@ -818,7 +818,8 @@ moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_sca
                                           void *stream);
 
 size_t moegg_grouped_gemm_dW_packed_workspace_bytes(int32_t num_tokens, int32_t topk,
-                                                    int32_t num_experts, int32_t N, int32_t K);
+                                                    int32_t num_experts, int32_t N, int32_t K,
+                                                    uint32_t flags);
 
 #ifdef __cplusplus
 }

@@ -177,8 +177,11 @@ def test_workspace_sizes(lib):
     assert b(10, 2, 0, 32, 64) == 0
     assert b(10, 2, 4, 63, 7) == 20 * 128 + 4 * 63 * 16
     d = lib.moegg_grouped_gemm_dW_packed_workspace_bytes
-    assert d(10, 2, 4, 0, 64) == 0
-    assert d(10, 2, 4, 64, 32) >= 20 * 32 * 2 and d(10, 2, 4, 63, 31) == 20 * 31 * 2
+    assert d(10, 2, 4, 0, 64, 0) == 0
+    assert d(10, 2, 4, 64, 32, PX) == 10 * 32 * 2            # token order
+    assert d(10, 2, 4, 64, 32, 0) == d(10, 2, 4, 64, 32, PY) == 20 * 32 * 2
+    assert d(10, 2, 4, 4096, 32, PX) == 20 * 32 * 2          # expert order
+    assert d(10, 2, 4, 63, 31, PX) == 20 * 31 * 2
 
 
 def test_binding_refuses():

@@ -183,7 +183,7 @@ def test_given_buffers(mg):
                      device="cuda")
     ws2 = torch.empty(lib.moegg_gated_bwd_workspace_bytes(T, k, E, K, I), dtype=torch.uint8,
                       device="cuda")
-    ws3 = torch.empty(mg.dw_packed_workspace_bytes(T, k, E, 2 * I, K), dtype=torch.uint8,
+    ws3 = torch.empty(mg.dw_packed_workspace_bytes(T, k, E, 2 * I, K, mg.PERMUTE_X), dtype=torch.uint8,
                       device="cuda")
     for seed in range(2):
         x = torch.randn(T, K, generator=g).bfloat16().cuda()

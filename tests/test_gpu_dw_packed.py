@@ -30,6 +30,9 @@ CASES = [
     (700, 1, 2, 128, 96, "none", False),
     (2100, 2, 3, 256, 64, "x", False),                   # split reductions
     (90, 3, 5, 33, 47, "y", False),
+    (300, 2, 3, 2504, 40, "x", False),                   # expanded in expert order
+    (300, 2, 3, 2496, 40, "x", True),                    # and in token order
+    (1100, 8, 4, 24, 136, "x", False),
 ]
 
 

@@ -155,7 +155,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moegg_grouped_gemm_dW_packed.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, u32,
                                                  vp, vp, sz, vp, vp]
     lib.moegg_grouped_gemm_dW_packed.restype = ctypes.c_int
-    lib.moegg_grouped_gemm_dW_packed_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.moegg_grouped_gemm_dW_packed_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, u32]
     lib.moegg_grouped_gemm_dW_packed_workspace_bytes.restype = sz
     _lib = lib
     return lib
@@ -1087,11 +1087,11 @@ def gated_bwd(dY, W, kept, m_sizes, gather_idx, topk: int, flags: int, *, want_h
     return _run(dev, stream, call)
 
 
-def dw_packed_workspace_bytes(num_tokens: int, topk: int, num_experts: int, N: int,
-                              K: int) -> int:
-    """Workspace bytes of grouped_gemm_dW_packed."""
+def dw_packed_workspace_bytes(num_tokens: int, topk: int, num_experts: int, N: int, K: int,
+                              flags: int) -> int:
+    """Workspace bytes of grouped_gemm_dW_packed with these flags."""
     return int(load_library().moegg_grouped_gemm_dW_packed_workspace_bytes(
-        num_tokens, topk, num_experts, N, K))
+        num_tokens, topk, num_experts, N, K, int(flags)))
 
 
 def grouped_gemm_dW_packed(Xq, x_scales, dY, m_sizes, gather_idx, topk: int, flags: int, *, K: int,
@@ -1114,7 +1114,7 @@ def grouped_gemm_dW_packed(Xq, x_scales, dY, m_sizes, gather_idx, topk: int, fla
     def call(stream_ptr):
         w, w_ptr = _out(dW, "dW", torch.float32 if flags & DW_FP32_OUT else torch.bfloat16,
                         (E, N, K), dev)
-        need = lib.moegg_grouped_gemm_dW_packed_workspace_bytes(T, topk, E, N, K)
+        need = lib.moegg_grouped_gemm_dW_packed_workspace_bytes(T, topk, E, N, K, int(flags))
         ws, ws_ptr = _workspace_arg(workspace, need, dev)
         _check(lib.moegg_grouped_gemm_dW_packed(
             _arg(Xq, "Xq", torch.int8, q_shape, index),

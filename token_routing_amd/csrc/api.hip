@@ -1478,20 +1478,36 @@ moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_siz
     return from_hip(moegg::gated_bwd_launch(p, cus, hs));
 }
 
-// Where dW's workspace holds X's rows again, and whether in expert order.
+// Where dW's workspace holds X's rows again.
 static int64_t packed_rows_offset(int64_t S, int32_t E, int32_t N, int32_t K)
 {
     return tiled_rows(N, K) ? moegg::dw_gather_offset(S, E, N, K) : 0;
 }
 
+// Whether they stand there in expert order (under PERMUTE_X; else in token order, and the
+// reduction gathers).  The order's copy writes topk - 1 times X's bytes more, and
+// the gather costs the reduction 1 to 5%: expert order pays above N of about 5000
+// (1 - 1 / topk).  8192 tokens of 2048, top-8: into 1536 598 us in token order, 677
+// in expert order; 4096 of 4096, top-2: into 28672 2148 and 2018.  The any-shape
+// reduction gathers at twice its time.
+static bool packed_in_order(int64_t T, int32_t topk, int32_t N, int32_t K)
+{
+    return fits(T * topk, K) &&
+           (!tiled_rows(N, K) || topk == 1 || (int64_t)N * topk > 5000 * (int64_t)(topk - 1));
+}
+static int64_t packed_rows(int64_t T, int32_t topk, int32_t N, int32_t K, uint32_t flags)
+{
+    return (flags & MOEGG_PERMUTE_X) && !packed_in_order(T, topk, N, K) ? T : T * topk;
+}
+
 size_t moegg_grouped_gemm_dW_packed_workspace_bytes(int32_t num_tokens, int32_t topk,
-                                                    int32_t num_experts, int32_t N, int32_t K)
+                                                    int32_t num_experts, int32_t N, int32_t K,
+                                                    uint32_t flags)
 {
     if (check_gemm_common(num_tokens, topk, num_experts, N, K) != MOEGG_OK)
         return 0;
-    const int64_t S = (int64_t)num_tokens * topk;
-    return (size_t)(packed_rows_offset(S, num_experts, N, K) +
-                    (fits(S, K) ? S : num_tokens) * (int64_t)K * 2);
+    return (size_t)(packed_rows_offset((int64_t)num_tokens * topk, num_experts, N, K) +
+                    packed_rows(num_tokens, topk, N, K, flags) * K * 2);
 }
 
 moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_scales,
@@ -1526,7 +1542,7 @@ moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_sca
     if (!Xq || !x_scales || !dY || !aligned16(Xq) || !aligned2(dY) || !aligned16(workspace))
         return MOEGG_EINVAL;
     const int64_t need = (int64_t)moegg_grouped_gemm_dW_packed_workspace_bytes(
-        num_tokens, topk, num_experts, N, K);
+        num_tokens, topk, num_experts, N, K, flags);
     if (!workspace || (int64_t)workspace_bytes < need)
         return MOEGG_EWORKSPACE;
     const int64_t Cp = moegg::packed_cols(K);
@@ -1538,8 +1554,7 @@ moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_sca
     int cus = 0;
     if (device_cus(&cus) != 0)
         return MOEGG_EHIP;
-    // In expert order, or in token order where that copy would be 2 GiB or more.
-    const bool sorted = px && fits(S, K);
+    const bool sorted = px && packed_in_order(num_tokens, topk, N, K);
     const int64_t off = packed_rows_offset(S, num_experts, N, K);
     moegg::UnpackRowsParams x;
     x.Q = reinterpret_cast<const char *>(Xq);

@@ -46,97 +46,175 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m)
     return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4e, 0xf, 0xf, false));
 }
 
+// Over the wave: rotations inside the rows of 16 lanes, then exchanges of rows and
+// halves, registers all (six shuffles through LDS: 65536 rows of 768 bf16 46 us).
 __device__ __forceinline__ uint32_t wave_max(uint32_t m)
 {
-    for (int d = 1; d < kWave; d <<= 1)
-        m = max(m, (uint32_t)__shfl_xor((int)m, d, kWave));
-    return m;
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xf, 0xf, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xf, 0xf, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xf, 0xf, false));
+    const auto r = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max(r[0], r[1]);
+    const auto h = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max(h[0], h[1]);
 }
 
-// round(127 x / m) of real numbers, ties to even.  t = x * (127 / m) is within
-// 2^-23 * 127 of the quotient; where that leaves the rounding open, the quotient
-// is taken in 64 bits: 127 x is exact there (31 bits), and a quotient of at least
-// 1/2 by a number of 24 bits is either a tie or at least 2^-34 away from one.
-__device__ __forceinline__ int row_code(float x, float inv, float m)
+// About 127 / m: v_rcp_f32 is good to an ulp, the product to half a one.  0 or
+// infinite where it leaves fp32's normal numbers.
+__device__ __forceinline__ float row_inverse(uint32_t m)
 {
-    const float t = x * inv;
-    const float r = rintf(t);
-    if (fabsf(fabsf(t - r) - 0.5f) < 1e-4f)
-        return (int)rint((double)x * 127.0 / (double)m);
-    return (int)r;
+    return 127.0f * __builtin_amdgcn_rcpf(__uint_as_float(m));
+}
+
+// round(127 x / m) of real numbers, ties to even, for 8 values, as bytes.  t = x * inv
+// is within 127 * 2^-22 of the quotient, and adding 1.5 * 2^23 leaves its rounding
+// in the low byte.  Where a t comes so near to a tie that the rounding is open (or
+// inv is no number to use), the quotients are taken in 64 bits: 127 x is exact there
+// (31 bits), and a quotient of at least 1/2 by a number of 24 bits is either a tie or
+// at least 2^-34 away from one.
+__device__ __forceinline__ void row_codes(const float (&x)[8], float inv, float m,
+                                          uint32_t (&w)[2])
+{
+    constexpr float kRound = 12582912.0f;
+    uint32_t c[8];
+    float open = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = x[i] * inv, r = t + kRound;
+        c[i] = __float_as_uint(r);
+        open = fmaxf(open, fabsf(t - (r - kRound)));
+    }
+    if (open > 0.49996f || !(inv > 0.0f && inv < __builtin_inff())) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            c[i] = (uint32_t)(int)rint((double)x[i] * 127.0 / (double)m);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0c0c0400u) |
+               __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x04000c0cu);
 }
 
 }  // namespace
 
-// One workgroup of THREADS per row.  A row's values stay in registers between
-// the maximum and the codes up to THREADS * 32 columns; the columns past that
-// are read again.
-template <int DT, int THREADS>
-__global__ __launch_bounds__(THREADS) void quant_rows_kernel(QuantParams a)
+// The codes of a row's columns col .. col + 7 (m: the bits of its largest value, inv
+// about 127 / m); a row of zeros, or one that is not finite, has codes 0.
+__device__ __forceinline__ void put_codes(char *q, int col, const float (&g)[8], uint32_t m,
+                                          float inv)
+{
+    uint32_t w[2] = {0, 0};
+    if (m - 1u < kInfBits - 1u)
+        row_codes(g, inv, __uint_as_float(m), w);
+    *reinterpret_cast<uint2 *>(q + col) = uint2{w[0], w[1]};
+}
+__device__ __forceinline__ float row_scale(uint32_t m)
+{
+    return m < kInfBits ? __uint_as_float(m) / 127.0f : __builtin_nanf("");
+}
+
+// Rows of up to PER * 512 columns: a wave per row, the next row's loads on their way
+// while this row's codes are made (65536 rows of 768 bf16: a workgroup of four rows
+// without that 42 us).
+template <int DT, int PER>
+__global__ __launch_bounds__(kPackThreads) void quant_short_kernel(QuantParams a)
 {
     typedef typename Elem<DT>::store_t T;
-    constexpr int PER = 4;
+    constexpr int V = 8 / Elem<DT>::kPer16;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t step = (int64_t)gridDim.x * (kPackThreads / kWave);
+    typename Pack16<DT>::vec_t next[PER][V];
+    auto load = [&](int64_t row) {
+        const T *x = static_cast<const T *>(a.X) + row * a.ldx;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int col = (i * kWave + lane) * 8 + v * Elem<DT>::kPer16;
+                next[i][v] = typename Pack16<DT>::vec_t{};
+                if (col < a.K)
+                    next[i][v] = load16<DT>(x, col, a.K);
+            }
+    };
+    int64_t row = (int64_t)blockIdx.x * (kPackThreads / kWave) + threadIdx.x / kWave;
+    if (row < a.rows)
+        load(row);
+    for (; row < a.rows; row += step) {
+        float f[PER][8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                f[i][k] = Elem<DT>::widen(next[i][k / Elem<DT>::kPer16][k % Elem<DT>::kPer16]);
+            m = max(m, abs_max_bits(f[i]));
+        }
+        if (row + step < a.rows)
+            load(row + step);
+        m = wave_max(m);
+        const float inv = row_inverse(m);
+        if (lane == 0)
+            a.scales[row] = row_scale(m);
+        char *q = a.Q + row * a.Kq;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int col = (i * kWave + lane) * 8;
+            if (col < a.Kq)
+                put_codes(q, col, f[i], m, inv);
+        }
+    }
+}
+
+// Longer rows: a workgroup per row.  Its values stay in registers between the
+// maximum and the codes up to 8192 columns; the columns past that are read again.
+template <int DT>
+__global__ __launch_bounds__(kPackThreads) void quant_long_kernel(QuantParams a)
+{
+    typedef typename Elem<DT>::store_t T;
+    constexpr int PER = 4, THREADS = kPackThreads;
     __shared__ uint32_t s_max[THREADS / kWave];
     const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
     const T *x = static_cast<const T *>(a.X) + row * a.ldx;
     char *q = a.Q + row * a.Kq;
     float f[PER][8];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int col = (i * THREADS + (int)threadIdx.x) * 8;
+        const int col = (i * THREADS + tid) * 8;
         if (col < a.K) {
             load8f<DT>(x, col, a.K, f[i]);
             m = max(m, abs_max_bits(f[i]));
         }
     }
-    for (int col = (PER * THREADS + (int)threadIdx.x) * 8; col < a.K; col += THREADS * 8) {
+    for (int col = (PER * THREADS + tid) * 8; col < a.K; col += THREADS * 8) {
         float g[8];
         load8f<DT>(x, col, a.K, g);
         m = max(m, abs_max_bits(g));
     }
     m = wave_max(m);
-    if constexpr (THREADS > kWave) {
-        if (threadIdx.x % kWave == 0)
-            s_max[threadIdx.x / kWave] = m;
-        __syncthreads();
+    if (tid % kWave == 0)
+        s_max[tid / kWave] = m;
+    __syncthreads();
 #pragma unroll
-        for (int w = 0; w < THREADS / kWave; ++w)
-            m = max(m, s_max[w]);
-    }
-    const bool finite = m < kInfBits;
-    const float top = __builtin_bit_cast(float, m);
-    // 127 / m overflows for the smallest subnormals: the codes then come from
-    // the 64-bit quotient (t is infinite or NaN, and compares as no tie).
-    const float inv = 127.0f / top;
-    const bool narrow = !(inv < __builtin_inff());
-    if (threadIdx.x == 0)
-        a.scales[row] = finite ? top / 127.0f : __builtin_nanf("");
-    auto put = [&](int col, const float (&g)[8]) {
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            int c = 0;
-            if (finite && m != 0)
-                c = narrow ? (int)rint((double)g[i] * 127.0 / (double)top)
-                           : row_code(g[i], inv, top);
-            w[i / 4] |= (uint32_t)(c & 255) << (8 * (i % 4));
-        }
-        *reinterpret_cast<uint2 *>(q + col) = uint2{w[0], w[1]};
-    };
+    for (int w = 0; w < THREADS / kWave; ++w)
+        m = max(m, s_max[w]);
+    const float inv = row_inverse(m);
+    if (tid == 0)
+        a.scales[row] = row_scale(m);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int col = (i * THREADS + (int)threadIdx.x) * 8;
+        const int col = (i * THREADS + tid) * 8;
         if (col < a.K)
-            put(col, f[i]);
+            put_codes(q, col, f[i], m, inv);
         else if (col < a.Kq)
             *reinterpret_cast<uint2 *>(q + col) = uint2{0, 0};
     }
-    for (int col = (PER * THREADS + (int)threadIdx.x) * 8; col < a.Kq; col += THREADS * 8) {
+    for (int col = (PER * THREADS + tid) * 8; col < a.Kq; col += THREADS * 8) {
         float g[8] = {};
         if (col < a.K)
             load8f<DT>(x, col, a.K, g);
-        put(col, g);
+        put_codes(q, col, g, m, inv);
     }
 }
 
@@ -274,13 +352,16 @@ unsigned pack_grid(int64_t items)
 template <int DT>
 void quant_cfg(const QuantParams &p, hipStream_t stream)
 {
-    // A wave per row up to the columns it keeps in registers.
-    if (p.K <= kWave * 32)
-        hipLaunchKernelGGL((quant_rows_kernel<DT, kWave>), dim3((unsigned)p.rows), dim3(kWave), 0,
-                           stream, p);
+    const dim3 waves(pack_grid((p.rows + 3) / 4) < 2048u ? pack_grid((p.rows + 3) / 4) : 2048u);
+    const dim3 block(kPackThreads);
+    if (p.K <= kWave * 8)
+        hipLaunchKernelGGL((quant_short_kernel<DT, 1>), waves, block, 0, stream, p);
+    else if (p.K <= kWave * 16)
+        hipLaunchKernelGGL((quant_short_kernel<DT, 2>), waves, block, 0, stream, p);
+    else if (p.K <= kWave * 32)
+        hipLaunchKernelGGL((quant_short_kernel<DT, 4>), waves, block, 0, stream, p);
     else
-        hipLaunchKernelGGL((quant_rows_kernel<DT, 256>), dim3((unsigned)p.rows), dim3(256), 0,
-                           stream, p);
+        hipLaunchKernelGGL(quant_long_kernel<DT>, dim3((unsigned)p.rows), block, 0, stream, p);
 }
 
 }  // namespace
