@@ -39,6 +39,12 @@ CASES = [
     (300, 1, 2, 137, 261, "silu", False),
     (411, 2, 3, 200, 129, "silu", True),
     (640, 1, 1, 72, 128, "gelu", False),
+    # middle and large tiles in both directions
+    (500, 2, 3, 40, 2600, "silu", True),
+    (1500, 1, 2, 24, 4001, "gelu", False),
+    (1500, 1, 2, 48, 4000, "silu", True),
+    (1500, 1, 2, 24, 8043, "silu", False),
+    (1500, 1, 2, 40, 8040, "gelu", True),
 ]
 IDS = ["-".join(map(str, c)) for c in CASES]
 

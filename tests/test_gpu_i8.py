@@ -37,6 +37,12 @@ CASES = [
     (520, 2, 4, 144, 1026, "gated", "gelu", True),
     (400, 2, 4, 80, 264, "sorted", None, False),
     (90, 2, 4, 80, 264, "sorted", "silu", False),
+    # sizes that take middle tiles (up to 128 rows a tile) and large ones
+    (700, 2, 3, 64, 5000, "plain", None, False),
+    (700, 2, 3, 64, 4998, "gated", "gelu", True),
+    (1500, 1, 2, 48, 8008, "plain", None, False),
+    (1500, 1, 2, 48, 8002, "gated", "silu", False),
+    (1500, 1, 2, 48, 7704, "scattered", None, False),
 ]
 
 

@@ -1310,20 +1310,13 @@ size_t moegg_gated_bwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t
     return (size_t)padded_bytes((int64_t)num_tokens * topk, N, num_experts, N, I);
 }
 
-// Copies a bf16 operand whose rows are not whole aligned 16-byte chunks.
-static hipError_t pad_operand(const char **src, int64_t *ld, char *dst, const int32_t *m_sizes,
-                              int64_t groups, int64_t rows, int cols, int cus, hipStream_t stream)
+// Adds a bf16 operand whose rows are not whole aligned 16-byte chunks to the copies.
+static void pad_operand(moegg::PadParams *p, const char **src, int64_t *ld, char *dst,
+                        const int32_t *m_sizes, int64_t rows, int64_t group_rows, int cols)
 {
-    moegg::PadParams p;
-    p.src = *src;
-    p.dst = dst;
-    p.m_sizes = m_sizes;
-    p.groups = groups;
-    p.rows = rows;
-    p.cols = cols;
+    p->op[p->num++] = {*src, dst, m_sizes, rows, group_rows, cols};
     *src = dst;
     *ld = moegg::padded_row_bytes(cols);
-    return moegg::pad_rows_launch(p, cus, stream);
 }
 
 moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_sizes,
@@ -1346,8 +1339,8 @@ moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_size
         (st = check_kept(A, Aq, As, false)) != MOEGG_OK)
         return st;
     const int64_t x_rows = (flags & MOEGG_PERMUTE_X) ? num_tokens : S;
-    const int64_t pad = moegg::padded_row_bytes(K);
-    if (!fits(x_rows, pad, 1) || !fits(N, pad, 1))
+    const int64_t row = moegg::padded_row_bytes(K);
+    if (!fits(x_rows, row, 1) || !fits(N, row, 1))
         return MOEGG_ESHAPE;
     if (num_tokens == 0)
         return MOEGG_OK;
@@ -1390,13 +1383,13 @@ moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_size
     p.flags = flags;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    hipError_t e = hipSuccess;
+    moegg::PadParams pad = {};
     if (pad_x)
-        e = pad_operand(&p.X, &p.ldx, ws, nullptr, 1, x_rows, K, cus, hs);
-    if (e == hipSuccess && pad_w)
-        e = pad_operand(&p.W, &p.ldw, ws + padded_second(x_rows, K), m_sizes, num_experts, N, K,
-                        cus, hs);
-    if (e != hipSuccess)
+        pad_operand(&pad, &p.X, &p.ldx, ws, nullptr, x_rows, 1, K);
+    if (pad_w)
+        pad_operand(&pad, &p.W, &p.ldw, ws + padded_second(x_rows, K), m_sizes,
+                    (int64_t)num_experts * N, N, K);
+    if (pad.num && moegg::pad_rows_launch(pad, hs) != hipSuccess)
         return MOEGG_EHIP;
     return from_hip(moegg::gated_fwd_launch(p, cus, hs));
 }
@@ -1467,13 +1460,13 @@ moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_siz
     p.flags = flags;
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    hipError_t e = hipSuccess;
+    moegg::PadParams pad = {};
     if (pad_y)
-        e = pad_operand(&p.dY, &p.ldy, ws, nullptr, 1, S, N, cus, hs);
-    if (e == hipSuccess && pad_w)
-        e = pad_operand(&p.W, &p.ldw, ws + padded_second(S, N), m_sizes, num_experts, N, I, cus,
-                        hs);
-    if (e != hipSuccess)
+        pad_operand(&pad, &p.dY, &p.ldy, ws, nullptr, S, 1, N);
+    if (pad_w)
+        pad_operand(&pad, &p.W, &p.ldw, ws + padded_second(S, N), m_sizes,
+                    (int64_t)num_experts * N, N, I);
+    if (pad.num && moegg::pad_rows_launch(pad, hs) != hipSuccess)
         return MOEGG_EHIP;
     return from_hip(moegg::gated_bwd_launch(p, cus, hs));
 }

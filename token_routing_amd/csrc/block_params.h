@@ -88,14 +88,19 @@ struct UnpackRowsParams {
     int topk, E, cols;
 };
 
-// Rows of bf16 copied to rows of whole 16-byte chunks: `groups` groups of
-// `rows` rows; a group whose entry of m_sizes is not positive is left out.
-struct PadParams {
+// Rows of bf16 copied to rows of whole 16-byte chunks, for up to two operands in one
+// launch: `rows` rows of `cols` columns, in groups of `group_rows`; a group whose
+// entry of m_sizes is not positive is left out (m_sizes null: none).
+struct PadOperand {
     const char *src;
     char *dst;
-    const int32_t *m_sizes;  // or null
-    int64_t groups, rows;
+    const int32_t *m_sizes;
+    int64_t rows, group_rows;
     int cols;
+};
+struct PadParams {
+    PadOperand op[2];
+    int num;
 };
 inline int64_t padded_row_bytes(int64_t cols)
 {
@@ -119,6 +124,6 @@ hipError_t quant_rows_launch(const QuantParams &p, int dtype, hipStream_t stream
 hipError_t pack8_launch(const PackParams &p, int dtype, hipStream_t stream);
 hipError_t unpack8_launch(const PackParams &p, int dtype, hipStream_t stream);
 hipError_t unpack_rows_launch(const UnpackRowsParams &p, int cus, hipStream_t stream);
-hipError_t pad_rows_launch(const PadParams &p, int cus, hipStream_t stream);
+hipError_t pad_rows_launch(const PadParams &p, hipStream_t stream);
 
 }  // namespace moegg

@@ -328,17 +328,29 @@ __global__ __launch_bounds__(kPackThreads) void unpack_rows_kernel(UnpackRowsPar
 
 __global__ __launch_bounds__(kPackThreads) void pad_rows_kernel(PadParams a)
 {
-    const int cpr = (a.cols + 7) / 8;
-    const int64_t total = a.groups * a.rows;
-    // Whole groups without rows are passed over; a workgroup takes a row at a time.
-    for (int64_t r = blockIdx.x; r < total; r += gridDim.x) {
-        if (a.m_sizes && a.m_sizes[r / a.rows] <= 0)
-            continue;
-        const uint16_t *src = reinterpret_cast<const uint16_t *>(a.src) + r * a.cols;
-        uint16_t *dst = reinterpret_cast<uint16_t *>(a.dst) + r * cpr * 8;
-        for (int c = threadIdx.x; c < cpr; c += kPackThreads)
-            *reinterpret_cast<Pack16<kBf16>::vec_t *>(dst + c * 8) =
-                load16<kBf16>(src, c * 8, a.cols);
+    for (int o = 0; o < a.num; ++o) {
+        const PadOperand &p = a.op[o];
+        const uint32_t cpr = (uint32_t)((p.cols + 7) / 8);
+        const int64_t total = p.rows * cpr;
+        for (int64_t base = (int64_t)blockIdx.x * kPackThreads; base < total;
+             base += (int64_t)gridDim.x * kPackThreads) {
+            const int64_t r0 = base / cpr;
+            const uint32_t in = (uint32_t)(base - r0 * cpr) + threadIdx.x;
+            const int64_t row = r0 + in / cpr;
+            const int c = (int)(in % cpr);
+            if (row >= p.rows)
+                continue;
+            if (p.m_sizes) {
+                int64_t g = r0 / p.group_rows;  // uniform; a few rows may pass its end
+                while (row >= (g + 1) * p.group_rows)
+                    ++g;
+                if (p.m_sizes[g] <= 0)
+                    continue;
+            }
+            *reinterpret_cast<uint4 *>(p.dst + (row * cpr + c) * 16) = __builtin_bit_cast(
+                uint4, load16<kBf16>(reinterpret_cast<const uint16_t *>(p.src) + row * p.cols,
+                                     c * 8, p.cols));
+        }
     }
 }
 
@@ -411,12 +423,13 @@ hipError_t unpack_rows_launch(const UnpackRowsParams &p, int cus, hipStream_t st
     return hipGetLastError();
 }
 
-hipError_t pad_rows_launch(const PadParams &p, int cus, hipStream_t stream)
+hipError_t pad_rows_launch(const PadParams &p, hipStream_t stream)
 {
-    const int64_t rows = p.groups * p.rows;
-    hipLaunchKernelGGL(pad_rows_kernel,
-                       dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(rows, cus * 16))),
-                       dim3(kPackThreads), 0, stream, p);
+    int64_t items = 1;
+    for (int o = 0; o < p.num; ++o)
+        items = std::max(items, (p.op[o].rows * ((p.op[o].cols + 7) / 8) + kPackThreads - 1) /
+                                    kPackThreads);
+    hipLaunchKernelGGL(pad_rows_kernel, dim3(pack_grid(items)), dim3(kPackThreads), 0, stream, p);
     return hipGetLastError();
 }
 
