@@ -669,8 +669,8 @@ size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, in
  *           aligned; columns from K on are zeros.
  *   scales  out [rows] fp32.
  * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  Errors:
- * ESHAPE for rows < 0 or past 2^24 - 1, K < 1, ldx < K, sizes past 2^40
- * bytes; EINVAL for an unknown dtype, NULL or misaligned pointers.
+ * ESHAPE for rows < 0 or past 2^24 - 1, K < 1 or past 2^30, ldx < K, sizes
+ * past 2^40 bytes; EINVAL for an unknown dtype, NULL or misaligned pointers.
  */
 moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t K,
                               int8_t *Q, float *scales, void *stream);
@@ -691,9 +691,9 @@ moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t
  *             the padded row length Kq, a multiple of 16.  Any int8 value.
  *   others    as in the forward; 2 GiB at most for Xq and for one expert's Wq.
  * Rows at positions past the sum of m_sizes are left as they were.  T = 0 is a
- * no-op.  Errors: as the forward, and ESHAPE for K not a multiple of 16 or past
- * MOEGG_MAX_I8_K, Xq or Wq not 16-byte aligned; EINVAL for both activations, or
- * HALVES without one.
+ * no-op.  Y overlaps no input.  Errors: as the forward, and ESHAPE for K not a multiple of 16 or past
+ * MOEGG_MAX_I8_K, Xq or Wq not 16-byte aligned; EINVAL for both activations,
+ * HALVES without one, or an overlap.
  */
 moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, const int8_t *Wq,
                                    const float *w_scales, const int32_t *m_sizes,
@@ -716,8 +716,8 @@ moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, cons
  *           16-byte aligned; codes from cols on are 0.
  *   scales  out [rows, Cp / 32], the bytes b.
  * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  Errors:
- * ESHAPE for rows < 0, cols < 1, ldx < cols, sizes past 2^40 bytes; EINVAL for
- * an unknown dtype, NULL or misaligned pointers.
+ * ESHAPE for rows < 0, cols < 1 or past 2^30, ldx < cols, sizes past 2^40
+ * bytes; EINVAL for an unknown dtype, NULL or misaligned pointers.
  */
 moegg_status moegg_pack8(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t cols,
                          int8_t *Q, uint8_t *scales, void *stream);
@@ -751,9 +751,10 @@ moegg_status moegg_unpack8(const int8_t *Q, const uint8_t *scales, int64_t rows,
  *          needed when K is not a multiple of 8 or X or W is not 16-byte
  *          aligned; else may be NULL.  No initialisation.
  * Rows at positions past the sum of m_sizes are left as they were.  T = 0 is a
- * no-op.  Errors: EINVAL for flags other than these, none or both activations,
- * Aq without As (or As without Aq, or A beside them), NULL or misaligned
- * pointers; ESHAPE for sizes as in the forward, I < 1; EWORKSPACE.
+ * no-op.  Outputs and the workspace overlap no input and not each other; a
+ * workspace serves one call at a time.  Errors: EINVAL for flags other than
+ * these, none or both activations, Aq without As (or As without Aq, or A beside
+ * them), NULL or misaligned pointers, an overlap; ESHAPE for sizes as in the forward, I < 1; EWORKSPACE.
  */
 moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_sizes,
                              const int32_t *gather_idx, int32_t num_tokens, int32_t topk,
@@ -785,8 +786,8 @@ size_t moegg_gated_fwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t
  *         bytes: needed when N or I is not a multiple of 8 or dY or W is not
  *         16-byte aligned.
  * Rows of dA and H at positions past the sum of m_sizes, and rows whose gather
- * entry is bad, are left as they were.  T = 0 is a no-op.  Errors as
- * moegg_gated_fwd; exactly one of A and (Aq, As) is given (EINVAL).
+ * entry is bad, are left as they were.  T = 0 is a no-op.  Overlaps and errors
+ * as moegg_gated_fwd, dA over A excepted; exactly one of A and (Aq, As) is given (EINVAL).
  */
 moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_sizes,
                              const int32_t *gather_idx, const void *A, const int8_t *Aq,
@@ -808,6 +809,7 @@ size_t moegg_gated_bwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t
  * else, the split of hot experts among it, as moegg_grouped_gemm_dW.
  *   workspace  device, 16-byte aligned, required:
  *              moegg_grouped_gemm_dW_packed_workspace_bytes(...) bytes.
+ * dW and the workspace overlap no input and not each other (EINVAL).
  */
 moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_scales,
                                           const void *dY, const int32_t *m_sizes,

@@ -200,3 +200,24 @@ def test_binding_refuses():
         mg.gated_fwd(cpu, torch.zeros(1, 3, 8, dtype=torch.bfloat16), None, None, 1, 32)
     with pytest.raises(ValueError):
         mg.gated_fwd(cpu, torch.zeros(1, 4, 8, dtype=torch.bfloat16), None, None, 1, 32, keep="int8")
+
+
+@pytest.mark.parametrize("call,kw,want", [
+    (quant, dict(K=(1 << 30) + 1, ld=1 << 31), ESHAPE),
+    (pack, dict(cols=(1 << 30) + 1, ld=1 << 31), ESHAPE),
+    (unpack, dict(cols=(1 << 30) + 1, ld=1 << 31), ESHAPE),
+    (i8, dict(Y=at(5)), EINVAL), (i8, dict(Y=at(6)), EINVAL),
+    (i8, dict(Y=at(8), flags=PY | MUL, w=at(8)), EINVAL),
+    (fwd, dict(H=at(3)), EINVAL), (fwd, dict(A=at(4)), EINVAL),
+    (fwd, dict(Aq=at(4, 16), As=at(7)), EINVAL),
+    (bwd, dict(dA=at(3)), EINVAL), (bwd, dict(H=at(4), flags=PY | SILU), EINVAL),
+    (bwd, dict(N=63, ws=at(4), n=1 << 30, flags=PY | SILU), EINVAL),
+    (dw, dict(out=at(4)), EINVAL), (dw, dict(ws=at(5)), EINVAL),
+])
+def test_far_columns_and_index_overlaps(lib, call, kw, want):
+    assert call(lib, **kw) == want
+
+
+def test_workspace_of_negative_sizes(lib):
+    assert lib.moegg_gated_fwd_workspace_bytes(10, 2, 4, -2**31, 64, PX) == 0
+    assert lib.moegg_gated_bwd_workspace_bytes(10, 2, 4, 64, -2**31) == 0

@@ -1104,10 +1104,12 @@ moegg_status moegg_lora_bwd(const void *X, int64_t ldx, const void *dY, int64_t 
 
 constexpr int64_t kMaxBytes = (int64_t)1 << 40;
 
-// Rows of K values of `dtype`, ld apart.
+// Rows of K values of `dtype`, ld apart.  K is held so that a column past it by a
+// workgroup's step is still an int.
+constexpr int32_t kMaxValues = 1 << 30;
 static moegg_status check_values(const void *X, int32_t dtype, int64_t ld, int64_t rows, int32_t K)
 {
-    if (rows < 0 || rows > INT32_MAX || K < 1 || ld < K || ld > kMaxBytes / 4 / (rows + 1))
+    if (rows < 0 || rows > INT32_MAX || K < 1 || K > kMaxValues || ld < K || ld > kMaxBytes / 4 / (rows + 1))
         return MOEGG_ESHAPE;
     if (!known_dtype(dtype))
         return MOEGG_EINVAL;
@@ -1139,9 +1141,7 @@ moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t
     p.scales = scales;
     p.rows = rows;
     p.K = K;
-    p.Kq = (int)(((int64_t)K + 15) / 16 * 16);
-    if (p.Kq < K)
-        return MOEGG_ESHAPE;
+    p.Kq = (K + 15) / 16 * 16;
     const Span outs[] = {{Q, rows * p.Kq}, {scales, rows * 4}};
     const Span ins[] = {values_span(X, dtype, ldx, rows, K)};
     if (outputs_meet(outs, ins))
@@ -1159,8 +1159,6 @@ static moegg_status pack_params(const void *X, int32_t dtype, int64_t ldx, int64
     if (!Q || !scales || !aligned16(Q))
         return MOEGG_EINVAL;
     const int64_t Cp = moegg::packed_cols(cols);
-    if (Cp > INT32_MAX)
-        return MOEGG_ESHAPE;
     const Span x = values_span(X, dtype, ldx, rows, cols);
     const Span q = {Q, rows * Cp}, s = {scales, rows * (Cp / moegg::kPackBlock)};
     if (meet(x, q) || meet(x, s) || (pack && meet(q, s)))
@@ -1246,7 +1244,9 @@ moegg_status moegg_grouped_gemm_i8(const int8_t *Xq, const float *x_scales, cons
     const Span outs[] = {{Y, S * (gated ? N / 2 : N) * 2}};
     const Span ins[] = {{Xq, x_rows * K}, {x_scales, x_rows * 4},
                         {Wq, (int64_t)num_experts * N * K},
-                        {w_scales, (int64_t)num_experts * N * 4}};
+                        {w_scales, (int64_t)num_experts * N * 4},
+                        {m_sizes, (int64_t)num_experts * 4}, {gather_idx, S * 4},
+                        {topk_weights, S * 4}};
     if (outputs_meet(outs, ins))
         return MOEGG_EINVAL;
     int cus = 0;
@@ -1295,7 +1295,7 @@ static int64_t padded_bytes(int64_t rows, int64_t cols, int64_t groups, int64_t 
 size_t moegg_gated_fwd_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts,
                                        int32_t I, int32_t K, uint32_t flags)
 {
-    if (I > INT32_MAX / 2 ||
+    if (I < 1 || I > INT32_MAX / 2 ||
         check_gemm_common(num_tokens, topk, num_experts, 2 * I, K) != MOEGG_OK)
         return 0;
     const int64_t rows = (int64_t)num_tokens * ((flags & MOEGG_PERMUTE_X) ? 1 : topk);
@@ -1358,7 +1358,8 @@ moegg_status moegg_gated_fwd(const void *X, const void *W, const int32_t *m_size
     const Span outs[] = {{H, S * I * 2}, {A, S * N * 2}, {Aq, S * 2 * Ip},
                          {As, S * 2 * Ip / moegg::kPackBlock},
                          {workspace, pad_x || pad_w ? need : 0}};
-    const Span ins[] = {{X, x_rows * K * 2}, {W, (int64_t)num_experts * N * K * 2}};
+    const Span ins[] = {{X, x_rows * K * 2}, {W, (int64_t)num_experts * N * K * 2},
+                        {m_sizes, (int64_t)num_experts * 4}, {gather_idx, S * 4}};
     if (outputs_meet(outs, ins))
         return MOEGG_EINVAL;
     int cus = 0;
@@ -1433,7 +1434,8 @@ moegg_status moegg_gated_bwd(const void *dY, const void *W, const int32_t *m_siz
                          {workspace, pad_y || pad_w ? need : 0}};
     const Span ins[] = {{dY, S * N * 2}, {W, (int64_t)num_experts * N * I * 2},
                         {A == dA ? nullptr : A, S * I * 4}, {Aq, S * 2 * Ip},
-                        {As, S * 2 * Ip / moegg::kPackBlock}};
+                        {As, S * 2 * Ip / moegg::kPackBlock},
+                        {m_sizes, (int64_t)num_experts * 4}, {gather_idx, S * 4}};
     if (outputs_meet(outs, ins))
         return MOEGG_EINVAL;
     int cus = 0;
@@ -1541,7 +1543,7 @@ moegg_status moegg_grouped_gemm_dW_packed(const int8_t *Xq, const uint8_t *x_sca
     const int64_t Cp = moegg::packed_cols(K);
     const Span outs[] = {{dW, (int64_t)num_experts * N * K * (fp32 ? 4 : 2)}, {workspace, need}};
     const Span ins[] = {{Xq, x_rows * Cp}, {x_scales, x_rows * Cp / moegg::kPackBlock},
-                        {dY, S * N * 2}};
+                        {dY, S * N * 2}, {m_sizes, (int64_t)num_experts * 4}, {gather_idx, S * 4}};
     if (outputs_meet(outs, ins))
         return MOEGG_EINVAL;
     int cus = 0;

@@ -38,6 +38,9 @@
 
 namespace moegg {
 
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
 constexpr int BK = 64;
 constexpr int kChunks = BK / 8;  // 16-byte chunks per LDS row
 
