@@ -275,15 +275,15 @@ def time_step(st, steps, warmup, min_warm_s=0.0):
 
 def kernel_source_sha(label=None):
     """sha256[:16] of the sources a kernel is built from (all kernels' when
-    label is None): the shared headers plus the kernel's own file."""
+    label is None): the shared headers plus the kernel's own files."""
     if label is None:
-        own = ("gemm.hip", "route.hip", "combine.hip")
+        own = ("gemm.hip", "gemm_engine.h", "route.hip", "combine.hip")
     elif label.startswith("combine"):
         own = ("combine.hip",)
     elif label.startswith("route"):
         own = ("route.hip",)
     else:
-        own = ("gemm.hip",)
+        own = ("gemm.hip", "gemm_engine.h")
     h = hashlib.sha256()
     for f in own + ("common.h", "gemm_params.h"):
         with open(os.path.join(ROOT, "token_routing_amd", "csrc", f), "rb") as fh:
