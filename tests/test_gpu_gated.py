@@ -39,6 +39,10 @@ CASES = [
     (300, 1, 2, 137, 261, "silu", False),
     (411, 2, 3, 200, 129, "silu", True),
     (640, 1, 1, 72, 128, "gelu", False),
+    # few rows, reductions of several waves
+    (6, 2, 6, 1032, 70, "silu", True),
+    (4, 1, 2, 2056, 33, "gelu", False),
+    (9, 1, 5, 1500, 21, "silu", False),
     # middle and large tiles in both directions
     (500, 2, 3, 40, 2600, "silu", True),
     (1500, 1, 2, 24, 4001, "gelu", False),

@@ -37,6 +37,15 @@ CASES = [
     (520, 2, 4, 144, 1026, "gated", "gelu", True),
     (400, 2, 4, 80, 264, "sorted", None, False),
     (90, 2, 4, 80, 264, "sorted", "silu", False),
+    # few rows: one to four of an expert at a time, reductions of parts and of several waves
+    (1, 8, 128, 768, 256, "scattered", None, False),
+    (1, 2, 4, 2064, 37, "plain", None, False),
+    (6, 2, 6, 2064, 37, "plain", None, False),
+    (3, 2, 4, 1040, 50, "gated", "silu", True),
+    (7, 1, 5, 2096, 134, "gated", "gelu", False),
+    (9, 2, 16, 2048, 130, "scattered", None, False),
+    (4, 1, 1, 4112, 18, "sorted", "silu", False),
+    (33, 1, 17, 1024, 65, "sorted", None, False),
     # sizes that take middle tiles (up to 128 rows a tile) and large ones
     (700, 2, 3, 64, 5000, "plain", None, False),
     (700, 2, 3, 64, 4998, "gated", "gelu", True),
@@ -163,6 +172,33 @@ def test_bad_device_data(mg):
     mg.grouped_gemm_i8(xq, xs, wq, ws, sizes, r["gather"], None, k, mg.PERMUTE_X, Y=y,
                        error_flags=err)
     assert int(err) & mg.DERR_M_SIZES
+
+
+def test_bad_gather_of_few_rows(mg):
+    """As above where experts have one to three rows."""
+    T, k, E, K, N = 4, 2, 4, 1040, 22
+    r, order, experts, g = routed(mg, T, k, E, 6, drop=False)
+    xq = torch.randint(-5, 6, (T, K), generator=g, dtype=torch.int8).cuda()
+    wq = torch.randint(-5, 6, (E, N, K), generator=g, dtype=torch.int8).cuda()
+    xs, ws = torch.ones(T, device="cuda"), torch.ones(E, N, device="cuda")
+    for flags, cols in ((mg.PERMUTE_X, N), (mg.PERMUTE_X | mg.GATED_SILU, N // 2)):
+        good = mg.grouped_gemm_i8(xq, xs, wq, ws, r["m_sizes"], r["gather"], None, k, flags)
+        gather = r["gather"].clone()
+        gather[1], gather[6] = -1, T * k
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        y = torch.full_like(good, 5.0)
+        mg.grouped_gemm_i8(xq, xs, wq, ws, r["m_sizes"], gather, None, k, flags, Y=y,
+                           error_flags=err)
+        assert int(err) == mg.DERR_GATHER and y.shape[1] == cols
+        keep = torch.ones(T * k, dtype=torch.bool, device="cuda")
+        keep[[1, 6]] = False
+        assert torch.equal(y[keep], good[keep]) and (y[~keep] == 5).all()
+        err.zero_()
+        sizes = r["m_sizes"].clone()
+        sizes[0] = -3
+        mg.grouped_gemm_i8(xq, xs, wq, ws, sizes, r["gather"], None, k, flags, Y=y,
+                           error_flags=err)
+        assert int(err) & mg.DERR_M_SIZES
 
 
 def test_no_tokens(mg):

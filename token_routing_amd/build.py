@@ -33,7 +33,7 @@ FLAGS = [
 ]
 
 SOURCES = ["route.hip", "gemm.hip", "generic.hip", "combine.hip", "gate.hip", "sort.hip",
-           "lora.hip", "block_i8.hip", "block_silu.hip", "block_gelu.hip", "block_bwd.hip",
+           "lora.hip", "block_i8.hip", "block_silu.hip", "block_gelu.hip", "block_bwd.hip", "block_vec.hip",
            "pack.hip", "api.hip"]
 
 

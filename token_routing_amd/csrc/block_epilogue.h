@@ -54,6 +54,9 @@ __device__ __forceinline__ void row_cols(const f32x16_t &acc, uint32_t (&v)[16])
         }
 }
 
+// The output: columns as they are, or gated by one of the activations.
+constexpr int kPlain = 0, kSilu = 1, kGelu = 2;
+
 // act(g) = g sigmoid(z(g)): z = g for silu, and 2 sqrt(2 / pi) (g + 0.044715 g^3) for
 // gelu's tanh form, since (1 + tanh y) / 2 = sigmoid(2 y).  sigmoid(z) = 1 / (1 +
 // 2^(-z log2 e)) by v_exp_f32 and v_rcp_f32, good to an ulp each, far below the

@@ -25,8 +25,6 @@ __device__ __forceinline__ int block_w_row(int n0, int r, int N, bool halves)
 
 // What a gated call keeps of its pre-activations.
 constexpr int kKeepNone = 0, kKeepBf16 = 1, kKeepPacked = 2;
-// The output: columns as they are, or gated by one of the activations.
-constexpr int kPlain = 0, kSilu = 1, kGelu = 2;
 
 template <class C, int ACT, int KEEP, bool TAIL>
 __global__ __launch_bounds__(C::NT) void block_fwd_kernel(BlockFwdParams a)

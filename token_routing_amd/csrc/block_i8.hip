@@ -34,6 +34,8 @@ static void i8_tail(const BlockFwdParams &p, int cus, hipStream_t stream)
 
 hipError_t i8_launch(const BlockFwdParams &p, int cus, hipStream_t stream)
 {
+    if (block_vec_pays(p, cus))
+        return block_vec_launch(p, cus, stream);
     const int cols = p.flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU) ? p.N / 2 : p.N;
     if (cols % 8)
         i8_tail<true>(p, cus, stream);

@@ -107,12 +107,17 @@ inline int64_t padded_row_bytes(int64_t cols)
     return (cols + 7) / 8 * 16;
 }
 
+// Whether rows of one expert are so few that vectors beat tiles, and that launch.
+bool block_vec_pays(const BlockFwdParams &p, int cus);
+hipError_t block_vec_launch(const BlockFwdParams &p, int cus, hipStream_t stream);
 hipError_t i8_launch(const BlockFwdParams &p, int cus, hipStream_t stream);
 // The two activations, compiled apart.
 void gated_fwd_silu(const BlockFwdParams &p, int cus, hipStream_t stream);
 void gated_fwd_gelu(const BlockFwdParams &p, int cus, hipStream_t stream);
 inline hipError_t gated_fwd_launch(const BlockFwdParams &p, int cus, hipStream_t stream)
 {
+    if (!p.A && !p.Aq && block_vec_pays(p, cus))
+        return block_vec_launch(p, cus, stream);
     if (p.flags & MOEGG_GATED_GELU)
         gated_fwd_gelu(p, cus, stream);
     else
