@@ -187,7 +187,8 @@ enum Shape { kSmallTiles, kMidTiles, kBigTiles };
 //           rows 318 us (middle 362, small 690), of 128 rows 85 (66, 140).
 // 256 x 128 and 128 x 256 tiles with 32-deep stages, two workgroups a unit, lose to
 // both (8192 rows of 4096 int8 into 28672 1.19 ms, large 0.98; 65536 of 768 into
-// 2048 248 us, large 236).  Swept over 1, 8 and 60 experts of 16 to 1024 rows and 512 to 8192 columns.
+// 2048 248 us, large 236).  Swept over 1, 8 and 60 experts of 16 to 1024 rows and 512
+// to 8192 columns.
 inline Shape tile_shape(int64_t S, int E, int cols, int small_cols, double most_small, int cus)
 {
     auto rounds = [&](int64_t bm, int64_t bn, int a_round) {
