@@ -43,6 +43,10 @@ CASES = [
     (6, 2, 6, 1032, 70, "silu", True),
     (4, 1, 2, 2056, 33, "gelu", False),
     (9, 1, 5, 1500, 21, "silu", False),
+    # middle tiles with four stages
+    (900, 2, 3, 72, 500, "silu", True),
+    (1001, 3, 9, 603, 517, "gelu", False),
+    (950, 2, 1, 640, 520, "silu", False),
     # middle and large tiles in both directions
     (500, 2, 3, 40, 2600, "silu", True),
     (1500, 1, 2, 24, 4001, "gelu", False),

@@ -46,6 +46,9 @@ CASES = [
     (9, 2, 16, 2048, 130, "scattered", None, False),
     (4, 1, 1, 4112, 18, "sorted", "silu", False),
     (33, 1, 17, 1024, 65, "sorted", None, False),
+    # middle tiles with four stages
+    (900, 2, 3, 1152, 1001, "scattered", None, False),
+    (900, 2, 3, 96, 1002, "gated", "silu", True),
     # sizes that take middle tiles (up to 128 rows a tile) and large ones
     (700, 2, 3, 64, 5000, "plain", None, False),
     (700, 2, 3, 64, 4998, "gated", "gelu", True),

@@ -236,6 +236,7 @@ __global__ __launch_bounds__(C::NT) void gated_bwd_kernel(GatedBwdParams a)
 
 using BwdBigCfg = RingCfg<256, 256, 2, 4, false, 64, 2>;
 using BwdMidCfg = RingCfg<128, 128, 2, 2, false, 64, 2>;
+using BwdDeepCfg = RingCfg<128, 128, 2, 2, false, 64, 4>;
 using BwdSmallCfg = RingCfg<32, 128, 1, 4, false, 64, 4>;
 
 template <class C, bool GELU, bool PACKED, bool TAIL>
@@ -256,6 +257,8 @@ static void gated_bwd_rows(const GatedBwdParams &p, int cus, hipStream_t stream)
         gated_bwd_cfg<BwdSmallCfg, GELU, PACKED, TAIL>(p, cus, stream);
     else if (shape == kMidTiles)
         gated_bwd_cfg<BwdMidCfg, GELU, PACKED, TAIL>(p, cus, stream);
+    else if (shape == kDeepTiles)
+        gated_bwd_cfg<BwdDeepCfg, GELU, PACKED, TAIL>(p, cus, stream);
     else
         gated_bwd_cfg<BwdBigCfg, GELU, PACKED, TAIL>(p, cus, stream);
 }

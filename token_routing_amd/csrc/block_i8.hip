@@ -5,6 +5,7 @@ namespace moegg {
 
 using I8BigCfg = RingCfg<256, 256, 2, 4, true, 64, 2>;
 using I8MidCfg = RingCfg<128, 128, 2, 2, true, 64, 2>;
+using I8DeepCfg = RingCfg<128, 128, 2, 2, true, 64, 4>;
 using I8SmallCfg = RingCfg<32, 128, 1, 4, true, 64, 4>;
 using I8SmallGatedCfg = RingCfg<32, 256, 1, 4, true, 64, 4>;
 
@@ -17,6 +18,8 @@ static void i8_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
         block_fwd_cfg<Small, ACT, kKeepNone, TAIL>(p, cus, stream);
     else if (shape == kMidTiles)
         block_fwd_cfg<I8MidCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
+    else if (shape == kDeepTiles)
+        block_fwd_cfg<I8DeepCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
     else
         block_fwd_cfg<I8BigCfg, ACT, kKeepNone, TAIL>(p, cus, stream);
 }

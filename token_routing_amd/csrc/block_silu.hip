@@ -5,6 +5,7 @@ namespace moegg {
 
 using GatedBigCfg = RingCfg<256, 256, 4, 2, false, 64, 2>;
 using GatedMidCfg = RingCfg<128, 128, 2, 2, false, 64, 2>;
+using GatedDeepCfg = RingCfg<128, 128, 2, 2, false, 64, 4>;
 using GatedSmallCfg = RingCfg<32, 256, 1, 4, false, 64, 4>;
 
 template <int ACT, int KEEP, bool TAIL>
@@ -15,6 +16,8 @@ static void gated_rows(const BlockFwdParams &p, int cus, hipStream_t stream)
         block_fwd_cfg<GatedSmallCfg, ACT, KEEP, TAIL>(p, cus, stream);
     else if (shape == kMidTiles)
         block_fwd_cfg<GatedMidCfg, ACT, KEEP, TAIL>(p, cus, stream);
+    else if (shape == kDeepTiles)
+        block_fwd_cfg<GatedDeepCfg, ACT, KEEP, TAIL>(p, cus, stream);
     else
         block_fwd_cfg<GatedBigCfg, ACT, KEEP, TAIL>(p, cus, stream);
 }
