@@ -68,6 +68,20 @@ def test_quant_rows_ties_in_64_bits(mg):
     assert np.array_equal(q.cpu().numpy(), np.rint(127 * v / np.abs(v).max(1)[:, None]))
 
 
+def test_quant_rows_largest(mg):
+    """Rows whose 127 / m is below fp32's normal numbers, or just above."""
+    g = torch.Generator().manual_seed(9)
+    m = torch.exp2(torch.rand(600, 1, generator=g, dtype=torch.float64) * 3 + 124.999).float()
+    x = torch.cat([m, (torch.rand(600, 63, generator=g) * 2 - 1) * m], 1)
+    k = torch.randint(0, 127, (600, 32), generator=g).double() + 0.5
+    x[:, 32:] = (k * m.double() / 127).float()
+    assert torch.isfinite(x).all()
+    q, s = mg.quant_rows(x.cuda())
+    v = f64(x)
+    assert np.array_equal(q.cpu().numpy(), np.rint(127 * v / np.abs(v).max(1)[:, None]))
+    assert np.array_equal(s.cpu().numpy(), np.abs(x.numpy()).max(1) / np.float32(127))
+
+
 def test_quant_rows_far_values(mg):
     x = torch.zeros(8, 40)
     x[0, 3], x[0, 4] = 3.4028234e38, -1.7e38

@@ -60,32 +60,33 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m)
     return max(h[0], h[1]);
 }
 
-// About 127 / m: v_rcp_f32 is good to an ulp, the product to half a one.  0 or
-// infinite where it leaves fp32's normal numbers.
+// About 127 / m: v_rcp_f32 is good to an ulp, the product to half a one (where both are
+// normal numbers).
 __device__ __forceinline__ float row_inverse(uint32_t m)
 {
     return 127.0f * __builtin_amdgcn_rcpf(__uint_as_float(m));
 }
 
-// round(127 x / m) of real numbers, ties to even, for 8 values, as bytes.  t = x * inv
-// is within 127 * 2^-22 of the quotient, and adding 1.5 * 2^23 leaves its rounding
-// in the low byte.  Where a t comes so near to a tie that the rounding is open (or
-// inv is no number to use), the quotients are taken in 64 bits: 127 x is exact there
-// (31 bits), and a quotient of at least 1/2 by a number of 24 bits is either a tie or
-// at least 2^-34 away from one.
+// round(127 x / m) of real numbers, ties to even, for 8 values, as bytes.  x times a
+// number just below 127 / m and x times one just above it (2^-21 beside inv, which is
+// within 1.5 * 2^-23) are rounded by adding 1.5 * 2^23 in an fma, which leaves the whole
+// number in the low byte: where both give the same, the quotient between them does.
+// Else it is so near to a tie that the rounding is open, and the quotients are taken in
+// 64 bits, as where inv is no number to use: 127 x is exact there (31 bits), and a
+// quotient of at least 1/2 by a number of 24 bits is either a tie or at least 2^-34
+// away from one.
 __device__ __forceinline__ void row_codes(const float (&x)[8], float inv, float m,
                                           uint32_t (&w)[2])
 {
-    constexpr float kRound = 12582912.0f;
-    uint32_t c[8];
-    float open = 0.0f;
+    constexpr float kRound = 12582912.0f, kStep = 0x1p-21f;
+    const float lo = inv * (1.0f - kStep), hi = inv * (1.0f + kStep);
+    uint32_t c[8], open = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = x[i] * inv, r = t + kRound;
-        c[i] = __float_as_uint(r);
-        open = fmaxf(open, fabsf(t - (r - kRound)));
+        c[i] = __float_as_uint(__builtin_fmaf(x[i], lo, kRound));
+        open = (c[i] ^ __float_as_uint(__builtin_fmaf(x[i], hi, kRound))) + open;
     }
-    if (open > 0.49996f || !(inv > 0.0f && inv < __builtin_inff())) {
+    if (open != 0 || !(inv > 127.0f * 0x1p-126f && hi < __builtin_inff())) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             c[i] = (uint32_t)(int)rint((double)x[i] * 127.0 / (double)m);
@@ -94,6 +95,31 @@ __device__ __forceinline__ void row_codes(const float (&x)[8], float inv, float 
     for (int h = 0; h < 2; ++h)
         w[h] = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0c0c0400u) |
                __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x04000c0cu);
+}
+
+// The fp32 bits of the largest magnitude among 8 values as they stand in memory.  16-bit
+// types are compared as they are, two at a time.
+template <int DT, int V>
+__device__ __forceinline__ uint32_t raw_max_bits(const typename Pack16<DT>::vec_t (&v)[V])
+{
+    if constexpr (DT == kFp32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                m = max(m, __float_as_uint(v[i][k]) & kAbsBits);
+        return m;
+    } else {
+        typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+        typedef uint32_t words_t __attribute__((ext_vector_type(4)));
+        const words_t w = __builtin_bit_cast(words_t, v[0]);
+        u16x2_t m = __builtin_bit_cast(u16x2_t, w[0] & 0x7fff7fffu);
+#pragma unroll
+        for (int k = 1; k < 4; ++k)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[k] & 0x7fff7fffu));
+        return __float_as_uint(Elem<DT>::widen(max(m[0], m[1])));
+    }
 }
 
 }  // namespace
@@ -147,7 +173,7 @@ __global__ __launch_bounds__(kPackThreads) void quant_short_kernel(QuantParams a
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 f[i][k] = Elem<DT>::widen(next[i][k / Elem<DT>::kPer16][k % Elem<DT>::kPer16]);
-            m = max(m, abs_max_bits(f[i]));
+            m = max(m, raw_max_bits<DT>(next[i]));
         }
         if (row + step < a.rows)
             load(row + step);
