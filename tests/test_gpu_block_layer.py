@@ -200,3 +200,45 @@ def test_given_buffers(mg):
         args = (xq, xs, d[0], r["m_sizes"], r["gather"], k, mg.PERMUTE_X)
         assert torch.equal(mg.grouped_gemm_dW_packed(*args, K=K, workspace=ws3),
                            mg.grouped_gemm_dW_packed(*args, K=K))
+
+
+@pytest.mark.parametrize("T", [4, 32])
+def test_graph_of_few_tokens(mg, T):
+    """A serving step of a few rows an expert, replayed for other tokens and other experts:
+    nothing of the capture's routing stays."""
+    layer = Layer(mg, T=T, E=16 if T > 4 else 4, K=1024, I=256, seed=12)
+    layer.serve()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = layer.serve()
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed)
+        ids = torch.randint(0, layer.E, (T, layer.k), generator=g, dtype=torch.int32)
+        if seed == 1:
+            ids[:] = 3                                   # one expert for all
+        if seed == 2:
+            ids[1:] = -1                                 # one token, the others dropped
+        layer.ids.copy_(ids)
+        layer.x.copy_(torch.randn(T, layer.K, generator=g).bfloat16())
+        want = layer.serve()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+        live = ids.reshape(-1).numpy() >= 0
+        got = f64(outs[0])
+        assert (np.abs(got[live]).max(1) > 0).all() and (got[~live] == 0).all()
+
+
+def test_few_rows_on_two_streams(mg):
+    layers = [Layer(mg, T=4, K=1024, I=256, seed=13), Layer(mg, T=5, K=2048, I=128, seed=14)]
+    want = [x.serve() for x in layers]
+    torch.cuda.synchronize()
+    got = []
+    for layer, s in zip(layers, [torch.cuda.Stream(), torch.cuda.Stream()]):
+        with torch.cuda.stream(s):
+            got.append([layer.serve() for _ in range(3)][-1])
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0])
