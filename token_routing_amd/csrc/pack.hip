@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m)
 }
 
 // Over the wave: rotations inside the rows of 16 lanes, then exchanges of rows and
-// halves, registers all (six shuffles through LDS: 65536 rows of 768 bf16 46 us).
+// halves, registers all (six shuffles through LDS cost 65536 rows 4 us).
 __device__ __forceinline__ uint32_t wave_max(uint32_t m)
 {
     m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xf, 0xf, false));
@@ -139,55 +139,51 @@ __device__ __forceinline__ float row_scale(uint32_t m)
     return m < kInfBits ? __uint_as_float(m) / 127.0f : __builtin_nanf("");
 }
 
-// Rows of up to PER * 512 columns: a wave per row, the next row's loads on their way
-// while this row's codes are made.  Bound by memory (65536 rows of 768 bf16: 41.5 us,
-// 3.6 TB/s read and written together) or by the launch (a token of 1024: 2.4 us).
-template <int DT, int PER>
+// Rows of up to PER * 512 columns: a wave for each.  TAIL: K is not a multiple of 8.
+// 65536 rows of bf16: of 768 42.7 us (3.5 TB/s read and written, where a row costs as much as
+// one of 1024), of 1024 42.7 (4.7), of 512 26.9 (3.8); a token of 1024 2.3 us, the launch.
+// Slower: waves that go on to further rows, their loads ahead (44.0, 48.3, 34.8: they wait for
+// their stores as well); two or four rows loaded together (41.7, 44.8, 25.8 and 43.5, 48.1, 27.2).
+template <int DT, int PER, bool TAIL>
 __global__ __launch_bounds__(kPackThreads) void quant_short_kernel(QuantParams a)
 {
     typedef typename Elem<DT>::store_t T;
+    typedef typename Pack16<DT>::vec_t vec_t;
     constexpr int V = 8 / Elem<DT>::kPer16;
     const int lane = threadIdx.x & (kWave - 1);
-    const int64_t step = (int64_t)gridDim.x * (kPackThreads / kWave);
-    typename Pack16<DT>::vec_t next[PER][V];
-    auto load = [&](int64_t row) {
-        const T *x = static_cast<const T *>(a.X) + row * a.ldx;
+    const int64_t row = (int64_t)blockIdx.x * (kPackThreads / kWave) + threadIdx.x / kWave;
+    if (row >= a.rows)
+        return;
+    const T *src = static_cast<const T *>(a.X) + row * a.ldx;
+    vec_t x[PER][V];
+    uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
+    for (int i = 0; i < PER; ++i)
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int col = (i * kWave + lane) * 8 + v * Elem<DT>::kPer16;
-                next[i][v] = typename Pack16<DT>::vec_t{};
-                if (col < a.K)
-                    next[i][v] = load16<DT>(x, col, a.K);
-            }
-    };
-    int64_t row = (int64_t)blockIdx.x * (kPackThreads / kWave) + threadIdx.x / kWave;
-    if (row < a.rows)
-        load(row);
-    for (; row < a.rows; row += step) {
-        float f[PER][8];
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[i][k] = Elem<DT>::widen(next[i][k / Elem<DT>::kPer16][k % Elem<DT>::kPer16]);
-            m = max(m, raw_max_bits<DT>(next[i]));
+        for (int v = 0; v < V; ++v) {
+            const int col = (i * kWave + lane) * 8 + v * Elem<DT>::kPer16;
+            x[i][v] = vec_t{};
+            if (col < a.K)
+                x[i][v] = TAIL ? load16<DT>(src, col, a.K)
+                               : *reinterpret_cast<const vec_t *>(src + col);
         }
-        if (row + step < a.rows)
-            load(row + step);
-        m = wave_max(m);
-        const float inv = row_inverse(m);
-        if (lane == 0)
-            a.scales[row] = row_scale(m);
-        char *q = a.Q + row * a.Kq;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int col = (i * kWave + lane) * 8;
-            if (col < a.Kq)
-                put_codes(q, col, f[i], m, inv);
-        }
+    for (int i = 0; i < PER; ++i)
+        m = max(m, raw_max_bits<DT>(x[i]));
+    m = wave_max(m);
+    const float inv = row_inverse(m);
+    if (lane == 0)
+        a.scales[row] = row_scale(m);
+    char *q = a.Q + row * a.Kq;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int col = (i * kWave + lane) * 8;
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            f[k] = Elem<DT>::widen(x[i][k / Elem<DT>::kPer16][k % Elem<DT>::kPer16]);
+        if (col < a.Kq)
+            put_codes(q, col, f, m, inv);
     }
 }
 
@@ -395,19 +391,29 @@ unsigned pack_grid(int64_t items)
     return (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, 256 * 32));
 }
 
+template <int DT, int PER>
+void quant_short(const QuantParams &p, hipStream_t stream)
+{
+    constexpr int kRows = kPackThreads / kWave;
+    const dim3 grid((unsigned)((p.rows + kRows - 1) / kRows)), block(kPackThreads);
+    if (p.K % 8)
+        hipLaunchKernelGGL((quant_short_kernel<DT, PER, true>), grid, block, 0, stream, p);
+    else
+        hipLaunchKernelGGL((quant_short_kernel<DT, PER, false>), grid, block, 0, stream, p);
+}
+
 template <int DT>
 void quant_cfg(const QuantParams &p, hipStream_t stream)
 {
-    const dim3 waves(pack_grid((p.rows + 3) / 4) < 2048u ? pack_grid((p.rows + 3) / 4) : 2048u);
-    const dim3 block(kPackThreads);
     if (p.K <= kWave * 8)
-        hipLaunchKernelGGL((quant_short_kernel<DT, 1>), waves, block, 0, stream, p);
+        quant_short<DT, 1>(p, stream);
     else if (p.K <= kWave * 16)
-        hipLaunchKernelGGL((quant_short_kernel<DT, 2>), waves, block, 0, stream, p);
+        quant_short<DT, 2>(p, stream);
     else if (p.K <= kWave * 32)
-        hipLaunchKernelGGL((quant_short_kernel<DT, 4>), waves, block, 0, stream, p);
+        quant_short<DT, 4>(p, stream);
     else
-        hipLaunchKernelGGL(quant_long_kernel<DT>, dim3((unsigned)p.rows), block, 0, stream, p);
+        hipLaunchKernelGGL(quant_long_kernel<DT>, dim3((unsigned)p.rows), dim3(kPackThreads), 0,
+                           stream, p);
 }
 
 }  // namespace
