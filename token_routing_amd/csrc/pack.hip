@@ -140,8 +140,8 @@ __device__ __forceinline__ float row_scale(uint32_t m)
 }
 
 // Rows of up to PER * 512 columns: a wave for each.  TAIL: K is not a multiple of 8.
-// 65536 rows of bf16: of 768 42.7 us (3.5 TB/s read and written, where a row costs as much as
-// one of 1024), of 1024 42.7 (4.7), of 512 26.9 (3.8); a token of 1024 2.3 us, the launch.
+// 65536 rows of bf16: of 768 40 us (3.8 TB/s read and written, where a row costs as much as
+// one of 1024), of 1024 43 (4.7), of 512 26.8 (3.8); a token of 1024 2.3 us, the launch.
 // Slower: waves that go on to further rows, their loads ahead (44.0, 48.3, 34.8: they wait for
 // their stores as well); two or four rows loaded together (41.7, 44.8, 25.8 and 43.5, 48.1, 27.2).
 template <int DT, int PER, bool TAIL>
@@ -189,9 +189,11 @@ __global__ __launch_bounds__(kPackThreads) void quant_short_kernel(QuantParams a
 
 // Longer rows: a workgroup per row.  Its values stay in registers between the
 // maximum and the codes up to 8192 columns; the columns past that are read again.
-// 4096 rows of 4096 bf16 (50 MB, from cache in part): 15 to 18 us.
+// Eight waves a SIMD: left alone the compiler takes 114 registers for four (32768 rows of
+// 4096 bf16 130 us, so 89; 4096 rows 20.1 and 16.6; a wave a row 85 and 19.8, but one row
+// 4.2 for 2.5).
 template <int DT>
-__global__ __launch_bounds__(kPackThreads) void quant_long_kernel(QuantParams a)
+__global__ __launch_bounds__(kPackThreads, 8) void quant_long_kernel(QuantParams a)
 {
     typedef typename Elem<DT>::store_t T;
     constexpr int PER = 4, THREADS = kPackThreads;
