@@ -233,24 +233,10 @@ static hipError_t block_vec_act(const BlockFwdParams &p, int cus, hipStream_t st
     return hipGetLastError();
 }
 
-// Up to about two rows for each expert (four where there are fewer), unless tiles of 32
-// rows fill the card anyway: one of their rounds over the compute units is worth 1024
-// bytes of a row of W, shorter rows leaving a wave little between its tables, loads
-// and sums.  In a graph, from memory, int8 (tiles / vectors, us):
-//   1 token of 1024 into 2 of 8 experts of 2048, gated             11.2 /  5.0
-//   1 token of 2048 into 8 of 128 experts of 1536, gated           19.0 /  9.9
-//   4 tokens of 4096 into 2 of 8 experts of 4096, gated            30.2 / 18.0
-//   16 of the same (S = 4 E)                                       39.8 / 35.9
-//   16 of 2048 columns (S = 4 E)                                   22.1 / 23.9
-//   8 and 16 tokens of 2048 into 8 of 128 experts of 1536, gated   50.2 / 39.5, 57.9 / 66.4
-//   1 and 4 rows of 768 into 8 of 128 experts of 2048              11.2 /  7.2, 16.3 / 20.3
 bool block_vec_pays(const BlockFwdParams &p, int cus)
 {
-    if (p.S > std::max<int64_t>(2 * (int64_t)p.E, 4))
-        return false;
-    const int tile = p.flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU) ? 256 : 128;
-    const int64_t tiles = std::min<int64_t>(p.S, p.E) * ((p.N + tile - 1) / tile);
-    return tiles * 1024 <= (int64_t)p.K * 2 * cus;
+    const bool gated = p.flags & (MOEGG_GATED_SILU | MOEGG_GATED_GELU);
+    return vec_pays(p.S, p.E, p.N, gated, (int64_t)p.K * 2, cus);
 }
 
 hipError_t block_vec_launch(const BlockFwdParams &p, int cus, hipStream_t stream)
