@@ -63,10 +63,12 @@ CASES = [
     i8(MIDDLE, many(60, 100, 150, 7), 400, 1222, "gated", "gelu", True),
     i8(MIDDLE, many(60, 100, 150, 7), 272, 2440, "scattered", topk=2),
     bwd(MIDDLE, many(60, 100, 150, 7), 136, 2440, "packed", py=True),
-    bwd(MIDDLE, many(60, 100, 150, 7), 200, 2440, "bf16", act="gelu", halves=True),
-    bwd(MIDDLE, many(60, 100, 150, 7), 264, 2437, "place"),
-    bwd(MIDDLE, many(60, 100, 150, 7), 328, 2437, "packed", act="gelu", topk=2),
-    # four stages in the ring, with more tiles than the rule expects of such calls
+    bwd(MIDDLE, many(60, 100, 150, 7), 200, 2440, "packed", act="gelu", halves=True),
+    # four stages in the ring: the backward's other forms of these calls, and calls with
+    # more tiles than the rule expects of them
+    bwd(DEEP, many(60, 100, 150, 7), 328, 2440, "bf16", act="gelu", halves=True),
+    bwd(DEEP, many(60, 100, 150, 7), 392, 2437, "place"),
+    bwd(DEEP, many(60, 100, 150, 7), 328, 2437, "packed", act="gelu", topk=2),
     fwd(DEEP, [129, 129, 129], 456, 4096, "packed"),
     fwd(DEEP, [129, 129, 129], 584, 4093, "bf16", act="gelu", halves=True),
     i8(DEEP, [129, 129, 129], 912, 4096, "gated", "silu"),
@@ -131,6 +133,8 @@ def load_rules(folder):
         f.write('#include "block_shape.h"\n'
                 'extern "C" int shape(int64_t S, int E, int cols, int small, double most, int cus)\n'
                 '{ return moegg::tile_shape(S, E, cols, small, most, cus); }\n'
+                'extern "C" int bwd_shape(int64_t S, int E, int cols, int two, int cus)\n'
+                '{ return moegg::bwd_shape(S, E, cols, 128, 0.9, two, cus); }\n'
                 'extern "C" int vec(int64_t S, int E, int cols, int gated, int64_t row, int cus)\n'
                 '{ return moegg::vec_pays(S, E, cols, gated, row, cus); }\n')
     subprocess.check_call(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I",
@@ -138,6 +142,7 @@ def load_rules(folder):
     rules = ctypes.CDLL(lib)
     i64, i32 = ctypes.c_int64, ctypes.c_int
     rules.shape.argtypes = [i64, i32, i32, i32, ctypes.c_double, i32]
+    rules.bwd_shape.argtypes = [i64, i32, i32, i32, i32]
     rules.vec.argtypes = [i64, i32, i32, i32, i64, i32]
     return rules
 
@@ -148,8 +153,9 @@ def shape_taken(rules, c, cus):
     row = -(-c["depth"] // 8) * 16 if c["op"] != "i8" else c["depth"]
     if serving and rules.vec(S, E, cols, gated(c), row, cus):
         return VECTORS
-    small = 256 if gated(c) else 128
-    return rules.shape(S, E, cols, small, 0.9 if c["op"] == "bwd" else 0.75, cus)
+    if c["op"] == "bwd":
+        return rules.bwd_shape(S, E, cols, c["kept"] == "packed" and cols % 8 == 0, cus)
+    return rules.shape(S, E, cols, 256 if gated(c) else 128, 0.75, cus)
 
 
 # ---------------------------------------------------------------- references on the GPU

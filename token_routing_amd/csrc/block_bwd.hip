@@ -252,15 +252,16 @@ static void gated_bwd_cfg(const GatedBwdParams &p, int cus, hipStream_t stream)
 template <bool GELU, bool PACKED, bool TAIL>
 static void gated_bwd_rows(const GatedBwdParams &p, int cus, hipStream_t stream)
 {
-    const Shape shape = tile_shape(p.S, p.E, p.I, BwdSmallCfg::BN, 0.9, cus);
+    constexpr bool TWO = PACKED && !TAIL;
+    const Shape shape = bwd_shape(p.S, p.E, p.I, BwdSmallCfg::BN, 0.9, TWO, cus);
     if (shape == kSmallTiles)
-        gated_bwd_cfg<BwdSmallCfg, GELU, PACKED, TAIL>(p, cus, stream);
-    else if (shape == kMidTiles)
-        gated_bwd_cfg<BwdMidCfg, GELU, PACKED, TAIL>(p, cus, stream);
-    else if (shape == kDeepTiles)
-        gated_bwd_cfg<BwdDeepCfg, GELU, PACKED, TAIL>(p, cus, stream);
-    else
-        gated_bwd_cfg<BwdBigCfg, GELU, PACKED, TAIL>(p, cus, stream);
+        return gated_bwd_cfg<BwdSmallCfg, GELU, PACKED, TAIL>(p, cus, stream);
+    if (shape == kBigTiles)
+        return gated_bwd_cfg<BwdBigCfg, GELU, PACKED, TAIL>(p, cus, stream);
+    if constexpr (TWO)
+        if (shape == kMidTiles)
+            return gated_bwd_cfg<BwdMidCfg, GELU, PACKED, TAIL>(p, cus, stream);
+    gated_bwd_cfg<BwdDeepCfg, GELU, PACKED, TAIL>(p, cus, stream);
 }
 
 template <bool GELU, bool PACKED>

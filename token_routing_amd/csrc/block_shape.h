@@ -53,6 +53,21 @@ inline Shape tile_shape(int64_t S, int E, int cols, int small_cols, double most_
     return rounds(128, 128, cus) <= 1.0 ? kDeepTiles : kMidTiles;
 }
 
+// The backward's: as above, where its middle tiles leave registers for two workgroups a
+// compute unit (`two`: 256 of them, which packed values in whole columns alone keep to;
+// the other forms take 260 to 268).  Else four stages at the same one workgroup a unit,
+// which cover a stage's way from memory where nothing else does: with A kept, 8 experts of
+// 1024 rows, 4096 into 4096, 418 us (two stages 532), 60 of 256 rows, 2048 into 768, 113
+// (133), 128 of 64, 768 into 512, 41 (40), the worst of 200 shapes 46 (45).  Held to 256
+// registers, the two-stage form gains where there are many tiles and loses where there
+// are up to two a unit (8 experts of 256 rows, 1024 into 2048, A kept: 34.4 us for 26.8).
+inline Shape bwd_shape(int64_t S, int E, int cols, int small_cols, double most_small, bool two,
+                       int cus)
+{
+    const Shape shape = tile_shape(S, E, cols, small_cols, most_small, cus);
+    return shape == kMidTiles && !two ? kDeepTiles : shape;
+}
+
 // Up to about two rows for each expert (four where there are fewer), unless tiles of 32
 // rows fill the card anyway: one of their rounds over the compute units is worth 1024
 // bytes of a row of W, shorter rows leaving a wave little between its tables, loads
