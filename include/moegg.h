@@ -668,9 +668,10 @@ size_t moegg_lora_bwd_workspace_bytes(int64_t num_rows, int32_t num_adapters, in
  *   Q       out [rows, Kq], Kq = K rounded up to a multiple of 16, 16-byte
  *           aligned; columns from K on are zeros.
  *   scales  out [rows] fp32.
- * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  Errors:
- * ESHAPE for rows < 0 or past 2^24 - 1, K < 1 or past 2^30, ldx < K, sizes
- * past 2^40 bytes; EINVAL for an unknown dtype, NULL or misaligned pointers.
+ * rows = 0 is a no-op.  Outputs overlap neither X nor each other.  More rows than
+ * 2^24 - 1 take several calls.  Errors: ESHAPE for rows < 0 or past that, K < 1 or past
+ * 2^30, ldx < K, sizes past 2^40 bytes; EINVAL for an unknown dtype, NULL or misaligned
+ * pointers.
  */
 moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t rows, int32_t K,
                               int8_t *Q, float *scales, void *stream);

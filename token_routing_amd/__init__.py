@@ -857,6 +857,7 @@ def lora_bwd(X, dY, A, B, H, m_sizes, gather_idx=None, *, ranks=None, scales=Non
 
 
 PACK_BLOCK = 32
+QUANT_MAX_ROWS = (1 << 24) - 1      # of one moegg_quant_rows
 
 
 def quant_rows(X, *, Q=None, scales=None, stream=None):
@@ -865,7 +866,8 @@ def quant_rows(X, *, Q=None, scales=None, stream=None):
     X: [..., K] bf16, fp16 or fp32; a matrix may have any row stride, more
     dimensions (weights [E, N, K]) are contiguous.  Returns (Q int8 [..., Kq],
     scales fp32 [...]) with Kq = K rounded up to a multiple of 16, the columns
-    from K on zero: what grouped_gemm_i8 takes for tokens and for weights.
+    from K on zero: what grouped_gemm_i8 takes for tokens and for weights.  Rows
+    past QUANT_MAX_ROWS take a launch for each so many.
     """
     lib = load_library()
     dev = X.device
@@ -881,8 +883,20 @@ def quant_rows(X, *, Q=None, scales=None, stream=None):
     def call(stream_ptr):
         q, q_ptr = _out(Q, "Q", torch.int8, lead + ((K + 15) // 16 * 16,), dev)
         s, s_ptr = _out(scales, "scales", torch.float32, lead, dev)
-        _check(lib.moegg_quant_rows(x_ptr, code, ldx, rows, K, q_ptr, s_ptr, stream_ptr),
-               "moegg_quant_rows")
+        if rows <= QUANT_MAX_ROWS:
+            _check(lib.moegg_quant_rows(x_ptr, code, ldx, rows, K, q_ptr, s_ptr, stream_ptr),
+                   "moegg_quant_rows")
+            return q, s
+        size = X.element_size()
+        spans = sorted([(x_ptr, ((rows - 1) * ldx + K) * size), (q_ptr, q.numel()),
+                        (s_ptr, 4 * rows)])
+        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("Q and scales must overlap neither X nor each other")
+        for at in range(0, rows, QUANT_MAX_ROWS):
+            _check(lib.moegg_quant_rows(x_ptr + at * ldx * size, code, ldx,
+                                        min(QUANT_MAX_ROWS, rows - at), K,
+                                        q_ptr + at * q.shape[-1], s_ptr + 4 * at, stream_ptr),
+                   "moegg_quant_rows")
         return q, s
 
     return _run(dev, stream, call)
