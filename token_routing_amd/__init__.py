@@ -1028,6 +1028,8 @@ def gated_fwd(X, W, m_sizes, gather_idx, topk: int, flags: int, *, keep=None, H=
         raise ValueError(f"W must have an even number of rows per expert, not {N}")
     if keep not in (None, "bf16", "packed"):
         raise ValueError(f"keep must be None, 'bf16' or 'packed', not {keep!r}")
+    if kept is not None and (keep is None or isinstance(kept, torch.Tensor) != (keep == "bf16")):
+        raise ValueError(f"kept does not fit keep={keep!r}: a tensor for 'bf16', a pair for 'packed'")
     padded = (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
 
     def call(stream_ptr):
@@ -1073,6 +1075,8 @@ def gated_bwd(dY, W, kept, m_sizes, gather_idx, topk: int, flags: int, *, want_h
     T = dY.shape[0] // topk
     S = T * topk
     padded = (I + PACK_BLOCK - 1) // PACK_BLOCK * PACK_BLOCK
+    if kept is None:
+        raise ValueError("kept must be what gated_fwd kept: a tensor or a packed pair")
 
     def call(stream_ptr):
         a_ptr = q_ptr = s_ptr = None
