@@ -684,6 +684,7 @@ moegg_status moegg_quant_rows(const void *X, int32_t dtype, int64_t ldx, int64_t
  * permute flags and FUSE_MUL_POST as in the forward, Y bf16 rounded once.
  *   MOEGG_GATED_SILU or MOEGG_GATED_GELU: Y [S, N/2] = act(gate) * linear with
  *   act(g) = g / (1 + e^-g), or g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)));
+ *   either is 0 where it is above -1.1e-36 and e^-g (e^-2y of tanh y) past 2^126;
  *   W rows in (gate, linear) pairs, or with MOEGG_GATED_HALVES the N/2 gate
  *   rows first.  Not with PERMUTE_Y or FUSE_MUL_POST.
  *

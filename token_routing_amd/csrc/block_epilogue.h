@@ -5,7 +5,8 @@
 // columns leave in whole 32- or 64-byte pieces without shared memory.  Their stores
 // are at the memory's rate (8192 x 14336 bf16 of H and twice that of A in 110 us), but
 // a compute unit's MFMAs wait for them: with 256 accumulator columns a wave pair
-// fills the registers, so that no second tile runs beside.  Tried and slower:
+// fills the registers, so that no second tile runs beside, and the next tile's first
+// waits count the stores (ring_loop).  Tried and slower:
 // nontemporal stores (the backward 1.19 -> 1.58 ms: a row's line leaves in pieces),
 // groups of workgroups started apart (no gain beyond their delay).
 #pragma once
@@ -59,7 +60,8 @@ constexpr int kPlain = 0, kSilu = 1, kGelu = 2;
 // act(g) = g sigmoid(z(g)): z = g for silu, and 2 sqrt(2 / pi) (g + 0.044715 g^3) for
 // gelu's tanh form, since (1 + tanh y) / 2 = sigmoid(2 y).  sigmoid(z) = 1 / (1 +
 // 2^(-z log2 e)) by v_exp_f32 and v_rcp_f32, good to an ulp each, far below the
-// one rounding of the result to bf16.
+// one rounding of the result to bf16.  v_rcp_f32 gives 0 below fp32's normal numbers:
+// from z of about -87.3 down, where silu is above -1.1e-36, the activation is 0.
 template <bool GELU>
 struct GateAct {
     static constexpr float kLog2e = 1.4426950408889634f;
