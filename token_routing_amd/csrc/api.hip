@@ -1482,9 +1482,15 @@ static int64_t packed_rows_offset(int64_t S, int32_t E, int32_t N, int32_t K)
 // Whether they stand there in expert order (under PERMUTE_X; else in token order, and the
 // reduction gathers).  The order's copy writes topk - 1 times X's bytes more, and
 // the gather costs the reduction 1 to 5%: expert order pays above N of about 5000
-// (1 - 1 / topk).  8192 tokens of 2048, top-8: into 1536 598 us in token order, 677
-// in expert order; 4096 of 4096, top-2: into 28672 2148 and 2018.  The any-shape
-// reduction gathers at twice its time.
+// (1 - 1 / topk).  Token order / expert order, us:
+//   8192 tokens of 2048, top-8 of 128    into 1536 535 / 627, 3584 1308 / 1308, 5120 1839 / 1821
+//   4096 of 4096, top-2 of 8             into 1536 187 / 198, 2560 206 / 200, 8192 612 / 573
+//   4096 of 2048, top-4 of 16            into 2048 169 / 168, 3584 279 / 273, 8192 633 / 599
+//   4096 of 4096, top-6 of 64            into 4096 1112 / 1207, 5120 1505 / 1479, 8192 2395 / 2451
+//   4096 of 768, top-8 of 128            into 4096 367 / 392, 5120 475 / 493, 8192 750 / 749
+// Of 64 points (these and three more settings, N of 1536 to 8192) it takes the slower side at
+// 14, at 12 of them by less than 2.5%, by 6% at most.  The any-shape reduction gathers at
+// twice its time.
 static bool packed_in_order(int64_t T, int32_t topk, int32_t N, int32_t K)
 {
     return fits(T * topk, K) &&

@@ -6,8 +6,10 @@
 // bytes each way.  W's rows are the reduction: its tiles go to LDS as they are and are
 // read transposed (ds_read_b64_tr_b16).  65536 rows of 2048 into 768 with 8-bit kept
 // values: 367 us (0.56 PFLOP/s, 2.9 TB/s), where the product bounds it at 133 us and
-// its bytes at 214; 8192 rows of 4096 into 14336 1.2 ms (0.80 PFLOP/s).  Main loop and
-// epilogue (kept values in, dA and H out) follow each other on a compute unit.
+// its bytes at 214; from bf16 406 us (233 of bytes).  8192 rows of 4096 into 14336 1.2 ms
+// (0.80 PFLOP/s), from bf16 1.26.  3003 odd rows, 1003 into 517: 34 us, from bf16 37, of
+// which copying the operands in front takes 11.  Main loop and epilogue (kept values in, dA
+// and H out) follow each other on a compute unit.
 #include "block_epilogue.h"
 
 namespace moegg {
@@ -181,8 +183,10 @@ __global__ __launch_bounds__(C::NT) void gated_bwd_kernel(GatedBwdParams a)
 
         const int I = a.I;
         const int64_t Ip = packed_cols(I);
-        // What was kept of block (i, j)'s columns, read a block ahead: the loads then
-        // stand before the stores of the block in front of them.
+        // What was kept of block (i, j)'s columns, its loads issued before the stores of the
+        // block in front of them.  Loads and stores stand under conditions of the lane, which
+        // the compiler cannot count: it waits for everything in flight, from packed values at
+        // every second block, from bf16 at each load.
         Kept<PACKED, TAIL> kept[2];
         auto load = [&](auto b) {
             constexpr int i = decltype(b)::value / C::FN, j = decltype(b)::value % C::FN;

@@ -12,8 +12,11 @@
 // (0.99) or of the whole stage (1.05), reads spread over the MFMAs (0.99), lines
 // touched two stages ahead (1.04).
 //
-// The epilogues leave LDS alone, so that a persistent kernel starts the next
-// tile's first stages (ring_start) before this tile's epilogue.
+// The epilogues leave LDS alone, so that a persistent kernel starts the copies of the
+// next tile's first stages (ring_start) before this tile's epilogue.  Its MFMAs do not
+// start so early: the epilogue's stores are issued behind those copies and count with them,
+// so that the first stage waits until a stage's copies' worth of operations is left, and the
+// second, in a ring of two, until every store is done.
 #pragma once
 
 #include "gemm_engine.h"

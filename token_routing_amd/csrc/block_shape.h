@@ -35,7 +35,7 @@ enum Shape { kSmallTiles, kMidTiles, kDeepTiles, kBigTiles };
 //           rows 318 us (middle 362, small 690), of 128 rows 85 (66, 140).
 // 256 x 128 and 128 x 256 tiles with 32-deep stages, two workgroups a unit, lose to
 // both (8192 rows of 4096 int8 into 28672 1.19 ms, large 0.98; 65536 of 768 into
-// 2048 248 us, large 236).  Swept over 1, 8 and 60 experts of 16 to 1024 rows and 512
+// 2048, each with 38 for their quantisation, 248 us, large 236).  Swept over 1, 8 and 60 experts of 16 to 1024 rows and 512
 // to 8192 columns.
 inline Shape tile_shape(int64_t S, int E, int cols, int small_cols, double most_small, int cus)
 {
@@ -71,14 +71,23 @@ inline Shape bwd_shape(int64_t S, int E, int cols, int small_cols, double most_s
 // Up to about two rows for each expert (four where there are fewer), unless tiles of 32
 // rows fill the card anyway: one of their rounds over the compute units is worth 1024
 // bytes of a row of W, shorter rows leaving a wave little between its tables, loads
-// and sums.  In a graph, from memory, int8 (tiles / vectors, us):
-//   1 token of 1024 into 2 of 8 experts of 2048, gated             11.2 /  5.0
-//   1 token of 2048 into 8 of 128 experts of 1536, gated           19.0 /  9.9
-//   4 tokens of 4096 into 2 of 8 experts of 4096, gated            30.2 / 18.0
-//   16 of the same (S = 4 E)                                       39.8 / 35.9
-//   16 of 2048 columns (S = 4 E)                                   22.1 / 23.9
-//   8 and 16 tokens of 2048 into 8 of 128 experts of 1536, gated   50.2 / 39.5, 57.9 / 66.4
-//   1 and 4 rows of 768 into 8 of 128 experts of 2048              11.2 /  7.2, 16.3 / 20.3
+// and sums.  In a graph, other experts' weights from memory each time (tiles / vectors, us;
+// int8 and gated unless said):
+//   1 token of 1024 into 2 of 8 experts of 2048                    11.8 /  5.6
+//   1 token of 2048 into 8 of 128 experts of 1536                  19.2 /  9.3
+//   1 token of 4096 into 2 of 8 experts of 14336, 28672, 57344     36.3 / 26.8, 55.5 / 48.3, 110 / 89
+//   1 token of 1024 into 2 of 8 experts of 32768                   20.6 / 20.1
+//   4 tokens of 4096 into 2 of 8 experts of 4096, 14336            33.8 / 22.9, 88.8 / 64.6
+//   8 tokens of 4096 into 2 of 8 experts of 4096, bf16             60.4 / 48.0
+//   8 and 16 tokens of 2048 into 8 of 128 experts of 1536          47.7 / 40.2, 54.6 / 60.9
+//   1 and 4 rows of 768 into 8 of 128 experts of 2048, plain       11.2 /  7.2, 16.3 / 20.3
+// Where it is the wrong side: at two rows an expert of 2048 bytes (256 rows over 128 experts
+// of 512 columns 28.3 / 33.4, of 1024 52.4 / 59.9); plain calls, whose tiles it counts by 128
+// columns (30 tokens of 4096 into 4 of 60 experts of 2816: 152 / 118, and it takes tiles);
+// and where routing, which the device alone knows, sends many rows to one expert, whose W
+// is then read once for every four of them (256 of 2048 into 1024, all to one of 128 experts:
+// 17.1 / 29.8; 128 of 8192 into 4096, all to one of 64: 48 / 95).  Fewer rows in all would bound
+// that and lose more where they spread (those 128 over all experts: 393 / 319).
 inline bool vec_pays(int64_t S, int E, int cols, bool gated, int64_t row_bytes, int cus)
 {
     if (S > std::max<int64_t>(2 * (int64_t)E, 4))
