@@ -273,19 +273,27 @@ def time_step(st, steps, warmup, min_warm_s=0.0):
     return per / steps, total / steps, wall
 
 
+# The sources that a kernel is built from, beside common.h and gemm_params.h: of the
+# GEMMs, routing and combine when no label is given; "block" is the 8-bit products, the
+# gated block and packed activations.
+KERNEL_SOURCES = {
+    None: ("gemm.hip", "gemm_engine.h", "route.hip", "combine.hip"),
+    "combine": ("combine.hip",),
+    "route": ("route.hip",),
+    "block": ("block_bwd.hip", "block_engine.h", "block_epilogue.h", "block_fwd.h",
+              "block_gelu.hip", "block_i8.hip", "block_params.h", "block_shape.h",
+              "block_silu.hip", "block_vec.hip", "elems.h", "gemm_engine.h", "pack.h", "pack.hip"),
+    "gemm": ("gemm.hip", "gemm_engine.h"),
+}
+
+
 def kernel_source_sha(label=None):
-    """sha256[:16] of the sources a kernel is built from (all kernels' when
-    label is None): the shared headers plus the kernel's own files."""
-    if label is None:
-        own = ("gemm.hip", "gemm_engine.h", "route.hip", "combine.hip")
-    elif label.startswith("combine"):
-        own = ("combine.hip",)
-    elif label.startswith("route"):
-        own = ("route.hip",)
-    else:
-        own = ("gemm.hip", "gemm_engine.h")
+    """sha256[:16] of the sources of a kernel (KERNEL_SOURCES)."""
+    kind = label
+    if label is not None:
+        kind = next((k for k in ("combine", "route", "block") if label.startswith(k)), "gemm")
     h = hashlib.sha256()
-    for f in own + ("common.h", "gemm_params.h"):
+    for f in KERNEL_SOURCES[kind] + ("common.h", "gemm_params.h"):
         with open(os.path.join(ROOT, "token_routing_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()[:16]
