@@ -96,7 +96,7 @@ __global__ __launch_bounds__(C::NT) void gated_bwd_kernel(GatedBwdParams a)
     const bool halves = a.flags & MOEGG_GATED_HALVES;
     const int nti = (a.I + C::BN - 1) / C::BN;
     const int total = build_expert_tables(a.m_sizes, a.E, a.S, s_roff, s_tstart, s_scratch, a.err,
-                                          [&](int m) { return (m + C::BM - 1) / C::BM * nti; });
+                                          [&](int m) { return tiles_of<C::BM>(m) * nti; });
     const int N = a.N, nsteps = (N + C::DEPTH - 1) / C::DEPTH;
     const u32x4_t dyr = rsrc_words(a.dY, a.S * a.ldy);
     const int wave = threadIdx.x / kWave;
@@ -113,7 +113,7 @@ __global__ __launch_bounds__(C::NT) void gated_bwd_kernel(GatedBwdParams a)
         const int mc = __builtin_amdgcn_readfirstlane(s_roff[x.e + 1] - s_roff[x.e]);
         const int u = t - __builtin_amdgcn_readfirstlane(s_tstart[x.e]);
         int mt, it;
-        band_raster<kBandMdX>(u, (mc + C::BM - 1) / C::BM, nti, mt, it);
+        band_raster<kBandMdX>(u, tiles_of<C::BM>(mc), nti, mt, it);
         x.p0 = __builtin_amdgcn_readfirstlane(s_roff[x.e]) + mt * C::BM;
         x.rows = min(C::BM, mc - mt * C::BM);
         x.i0 = it * C::BN;

@@ -60,7 +60,7 @@ __global__ __launch_bounds__(C::NT) void block_fwd_kernel(BlockFwdParams a)
     const bool halves = a.flags & MOEGG_GATED_HALVES;
     const int ntn = (a.N + C::BN - 1) / C::BN;
     const int total = build_expert_tables(a.m_sizes, a.E, a.S, s_roff, s_tstart, s_scratch, a.err,
-                                          [&](int m) { return (m + C::BM - 1) / C::BM * ntn; });
+                                          [&](int m) { return tiles_of<C::BM>(m) * ntn; });
     const int K = a.K, nsteps = (K + C::DEPTH - 1) / C::DEPTH;
     const int64_t x_rows = px ? a.S / a.topk : a.S;
     const u32x4_t xr = rsrc_words(a.X, x_rows * a.ldx);
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(C::NT) void block_fwd_kernel(BlockFwdParams a)
         const int mc = __builtin_amdgcn_readfirstlane(s_roff[x.e + 1] - s_roff[x.e]);
         const int u = t - __builtin_amdgcn_readfirstlane(s_tstart[x.e]);
         int mt, nt;
-        band_raster<kBandM>(u, (mc + C::BM - 1) / C::BM, ntn, mt, nt);
+        band_raster<kBandM>(u, tiles_of<C::BM>(mc), ntn, mt, nt);
         x.p0 = __builtin_amdgcn_readfirstlane(s_roff[x.e]) + mt * C::BM;
         x.rows = min(C::BM, mc - mt * C::BM);
         x.n0 = nt * C::BN;
