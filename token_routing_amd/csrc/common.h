@@ -80,6 +80,45 @@ __device__ inline void wave0_exclusive_scan(int *vals, int n, int *total)
     __syncthreads();
 }
 
+// The same of row counts of at most cap each, every sum held at cap: counts whose sum passes
+// 32 bits do not wrap around to rows before the first.  Whether the sum passes cap is
+// returned in the first wave.
+__device__ inline bool wave0_exclusive_scan_to(int *vals, int n, int cap, int *total)
+{
+    bool over = false;
+    auto add = [&](uint32_t a, uint32_t b) {
+        over |= a + b > (uint32_t)cap;
+        return min(a + b, (uint32_t)cap);
+    };
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        const int lane = threadIdx.x;
+        const int per = (n + kWave - 1) / kWave;
+        const int lo = lane * per;
+        const int hi = min(n, lo + per);
+        uint32_t incl = 0;
+        for (int i = lo; i < hi; ++i)
+            incl = add(incl, vals[i]);
+        for (int d = 1; d < kWave; d <<= 1) {
+            const uint32_t v = __shfl_up(incl, d, kWave);
+            if (lane >= d)
+                incl = add(incl, v);
+        }
+        uint32_t run = __shfl_up(incl, 1, kWave);
+        if (lane == 0)
+            run = 0;
+        for (int i = lo; i < hi; ++i) {
+            const int v = vals[i];
+            vals[i] = (int)run;
+            run = add(run, v);
+        }
+        if (lane == kWave - 1)
+            *total = (int)incl;
+    }
+    __syncthreads();
+    return over;
+}
+
 // Largest e in [0, n) with starts[e] <= t (starts non-decreasing, starts[0] = 0).
 __device__ __forceinline__ int upper_index(const int *starts, int n, int t)
 {
@@ -94,7 +133,7 @@ __device__ __forceinline__ int upper_index(const int *starts, int n, int t)
     return lo;
 }
 
-// s_roff[0..E]: expert row starts clipped to [0, S] (s_roff[E] = end);
+// s_roff[0..E]: expert row starts clipped to [0, S], S < 2^31 (s_roff[E] = end);
 // s_tstart[0..E]: first tile of each expert for tiles_of(rows).  Flags
 // negative m_sizes and sums past S.
 template <class TilesOf>
@@ -102,23 +141,16 @@ __device__ __forceinline__ int build_expert_tables(const int32_t *m_sizes, int E
                                                    int *s_roff, int *s_tstart, int *s_scratch,
                                                    int32_t *err, TilesOf tiles_of)
 {
+    const int cap = (int)S;
     bool bad = false;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
         const int m = m_sizes[e];
-        bad |= m < 0;
-        s_roff[e] = m < 0 ? 0 : m;
+        bad |= m < 0 || m > cap;
+        s_roff[e] = min(max(m, 0), cap);
     }
-    wave0_exclusive_scan(s_roff, E, &s_scratch[0]);
-    const int total = s_scratch[0];
-    if (threadIdx.x == 0) {
-        bad |= total > S || total < 0;
-        s_roff[E] = (int)min((int64_t)total, S);
-    }
-    for (int e = threadIdx.x; e < E; e += blockDim.x)
-        s_roff[e] = (int)min((int64_t)s_roff[e], S);
+    bad |= wave0_exclusive_scan_to(s_roff, E, cap, &s_roff[E]);
     if (bad)
         raise_error(err, kErrMSizes);
-    __syncthreads();
     for (int e = threadIdx.x; e < E; e += blockDim.x)
         s_tstart[e] = tiles_of(s_roff[e + 1] - s_roff[e]);
     wave0_exclusive_scan(s_tstart, E, &s_scratch[1]);
