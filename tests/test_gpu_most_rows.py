@@ -51,3 +51,29 @@ def test_one_expert_of_all_slots(mg, gated):
             parts.append((v.float() * 2.0 ** -12).bfloat16())
     want = torch.cat(parts)
     assert torch.equal(y.view(T, K_TOP), want.expand(T, K_TOP))
+
+
+@pytest.mark.parametrize("K,N", [(8, 8), (3, 1)], ids=["tiles", "any shape"])
+@pytest.mark.parametrize("first", [0, 30])
+def test_forward_of_all_slots(mg, K, N, first):
+    """The bf16 forward: small whole numbers, whose sums of at most 128 bf16 holds."""
+    S = T * K_TOP
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-4, 5, (T, K), generator=g, dtype=torch.int8, device="cuda").bfloat16()
+    w = torch.randint(-4, 5, (2, N, K), generator=g, device="cuda").bfloat16()
+    gather = torch.arange(S, dtype=torch.int32, device="cuda")
+    m = torch.tensor([first, S - first], dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = torch.full((S, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    mg.grouped_gemm_fwd(x, w, m, gather, None, K_TOP, mg.PERMUTE_X, Y=y, error_flags=err)
+    assert int(err) == 0
+    del gather
+    y = y.view(T, K_TOP, N)
+    for a in range(0, T, 1 << 24):
+        v = x[a:a + (1 << 24)].float()
+        want = (v @ w[1].float().t()).bfloat16()[:, None, :].expand(-1, K_TOP, -1)
+        if a == 0 and first:
+            want = want.contiguous()
+            want.view(-1, N)[:first] = (v[:2] @ w[0].float().t()).bfloat16().repeat_interleave(
+                K_TOP, 0)[:first]
+        assert torch.equal(y[a:a + (1 << 24)], want)

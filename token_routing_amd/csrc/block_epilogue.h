@@ -144,14 +144,6 @@ __device__ __forceinline__ u16x8_any_t load8(const char *row, int c, int n)
     return v;
 }
 
-// Tiles of BLOCK rows that hold m >= 0 rows.  Rounded up without a sign: an expert may have
-// up to 2^31 - 1 rows.
-template <int BLOCK>
-__device__ __forceinline__ int tiles_of(int m)
-{
-    return (int)(((uint32_t)m + (BLOCK - 1)) / BLOCK);
-}
-
 // f(i) for the constants i = 0 .. N - 1: an epilogue's block indices have to be
 // constants whatever its size (accumulators indexed by a variable live in memory).
 template <class F, int... I>

@@ -133,6 +133,14 @@ __device__ __forceinline__ int upper_index(const int *starts, int n, int t)
     return lo;
 }
 
+// Tiles of BLOCK rows that hold m >= 0 rows.  Rounded up without a sign: an expert may have
+// up to 2^31 - 1 rows.
+template <int BLOCK>
+__device__ __forceinline__ int tiles_of(int m)
+{
+    return (int)(((uint32_t)m + (BLOCK - 1)) / BLOCK);
+}
+
 // s_roff[0..E]: expert row starts clipped to [0, S], S < 2^31 (s_roff[E] = end);
 // s_tstart[0..E]: first tile of each expert for tiles_of(rows).  Flags
 // negative m_sizes and sums past S.

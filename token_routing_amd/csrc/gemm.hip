@@ -37,7 +37,7 @@ __global__ __launch_bounds__(C::NT) void fwd_kernel(FwdParams a)
     const bool fm = a.flags & MOEGG_FUSE_MUL_POST;
     const int ntn = (a.N + C::BN - 1) / C::BN;
     const int total = build_expert_tables(a.m_sizes, a.E, a.S, s_roff, s_tstart, s_scratch, a.err,
-                                          [&](int m) { return (m + C::BM - 1) / C::BM * ntn; });
+                                          [&](int m) { return tiles_of<C::BM>(m) * ntn; });
     const int nsteps = (a.K + BK - 1) / BK;
     const int64_t row_bytes = (int64_t)a.K * 2;
     const int64_t x_rows = px ? a.S / a.topk : a.S;
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(C::NT) void fwd_kernel(FwdParams a)
     auto tile = [&](int t, int &e, int &p0, int &rows, int &n0) {
         e = __builtin_amdgcn_readfirstlane(upper_index(s_tstart, a.E, t));
         const int mc = __builtin_amdgcn_readfirstlane(s_roff[e + 1] - s_roff[e]);
-        const int mtiles = (mc + C::BM - 1) / C::BM;
+        const int mtiles = tiles_of<C::BM>(mc);
         const int u = t - __builtin_amdgcn_readfirstlane(s_tstart[e]);
         int mt, nt;
         band_raster<kBandM>(u, mtiles, ntn, mt, nt);

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kAnyThreads) void fwd_any_kernel(FwdParams a)
     __shared__ int s_scratch[2];
     const int ct = (a.N + 31) / 32;
     const int total = build_expert_tables(a.m_sizes, a.E, a.S, s_roff, s_tstart, s_scratch, a.err,
-                                          [&](int rows) { return (rows + 31) / 32 * ct; });
+                                          [&](int rows) { return tiles_of<32>(rows) * ct; });
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     const int col = lane & 31, half = lane >> 5;
     const bool px = a.flags & MOEGG_PERMUTE_X, py = a.flags & MOEGG_PERMUTE_Y;
@@ -93,16 +93,18 @@ __global__ __launch_bounds__(kAnyThreads) void fwd_any_kernel(FwdParams a)
         const int e = upper_index(s_tstart, a.E, t);
         const int u = t - s_tstart[e];
         const int i0 = (u / ct) * 32, n0 = (u % ct) * 32;
-        const int pb = s_roff[e], pe = s_roff[e + 1];
+        // The block's first position and its expert's rows from there on (no position past
+        // the last one is formed: it may not fit 32 bits).
+        const int pb = s_roff[e] + i0, left = s_roff[e + 1] - pb;
         const __amdgpu_buffer_rsrc_t wr = any_rsrc(a.W + e * wbytes, wbytes);
         // A: this lane's row, position pb + i0 + col; B: W row n0 + col.
-        const int p = pb + i0 + col;
+        const int p = pb + min(col, left - 1);
         int g = p;
         if (px || py)
-            g = a.gather[min(p, pe - 1)];
+            g = a.gather[p];
         const bool gok = !(px || py) || (uint32_t)g < (uint32_t)a.S;
-        const bool aok = p < pe && gok;
-        bad |= p < pe && !gok;
+        const bool aok = col < left && gok;
+        bad |= col < left && !gok;
         const uint32_t arow = aok ? (uint32_t)((px ? g / a.topk : p) * (int64_t)a.K * 2) : 0;
         const bool bok = n0 + col < a.N;
         const uint32_t brow = bok ? (uint32_t)((n0 + col) * (int64_t)a.K * 2) : 0;
@@ -122,13 +124,14 @@ __global__ __launch_bounds__(kAnyThreads) void fwd_any_kernel(FwdParams a)
         const int n = n0 + col;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int q = pb + i0 + out_row(r);
+            const int row = out_row(r);
             float v = acc[r];
             float partner = 0.0f;
             if constexpr (GATED)
                 partner = __shfl_xor(v, 1, kWave);  // column n ^ 1 of the same row
-            if (q >= pe)
+            if (row >= left)
                 continue;
+            const int q = pb + row;
             int gq = q;
             if (px || py) {
                 gq = a.gather[q];
