@@ -170,3 +170,35 @@ def test_far_block(mg):
         rounds.check(da[at], rounds.join(dg, du, True), rounds.join(tg, tu, True), "dA")
         rounds.check(h2[at], hh, th, "H again")
         del h, h2, da, kept
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 1040, 50), (90, 80, 136), (300, 64, 520), (1500, 48, 4000)])
+def test_outputs_beside_16_bytes(mg, T, K, N):
+    """Y, dA and H that begin 2 bytes off a 16-byte border, and nothing written beside them."""
+    r, order, experts, g = routed(mg, T, 2, 3, T)
+    S, n = 2 * T, order.size
+
+    def off(rows, cols):
+        flat = torch.full((rows * cols + 9,), 9.0, dtype=torch.bfloat16, device="cuda")
+        return flat, flat[1:rows * cols + 1].view(rows, cols)
+
+    xq, xs = mg.quant_rows(torch.randn(T, K, generator=g).cuda())
+    wq, ws = mg.quant_rows(torch.randn(3, N, K, generator=g).cuda())
+    for f, cols in ((0, N), (mg.GATED_SILU, N // 2)):
+        flat, y = off(S, cols)
+        args = (xq, xs, wq, ws, r["m_sizes"], r["gather"], None, 2, mg.PERMUTE_X | f)
+        mg.grouped_gemm_i8(*args, Y=y)
+        assert torch.equal(y[:n], mg.grouped_gemm_i8(*args)[:n]) and (y[n:] == 9).all()
+        assert (flat[:1] == 9).all() and (flat[-8:] == 9).all()
+    I = N // 2
+    kept, _, _ = kept_values(g, S, I, False, True)
+    dy = torch.randn(S, K, generator=g).bfloat16().cuda()
+    wd = torch.randn(3, K, I, generator=g).bfloat16().cuda()
+    args = (dy, wd, to_cuda(kept), r["m_sizes"], r["gather"], 2)
+    for f in (mg.GATED_SILU, mg.GATED_GELU | mg.GATED_HALVES):
+        (fa, da), (fh, h) = off(S, 2 * I), off(S, I)
+        mg.gated_bwd(*args, f, dA=da, H=h)
+        da2, h2 = mg.gated_bwd(*args, f)
+        assert torch.equal(da[:n], da2[:n]) and torch.equal(h[:n], h2[:n])
+        for flat, t in ((fa, da), (fh, h)):
+            assert (t[n:] == 9).all() and (flat[:1] == 9).all() and (flat[-8:] == 9).all()
