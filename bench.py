@@ -673,7 +673,7 @@ def summarize(prof_dir, workload, command):
     os.makedirs(os.path.join(ROOT, "profiles"), exist_ok=True)
     lines = [f"# rocprofv3 kernel statistics: {workload}", "",
              f"Workload: {WORKLOAD_DESC[workload]}", "",
-             "Commands (from the repository root on the GPU box):", "",
+             "Commands (on an MI355X):", "",
              "```", *command.strip().splitlines(), "```", "",
              f"Kernel sources sha256[:16]: `{sha}`", "",
              "| kernel | calls | average ns | total % |", "|---|---|---|---|"]
