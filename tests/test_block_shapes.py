@@ -1,10 +1,10 @@
-"""Which kernel the calls of tests/_rounds.py take on a card of 256 compute units, by the
+"""Which kernel the calls of tests/_tiles.py take on a card of 256 compute units, by the
 library's own rules: each case runs the kernel that it is there for, with more tiles than
 the launch has workgroups, and with reductions that go round the ring of stages."""
 
 import pytest
 
-from tests import _rounds as r
+from tests import _tiles as r
 
 CUS = 256
 

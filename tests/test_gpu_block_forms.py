@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests import _rounds as rounds
+from tests import _tiles as tiles
 from tests._block import HALF, U, check, f64, gated_ref, grouped, routed, split, sum_err
 from tests._block import pack_ref, unpack_ref
 from tests.test_gpu_gated import CASES, IDS, bwd_ref, flags_of, inputs, join, kept_values, to_cuda
@@ -136,7 +136,7 @@ def test_far_integers(mg, form):
     at = far_rows(S, N)
     p = S - 1 - at if form == "scattered" else at
     ref = (xq[p].double() @ wq[0].double().t()) * xs[p].double()[:, None] * ws.double()
-    rounds.check(y[at], ref, ref.abs() * (HALF + 6 * U))
+    tiles.check(y[at], ref, ref.abs() * (HALF + 6 * U))
 
 
 def test_far_block(mg):
@@ -151,24 +151,24 @@ def test_far_block(mg):
     at = far_rows(S, 2 * I)
     v, mag = x[at].double() @ w[0].double().t(), x[at].double().abs() @ w[0].double().abs().t()
     e = sum_err(mag, K)
-    (gt, ut), (ge, ue) = rounds.split(v, True), rounds.split(e, True)
+    (gt, ut), (ge, ue) = tiles.split(v, True), tiles.split(e, True)
     dh, dmag = (x[at].double() @ wd[0].double(), x[at].double().abs() @ wd[0].double().abs())
     for keep in ("bf16", "packed"):
         h, kept = mg.gated_fwd(x, w, m, None, 1, f, keep=keep)
-        rounds.check(h[at], *rounds.gated_ref(gt, ut, ge, ue, "silu"), "H")
+        tiles.check(h[at], *tiles.gated_ref(gt, ut, ge, ue, "silu"), "H")
         if keep == "bf16":
-            rounds.check(kept[at], v, e + (v.abs() + e) * HALF, "A")
-            kg, ku = rounds.split(kept[at].double(), True)
+            tiles.check(kept[at], v, e + (v.abs() + e) * HALF, "A")
+            kg, ku = tiles.split(kept[at].double(), True)
         else:
             parts = [[t[at].chunk(2, 1)[i] for t in kept] for i in range(2)]
-            (kg, gs), (ku, us) = (rounds.unpack_ref(q, s, I) for q, s in parts)
-            rounds.check(kg, gt, gs / 2 + ge, "gate codes")
-            rounds.check(ku, ut, us / 2 + ue, "linear codes")
+            (kg, gs), (ku, us) = (tiles.unpack_ref(q, s, I) for q, s in parts)
+            tiles.check(kg, gt, gs / 2 + ge, "gate codes")
+            tiles.check(ku, ut, us / 2 + ue, "linear codes")
         da, h2 = mg.gated_bwd(x, wd, kept, m, None, 1, f, H=h)
         assert h2 is h
-        (dg, tg), (du, tu), (hh, th) = rounds.bwd_ref(kg, ku, dh, sum_err(dmag, K), "silu")
-        rounds.check(da[at], rounds.join(dg, du, True), rounds.join(tg, tu, True), "dA")
-        rounds.check(h2[at], hh, th, "H again")
+        (dg, tg), (du, tu), (hh, th) = tiles.bwd_ref(kg, ku, dh, sum_err(dmag, K), "silu")
+        tiles.check(da[at], tiles.join(dg, du, True), tiles.join(tg, tu, True), "dA")
+        tiles.check(h2[at], hh, th, "H again")
         del h, h2, da, kept
 
 

@@ -8,9 +8,9 @@ takes is asserted in tests/test_block_shapes.py."""
 import pytest
 import torch
 
-from tests import _rounds as r
+from tests import _tiles as r
 from tests._block import HALF, U
-from tests._rounds import check, gated_ref, grouped, join, split, sum_err, unpack_ref
+from tests._tiles import check, gated_ref, grouped, join, split, sum_err, unpack_ref
 
 pytestmark = pytest.mark.gpu
 
